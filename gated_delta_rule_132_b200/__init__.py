@@ -3,7 +3,9 @@ with a thin Python binding.
 
 The compute entry points (``kda_chunk_fwd``, ``kda_decode_step``,
 ``kda_decode_tokens``) live in
-``gated_delta_rule_132_b200.kda`` and load the in-tree ``libkda_b200.so`` on
+``gated_delta_rule_132_b200.kda``, those of the full-attention layer
+(``kda_attn_fwd``, ``kda_attn_bwd``, ``kda_attn_tree`` and the page calls
+``kda_cache_*``) in ``gated_delta_rule_132_b200.attn``; both load the in-tree ``libkda_b200.so`` on
 first use; ``inputs`` holds the seeded synthetic-input generators.
 """
 import importlib
@@ -14,9 +16,14 @@ _EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_prepare", "kda_chunk_fwd_carry",
             "kda_decode_step", "kda_decode_tokens", "kda_gdn_chunk_fwd", "kda_chunk_bwd",
             "kda_chunk_fwd_workspace_size",
             "ChunkFwdCall", "lib", "KdaError")
+_ATTN_EXPORTS = ("kda_attn_fwd", "kda_attn_bwd", "kda_attn_tree", "kda_attn_status",
+                 "kda_cache_fork", "kda_cache_reserve", "kda_cache_release", "kda_cache_append",
+                 "kda_cache_compact", "kda_cache_copy_pages")
 
 
 def __getattr__(name):
     if name in _EXPORTS:
         return getattr(importlib.import_module(".kda", __name__), name)
+    if name in _ATTN_EXPORTS:
+        return getattr(importlib.import_module(".attn", __name__), name)
     raise AttributeError(name)

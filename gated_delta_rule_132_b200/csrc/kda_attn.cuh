@@ -1,0 +1,105 @@
+// kda_attn.cuh — declarations shared by the full-attention translation units.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// A prompt-attention call after host-side validation.
+struct AttnProblem {
+    const void *q, *k, *v;
+    const int32_t *cu_seqlens;  // device, or null (uniform sequences of length T)
+    int N, B, T, Hq, Hkv, d;
+    float scale;
+    kda_dtype_t dtype;
+    long long tokens;           // B * T
+};
+
+// One tile of consecutive tokens of one sequence: the unit of work of the prompt
+// kernels, listed longest sequence first and, within a sequence, the last tile
+// (the one that sees most keys) first, so that the last CTAs to start are short.
+struct __align__(16) AttnTile {
+    int first;      // packed token of the tile's first row
+    int seq_start;  // packed token range of its sequence
+    int seq_end;
+    int unused;
+};
+
+// Most tiles of `rows` tokens that the sequences can have.
+inline long long attn_tiles(const AttnProblem &p, int rows)
+{
+    return p.cu_seqlens ? p.tokens / rows + p.N
+                        : (long long)p.B * ((p.T + rows - 1) / rows);
+}
+
+// Workspace of a prompt call: the header (status word), the plan (varlen calls:
+// sanitised starts, longest-first order, tile offsets; the tile list) and, for the
+// backward, D_r = <dO_r, o_r>.
+struct AttnWorkspace {
+    size_t starts, order, tiles, delta, total;
+};
+
+inline AttnWorkspace attn_workspace_layout(const AttnProblem &p, int rows, bool bwd)
+{
+    AttnWorkspace w;
+    size_t at = kWsHeader;
+    w.starts = at; at += sizeof(int32_t) * ((size_t)p.N + 1);
+    w.order = at; at += sizeof(int32_t) * 2 * ((size_t)p.N + 1);
+    at = align_up(at, 16);
+    w.tiles = at; at += sizeof(AttnTile) * (size_t)attn_tiles(p, rows);
+    at = align_up(at, 256);
+    w.delta = at; if (bwd) at += sizeof(float) * (size_t)p.tokens * p.Hq;
+    w.total = align_up(at, 256);
+    return w;
+}
+
+// Clears the status word and lists the tiles (the list's unused end gets empty
+// sequences).
+cudaError_t launch_attn_plan(const AttnProblem &p, int rows, void *workspace, cudaStream_t st);
+
+int attn_fwd_rows(const AttnProblem &p);  // tokens per tile of the path that serves p
+int attn_bwd_rows(const AttnProblem &p);
+cudaError_t launch_attn_fwd(const AttnProblem &p, void *o, float *lse, void *workspace,
+                            cudaStream_t st);
+cudaError_t launch_attn_bwd(const AttnProblem &p, const void *o, const float *lse,
+                            const void *dO, void *gq, void *gk, void *gv, void *workspace,
+                            cudaStream_t st);
+
+// A tree-attention call after host-side validation.
+struct TreeProblem {
+    const void *q, *k_pages, *v_pages;
+    const int32_t *table, *ctx_lens, *parents;
+    int N, R, Hq, Hkv, d, P, M, page_shift;
+    float scale;
+    kda_dtype_t dtype;
+    void *o;
+    float *lse;
+};
+size_t tree_workspace_bytes(const TreeProblem &p);
+cudaError_t launch_attn_tree(const TreeProblem &p, void *workspace, cudaStream_t st);
+
+// Launches of the cache's page calls (kda_cache.cu); sizes are validated.
+struct PagePool {
+    void *k, *v;
+    int P, Hkv, d, page_shift, elem;  // elem: bytes per element
+};
+cudaError_t launch_cache_fork(int32_t *refs, const int32_t *table, const int32_t *lens,
+                              const int32_t *parents, int N_in, int N_out, int M, int P,
+                              int32_t *new_table, int32_t *new_lens, cudaStream_t st);
+cudaError_t launch_cache_reserve(int32_t *refs, int32_t *table, int32_t *lens,
+                                 const int32_t *add, int N, int M, int P, int page_shift,
+                                 int32_t *copies, int32_t *status, void *workspace,
+                                 cudaStream_t st);
+cudaError_t launch_cache_release(int32_t *refs, int32_t *table, int32_t *lens,
+                                 const int32_t *new_lens, int N, int M, int P, int page_shift,
+                                 cudaStream_t st);
+cudaError_t launch_cache_append(const PagePool &pool, const int32_t *table, const int32_t *start,
+                                const void *k_new, const void *v_new, const int32_t *cu_seqlens,
+                                int N, int B, int T, int M, cudaStream_t st);
+cudaError_t launch_cache_compact(const PagePool &pool, const int32_t *table,
+                                 const int32_t *ctx_lens, const int32_t *path, int N, int R,
+                                 int M, int32_t *new_lens, cudaStream_t st);
+cudaError_t launch_cache_copy(const PagePool &pool, const int32_t *copies, int C,
+                              cudaStream_t st);
+
+}  // namespace kda

@@ -1,0 +1,429 @@
+// kda_cache.cu — pages of the full-attention layers' key/value cache: tables that
+// fork, grow and shrink on the device, and the data moves that go with them.
+//
+// The table calls read and write a few hundred kilobytes at most and are bound by
+// the latency of their dependent steps; the data calls are bound by HBM and move
+// 16 bytes per thread and access, the pages of one (page, head) being contiguous.
+// Reference counts are kept with integer atomics, whose order does not change the
+// result; pages are handed out by prefix sums in row order.
+#include "kda_attn.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kWide = 1024;
+
+__device__ __forceinline__ bool page_ok(int id, int P) { return (unsigned)id < (unsigned)P; }
+
+// Tokens of a row, whatever the table's owner wrote: at least 0, at most M pages.
+__device__ __forceinline__ int clamp_len(int len, int M, int shift)
+{
+    return min(max(len, 0), M << shift);
+}
+
+__device__ __forceinline__ int pages_of(int len, int shift)
+{
+    return (len >> shift) + ((len & ((1 << shift) - 1)) != 0);
+}
+
+// ---------------------------------------------------------------- fork
+// One warp per row: the first N_out copy a row of the old table and take hold of its
+// pages, the other N_in let go of an old row's pages.
+__global__ void __launch_bounds__(256)
+cache_fork_kernel(int32_t *refs, const int32_t *table, const int32_t *lens,
+                  const int32_t *parents, int N_in, int N_out, int M, int P,
+                  int32_t *new_table, int32_t *new_lens)
+{
+    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (w >= (long long)N_out + N_in) return;
+    if (w < N_out) {
+        const int from = parents[w];
+        const bool any = (unsigned)from < (unsigned)N_in;
+        for (int m = lane; m < M; m += 32) {
+            const int id = any ? table[(size_t)from * M + m] : -1;
+            new_table[(size_t)w * M + m] = id;
+            if (page_ok(id, P)) atomicAdd(refs + id, 1);
+        }
+        if (lane == 0) new_lens[w] = any ? lens[from] : 0;
+        return;
+    }
+    const size_t n = (size_t)(w - N_out);
+    for (int m = lane; m < M; m += 32) {
+        const int id = table[n * M + m];
+        if (page_ok(id, P)) atomicSub(refs + id, 1);
+    }
+}
+
+// ---------------------------------------------------------------- reserve
+// Inclusive scan over a block of kWide threads.
+__device__ long long block_scan(long long x, long long *s_warp)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        long long v = s_warp[lane];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, off);
+            if (lane >= off) v += y;
+        }
+        s_warp[lane] = v;
+    }
+    __syncthreads();
+    if (warp > 0) x += s_warp[warp - 1];
+    __syncthreads();
+    return x;
+}
+
+struct Row {
+    int len, have, tail;  // tail: the partly filled last page that is to be written, or -1
+    long long want;       // pages after the call
+};
+
+__device__ __forceinline__ Row row_of(const int32_t *table, const int32_t *lens,
+                                      const int32_t *add, int n, int M, int P, int shift)
+{
+    Row r;
+    r.len = clamp_len(lens[n], M, shift);
+    r.have = pages_of(r.len, shift);
+    const int more = max(add[n], 0);
+    r.want = ((long long)r.len + more + (1 << shift) - 1) >> shift;
+    r.tail = -1;
+    if (more > 0 && (r.len & ((1 << shift) - 1))) {
+        const int id = table[(size_t)n * M + r.have - 1];
+        if (page_ok(id, P)) r.tail = id;
+    }
+    return r;
+}
+
+// One block: rows and pages are few, and their order is what makes the result.
+// A row copies its last page unless it is the page's only holder, or the last of
+// rows of this call that are together all its holders; both follow from the number
+// of such rows per page and the largest of them, which atomics count in any order.
+__global__ void __launch_bounds__(kWide)
+cache_reserve_kernel(int32_t *refs, int32_t *table, int32_t *lens, const int32_t *add, int N,
+                     int M, int P, int shift, int32_t *copies, int32_t *status,
+                     int32_t *ws)
+{
+    __shared__ long long s_warp[32];
+    __shared__ long long s_carry;
+    __shared__ int s_over;
+    int32_t *sharers = ws, *last = ws + P, *freed = ws + 2 * (size_t)P;
+    int32_t *first = ws + 3 * (size_t)P, *cow = first + N;
+    const int tid = threadIdx.x;
+    if (tid == 0) { s_over = INT32_MAX; s_carry = 0; }
+    for (int n = tid; n < N; n += kWide) {
+        const Row r = row_of(table, lens, add, n, M, P, shift);
+        if (r.tail >= 0) { sharers[r.tail] = 0; last[r.tail] = -1; }
+    }
+    __syncthreads();
+    for (int n = tid; n < N; n += kWide) {
+        const Row r = row_of(table, lens, add, n, M, P, shift);
+        if (r.want > M) atomicMin(&s_over, n);
+        if (r.tail >= 0) { atomicAdd(sharers + r.tail, 1); atomicMax(last + r.tail, n); }
+    }
+    __syncthreads();
+    // pages each row takes, and where its share of the free pages begins
+    for (int base = 0; base < N; base += kWide) {
+        const int n = base + tid;
+        long long count = 0;
+        if (n < N) {
+            const Row r = row_of(table, lens, add, n, M, P, shift);
+            const bool copy = r.tail >= 0 && refs[r.tail] > 1 &&
+                              !(sharers[r.tail] >= refs[r.tail] && last[r.tail] == n);
+            cow[n] = copy;
+            count = (copy ? 1 : 0) + (r.want - r.have);
+        }
+        const long long incl = block_scan(count, s_warp);
+        const long long carry = s_carry;
+        if (n < N) first[n] = (int)min(carry + incl - count, (long long)INT32_MAX);
+        __syncthreads();
+        if (tid == kWide - 1) s_carry = carry + incl;
+        __syncthreads();
+    }
+    const long long need = s_carry;
+    __syncthreads();
+    // the lowest free pages in order, as many as are needed
+    if (tid == 0) s_carry = 0;
+    __syncthreads();
+    constexpr int kEach = 8;
+    for (int base = 0; base < P; base += kWide * kEach) {
+        const long long carry = s_carry;
+        if (carry >= need) break;
+        const int at = base + tid * kEach;
+        unsigned bits = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+            if (at + j < P && refs[at + j] == 0) bits |= 1u << j;
+        const int mine = __popc(bits);
+        const long long incl = block_scan(mine, s_warp);
+        long long to = carry + incl - mine;
+        for (; bits; bits &= bits - 1, ++to)
+            if (to < need) freed[to] = at + __ffs(bits) - 1;
+        __syncthreads();
+        if (tid == kWide - 1) s_carry = carry + incl;
+        __syncthreads();
+    }
+    const long long found = s_carry;
+    const int over = s_over;
+    const bool fails = over != INT32_MAX || found < need;
+    if (tid == 0)
+        *status = over != INT32_MAX ? -1 - over
+                  : found < need    ? (int)min(need - found, (long long)INT32_MAX)
+                                    : 0;
+    // one warp per row
+    const int lane = tid & 31;
+    for (int n = tid >> 5; n < N; n += kWide / 32) {
+        int from = -1, to = -1;
+        if (!fails) {
+            const Row r = row_of(table, lens, add, n, M, P, shift);
+            const bool copy = cow[n] != 0;
+            const int at = first[n];
+            __syncwarp();
+            if (copy) { from = r.tail; to = freed[at]; }
+            const int more = (int)(r.want - r.have);
+            for (int j = lane; j < more; j += 32) {
+                const int id = freed[at + copy + j];
+                table[(size_t)n * M + r.have + j] = id;
+                refs[id] = 1;
+            }
+            if (lane == 0) {
+                if (copy) {
+                    table[(size_t)n * M + r.have - 1] = to;
+                    refs[to] = 1;
+                    atomicSub(refs + from, 1);
+                }
+                lens[n] = r.len + max(add[n], 0);
+            }
+        }
+        if (lane < 2) copies[2 * (size_t)n + lane] = lane ? to : from;
+    }
+}
+
+// ---------------------------------------------------------------- release
+__global__ void __launch_bounds__(256)
+cache_release_kernel(int32_t *refs, int32_t *table, int32_t *lens, const int32_t *new_lens,
+                     int N, int M, int P, int shift)
+{
+    const long long n = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (n >= N) return;
+    const int len = clamp_len(min(lens[n], new_lens[n]), M, shift);
+    __syncwarp();
+    if (lane == 0) lens[n] = len;
+    for (int m = pages_of(len, shift) + lane; m < M; m += 32) {
+        const int id = table[n * M + m];
+        if (page_ok(id, P)) atomicSub(refs + id, 1);
+        table[n * M + m] = -1;
+    }
+}
+
+// ---------------------------------------------------------------- data
+// Byte offset of position pos of a row, head hk, in a pool; -1 where it has no page.
+__device__ __forceinline__ long long place(const PagePool &pool, const int32_t *row, int M,
+                                           long long pos, int hk)
+{
+    if (pos < 0 || pos >= (long long)M << pool.page_shift) return -1;
+    const int id = row[pos >> pool.page_shift];
+    if (!page_ok(id, pool.P)) return -1;
+    const long long slot = pos & ((1 << pool.page_shift) - 1);
+    return ((((long long)id * pool.Hkv + hk) << pool.page_shift) + slot) * pool.d * pool.elem;
+}
+
+// One thread per 16 bytes of a token's keys and of its values.
+__global__ void __launch_bounds__(256)
+cache_append_kernel(PagePool pool, const int32_t *table, const int32_t *start,
+                    const char *k_new, const char *v_new, const int32_t *cu, int N, int T,
+                    int M, long long units, int head_units)
+{
+    const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (u >= units) return;
+    const int per_token = pool.Hkv * head_units;
+    const long long t = u / per_token;
+    const int in = (int)(u % per_token), hk = in / head_units, x = in % head_units;
+    int n;
+    long long pos;
+    if (cu) {  // the last sequence that starts at or before t
+        int lo = 0, hi = N;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cu[mid] <= t) lo = mid; else hi = mid;
+        }
+        n = lo;
+        if (t < cu[n] || t >= cu[n + 1]) return;
+        pos = t - cu[n];
+    } else {
+        n = (int)(t / T);
+        pos = t % T;
+    }
+    const long long to = place(pool, table + (size_t)n * M, M, start[n] + pos, hk);
+    if (start[n] < 0 || to < 0) return;
+    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(k_new) + u);
+    const uint4 b = __ldg(reinterpret_cast<const uint4 *>(v_new) + u);
+    *reinterpret_cast<uint4 *>(static_cast<char *>(pool.k) + to + x * 16) = a;
+    *reinterpret_cast<uint4 *>(static_cast<char *>(pool.v) + to + x * 16) = b;
+}
+
+// One block per sequence and 256 16-byte columns of (k or v, head). A thread moves its
+// column's kept tokens in order, four reads ahead of four writes: path[j] >= j and the
+// path increases, so a token is read before its place is written.
+__global__ void __launch_bounds__(256)
+cache_compact_kernel(PagePool pool, const int32_t *table, const int32_t *ctx_lens,
+                     const int32_t *path, int R, int M, int head_units, int32_t *new_lens)
+{
+    __shared__ int s_path[1024];
+    __shared__ int s_kept;
+    const int n = blockIdx.x, tid = threadIdx.x;
+    if (tid == 0) s_kept = R;
+    __syncthreads();
+    for (int j = tid; j < R; j += 256) {
+        const int a = path[(size_t)n * R + j];
+        const int before = j ? path[(size_t)n * R + j - 1] : -1;
+        s_path[j] = a;
+        if (a <= before || a >= R || a < 0) atomicMin(&s_kept, j);
+    }
+    __syncthreads();
+    const int kept = s_kept;
+    const int ctx = clamp_len(ctx_lens[n], M, pool.page_shift);
+    if (blockIdx.y == 0 && tid == 0) new_lens[n] = ctx + kept;
+    const int u = blockIdx.y * 256 + tid, per_pool = pool.Hkv * head_units;
+    if (u >= 2 * per_pool) return;
+    char *base = static_cast<char *>(u < per_pool ? pool.k : pool.v) + (u % head_units) * 16;
+    const int hk = u % per_pool / head_units;
+    const int32_t *row = table + (size_t)n * M;
+    constexpr int kAhead = 4;
+    for (int j0 = 0; j0 < kept; j0 += kAhead) {
+        uint4 x[kAhead];
+        long long to[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            to[i] = -1;
+            const int j = j0 + i;
+            if (j >= kept || s_path[j] == j) continue;
+            const long long from = place(pool, row, M, (long long)ctx + s_path[j], hk);
+            if (from < 0) continue;
+            to[i] = place(pool, row, M, (long long)ctx + j, hk);
+            x[i] = *reinterpret_cast<const uint4 *>(base + from);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (to[i] >= 0) *reinterpret_cast<uint4 *>(base + to[i]) = x[i];
+    }
+}
+
+// One block per pair, slice of the page, and pool. Whether a pair is left out is found
+// from the whole list by every block of it: the list is short.
+__global__ void __launch_bounds__(256)
+cache_copy_kernel(PagePool pool, const int2 *copies, int C, long long page_units)
+{
+    const int c = blockIdx.x;
+    const int2 me = copies[c];
+    if (!page_ok(me.x, pool.P) || !page_ok(me.y, pool.P) || me.x == me.y) return;
+    int out = 0;
+    for (int i = threadIdx.x; i < C; i += 256) {
+        const int2 o = copies[i];
+        if (!page_ok(o.x, pool.P) || !page_ok(o.y, pool.P) || o.x == o.y) continue;
+        out |= (i < c && o.y == me.y) || o.x == me.y;
+    }
+    if (__syncthreads_or(out)) return;
+    char *p = static_cast<char *>(blockIdx.z ? pool.v : pool.k);
+    const uint4 *src = reinterpret_cast<const uint4 *>(p) + (size_t)me.x * page_units;
+    uint4 *dst = reinterpret_cast<uint4 *>(p) + (size_t)me.y * page_units;
+    constexpr int kEach = 4;
+    for (long long base = (long long)blockIdx.y * 256 * kEach; base < page_units;
+         base += (long long)gridDim.y * 256 * kEach) {
+        uint4 x[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const long long at = base + i * 256 + threadIdx.x;
+            if (at < page_units) x[i] = src[at];
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const long long at = base + i * 256 + threadIdx.x;
+            if (at < page_units) dst[at] = x[i];
+        }
+    }
+}
+
+cudaError_t launched()
+{
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_fork(int32_t *refs, const int32_t *table, const int32_t *lens,
+                              const int32_t *parents, int N_in, int N_out, int M, int P,
+                              int32_t *new_table, int32_t *new_lens, cudaStream_t st)
+{
+    const long long warps = (long long)N_in + N_out;
+    cache_fork_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(
+        refs, table, lens, parents, N_in, N_out, M, P, new_table, new_lens);
+    return launched();
+}
+
+cudaError_t launch_cache_reserve(int32_t *refs, int32_t *table, int32_t *lens,
+                                 const int32_t *add, int N, int M, int P, int page_shift,
+                                 int32_t *copies, int32_t *status, void *workspace,
+                                 cudaStream_t st)
+{
+    cache_reserve_kernel<<<1, kWide, 0, st>>>(refs, table, lens, add, N, M, P, page_shift, copies,
+                                              status, static_cast<int32_t *>(workspace));
+    return launched();
+}
+
+cudaError_t launch_cache_release(int32_t *refs, int32_t *table, int32_t *lens,
+                                 const int32_t *new_lens, int N, int M, int P, int page_shift,
+                                 cudaStream_t st)
+{
+    cache_release_kernel<<<(unsigned)(((long long)N + 7) / 8), 256, 0, st>>>(
+        refs, table, lens, new_lens, N, M, P, page_shift);
+    return launched();
+}
+
+cudaError_t launch_cache_append(const PagePool &pool, const int32_t *table, const int32_t *start,
+                                const void *k_new, const void *v_new, const int32_t *cu_seqlens,
+                                int N, int B, int T, int M, cudaStream_t st)
+{
+    const int head_units = pool.d * pool.elem / 16;
+    const long long units = (long long)B * T * pool.Hkv * head_units;
+    const long long blocks = (units + 255) / 256;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    cache_append_kernel<<<(unsigned)blocks, 256, 0, st>>>(
+        pool, table, start, static_cast<const char *>(k_new), static_cast<const char *>(v_new),
+        cu_seqlens, N, T, M, units, head_units);
+    return launched();
+}
+
+cudaError_t launch_cache_compact(const PagePool &pool, const int32_t *table,
+                                 const int32_t *ctx_lens, const int32_t *path, int N, int R,
+                                 int M, int32_t *new_lens, cudaStream_t st)
+{
+    const int head_units = pool.d * pool.elem / 16;
+    const dim3 grid((unsigned)N, (unsigned)((2 * pool.Hkv * head_units + 255) / 256));
+    cache_compact_kernel<<<grid, 256, 0, st>>>(pool, table, ctx_lens, path, R, M, head_units,
+                                               new_lens);
+    return launched();
+}
+
+cudaError_t launch_cache_copy(const PagePool &pool, const int32_t *copies, int C,
+                              cudaStream_t st)
+{
+    const long long units = ((long long)pool.Hkv << pool.page_shift) * pool.d * pool.elem / 16;
+    const long long slices = (units + 1023) / 1024;
+    const dim3 grid((unsigned)C, (unsigned)(slices < 64 ? slices : 64), 2);
+    cache_copy_kernel<<<grid, 256, 0, st>>>(pool, reinterpret_cast<const int2 *>(copies), C,
+                                            units);
+    return launched();
+}
+
+}  // namespace kda

@@ -408,6 +408,145 @@ kda_status_t kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
                                    int dk, int dv, float scale, void *o, float *S_final,
                                    int algo, void *stream);
 
+/*
+ * Full attention. A hybrid model interleaves the KDA layers with full-attention
+ * layers without position encoding ("Kimi Linear" juejin.cn page, section 三 3️⃣ and
+ * 4️⃣); the calls below are that layer's token mixing with grouped heads: query
+ * head h reads key/value head h / (Hq / Hkv). The pages give the definition only
+ * (softmax(Q K^T / sqrt(d)) V); the paged cache is this library's own.
+ *
+ * Layouts (dense, row-major, 16-byte aligned device buffers; dtype fp32 or bf16;
+ * d in {32, 64, 128}; Hq a multiple of Hkv):
+ *   q, o, dO, grad_q          [B, T, Hq, d]      dtype
+ *   k, v, grad_k, grad_v      [B, T, Hkv, d]     dtype
+ *   lse                       [B, T, Hq]         fp32, natural logarithm
+ * Sequences (cu_seqlens, n_seqs) as for the prefill; offsets are sanitised on the
+ * device in the same way. `scale` must be positive and finite. Sums, softmax
+ * statistics and accumulators are fp32; with bf16 inputs the probabilities (and
+ * in the backward the score gradients) are rounded to bf16 as operands of the
+ * tensor-core products. Results do not depend on the order of execution.
+ *
+ * kda_attn_fwd: causal attention of every sequence,
+ *     s_rc = scale <q_r, k_c> (c <= r),  lse_r = log sum_c e^(s_rc),
+ *     o_r = sum_c e^(s_rc - lse_r) v_c.
+ * Keys and values a row does not see have no influence on it, whatever they hold
+ * (infinities and NaN included). Tokens outside every sequence are not written.
+ * lse may be NULL. T = 0 returns KDA_OK without touching anything.
+ *
+ * kda_attn_bwd: the gradients of <dO, o> with respect to q, k and v in the inputs'
+ * dtype, from the forward's inputs, its o and its lse:
+ *     p_rc = e^(s_rc - lse_r),  D_r = <dO_r, o_r>,  ds_rc = scale p_rc (<dO_r, v_c> - D_r),
+ *     grad_q_r = sum_c ds_rc k_c,  grad_k_c = sum_r ds_rc q_r,  grad_v_c = sum_r p_rc dO_r
+ * (grad_k and grad_v summed over the group's query heads in fp32 before rounding).
+ *
+ * Errors as for kda_chunk_fwd. kda_attn_status reads the status word of the last
+ * kda_attn_fwd / kda_attn_bwd on a workspace, as kda_chunk_fwd_status does.
+ */
+size_t kda_attn_fwd_workspace_size(int B, int T, int Hq, int Hkv, int d, int n_seqs,
+                                   kda_dtype_t dtype);
+kda_status_t kda_attn_fwd(const void *q, const void *k, const void *v, kda_dtype_t dtype,
+                          const int32_t *cu_seqlens, int n_seqs, int B, int T, int Hq, int Hkv,
+                          int d, float scale, void *o, float *lse, void *workspace,
+                          size_t workspace_bytes, void *stream);
+size_t kda_attn_bwd_workspace_size(int B, int T, int Hq, int Hkv, int d, int n_seqs,
+                                   kda_dtype_t dtype);
+kda_status_t kda_attn_bwd(const void *q, const void *k, const void *v, const void *o,
+                          const float *lse, const void *dO, kda_dtype_t dtype,
+                          const int32_t *cu_seqlens, int n_seqs, int B, int T, int Hq, int Hkv,
+                          int d, float scale, void *grad_q, void *grad_k, void *grad_v,
+                          void *workspace, size_t workspace_bytes, void *stream);
+kda_status_t kda_attn_status(const void *workspace, size_t workspace_bytes, int *device_code,
+                             void *stream);
+
+/*
+ * The paged key/value cache of one full-attention layer:
+ *   k_pages, v_pages  [P, Hkv, page_size, d]  dtype; page_size a power of two, 1..1024
+ *   block_table       int32 [N, M]   page of each page_size tokens of a sequence (row);
+ *                                    entries behind the last page hold -1
+ *   lens              int32 [N]      tokens in each row
+ *   refs              int32 [P]      rows that hold each page; 0: the page is free
+ * One block_table, lens and refs serve the pools of all layers. A page number outside
+ * [0, P) reads as no page: its tokens are not attended to, not written and not counted.
+ *
+ * kda_attn_tree: attention of R drafted tokens per sequence over its cache. Token i of
+ * sequence n sits at position ctx_lens[n] + i, where its key and value already are
+ * (kda_cache_append). It attends to the positions [0, ctx_lens[n]), to itself and to
+ * the drafted tokens above it in the tree: parents[n, i] is its parent's index (less
+ * than i), or -1 where the parent is the last cached token. Any other value makes the
+ * token absent, and with it all tokens that descend from it: absent tokens, and tokens
+ * that find no key at all, get o = 0 and lse = -inf. parents = NULL is a chain (parent
+ * i - 1); R = 1 with it is the ordinary decode step.
+ *   q, o      [N, R, Hq, d]  dtype          lse  fp32 [N, R, Hq] or NULL
+ *   ctx_lens  int32 [N], clamped to [0, M * page_size]
+ *   parents   int32 [N, R] or NULL          R <= 64
+ * R = 0 returns KDA_OK without touching anything.
+ */
+size_t kda_attn_tree_workspace_size(int N, int R, int Hq, int Hkv, int d, int M, int page_size,
+                                    kda_dtype_t dtype);
+kda_status_t kda_attn_tree(const void *q, const void *k_pages, const void *v_pages,
+                           kda_dtype_t dtype, const int32_t *block_table, const int32_t *ctx_lens,
+                           const int32_t *parents, int N, int R, int Hq, int Hkv, int d, int P,
+                           int M, int page_size, float scale, void *o, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Pages of the cache. The table calls work on block_table, lens and refs once for all
+ * layers; the data calls move keys and values of one layer's pools. Everything stays on
+ * the device and is deterministic.
+ *
+ * kda_cache_fork (table): row n of the new table (N_out rows) becomes a copy of row
+ * parents[n] of the old one, sharing all its pages (parents outside [0, N_in) give an
+ * empty row); then the old rows end. A row taken twice is forked, one taken by nobody
+ * is freed. The new table and lens must not overlap the old ones.
+ *
+ * kda_cache_reserve (table): makes room for add[n] >= 0 more tokens in every row and
+ * adds them to lens. Pages are the lowest-numbered free ones, handed out row after
+ * row. A last page that is partly filled and held by other rows too is replaced by a
+ * new one first; copies[n] = (old page, new page) then, else (-1, -1): pass it to
+ * kda_cache_copy_pages for every layer. Of several rows that share such a page and
+ * together are all its holders, the last one keeps it. All or nothing: status[0] = 0,
+ * or the number of pages that are missing, or -1 - n for the first row n that would
+ * need more than M pages; where it is not 0, nothing has changed and copies is all -1.
+ *
+ * kda_cache_release (table): cuts every row to min(lens[n], new_lens[n]) tokens and
+ * lets go of the pages behind (new_lens = 0 frees the row).
+ *
+ * kda_cache_append (data): writes k_new and v_new ([B, T, Hkv, d], sequences as for the
+ * prefill) into the rows' pages, sequence n from position start[n] on.
+ *
+ * kda_cache_compact (data): keeps the drafted tokens path[n, 0], path[n, 1], ... (an
+ * increasing list of indices below R, ended by the first entry that is not one) of row
+ * n, whose drafts begin at position ctx_lens[n]: moves them together to ctx_lens[n],
+ * ctx_lens[n] + 1, ..., and writes ctx_lens[n] plus their number to new_lens[n].
+ *
+ * kda_cache_copy_pages (data): copies page copies[c, 0] to page copies[c, 1] for every
+ * c < C (at most 16384). A pair with a number outside [0, P), with a destination that
+ * an earlier pair already has, or with one that is the source of another pair is left out.
+ */
+kda_status_t kda_cache_fork(int32_t *refs, const int32_t *block_table, const int32_t *lens,
+                            const int32_t *parents, int N_in, int N_out, int M, int P,
+                            int32_t *new_table, int32_t *new_lens, void *stream);
+size_t kda_cache_reserve_workspace_size(int N, int M, int P);
+kda_status_t kda_cache_reserve(int32_t *refs, int32_t *block_table, int32_t *lens,
+                               const int32_t *add, int N, int M, int P, int page_size,
+                               int32_t *copies, int32_t *status, void *workspace,
+                               size_t workspace_bytes, void *stream);
+kda_status_t kda_cache_release(int32_t *refs, int32_t *block_table, int32_t *lens,
+                               const int32_t *new_lens, int N, int M, int P, int page_size,
+                               void *stream);
+kda_status_t kda_cache_append(void *k_pages, void *v_pages, kda_dtype_t dtype,
+                              const int32_t *block_table, const int32_t *start,
+                              const void *k_new, const void *v_new, const int32_t *cu_seqlens,
+                              int n_seqs, int B, int T, int Hkv, int d, int P, int M,
+                              int page_size, void *stream);
+kda_status_t kda_cache_compact(void *k_pages, void *v_pages, kda_dtype_t dtype,
+                               const int32_t *block_table, const int32_t *ctx_lens,
+                               const int32_t *path, int N, int R, int Hkv, int d, int P, int M,
+                               int page_size, int32_t *new_lens, void *stream);
+kda_status_t kda_cache_copy_pages(void *k_pages, void *v_pages, kda_dtype_t dtype,
+                                  const int32_t *copies, int C, int Hkv, int d, int P,
+                                  int page_size, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
