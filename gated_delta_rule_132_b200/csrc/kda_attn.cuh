@@ -65,6 +65,11 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, const void *o, const float *ls
                             const void *dO, void *gq, void *gk, void *gv, void *workspace,
                             cudaStream_t st);
 
+// The tensor-core path (bf16).
+int attn_tc_fwd_rows();
+cudaError_t launch_attn_tc_fwd(const AttnProblem &p, void *o, float *lse, void *workspace,
+                               cudaStream_t st);
+
 // A tree-attention call after host-side validation.
 struct TreeProblem {
     const void *q, *k_pages, *v_pages;

@@ -1,0 +1,351 @@
+// kda_attn_fwd.cu — causal prompt attention on the tensor cores (bf16, d = 32, 64, 128).
+//
+// One CTA per (256 query tokens, query head): two query tiles of 128 rows that share
+// the key/value tiles, walked from the diagonal down to the sequence's first tile.
+// Per tile pair S = Q K^T goes to TMEM, one thread per row turns it into
+// P = 2^(c s - c m) (c = scale log2 e, m the row's running reference) in registers,
+// writes P in bf16 over S, and O += P V reads it from there. Warps 0-3 own the rows of
+// query tile 0, warps 4-7 those of tile 1; warp 8 issues the MMAs, ordered so that one
+// tile's products run while the other tile's rows are in the softmax; warp 9 loads.
+//
+// The reference m moves only when the row maximum has grown by more than 2^8 in
+// weight: P stays below 2^8, its bf16 relative error and the fp32 sums do not depend
+// on the reference, and O is hardly ever rescaled. Sums use P before its rounding.
+//
+// A masked probability is 0, but 0 times an infinity or NaN in a later token's (or
+// another sequence's) value row is NaN. Rows with a result that is not finite are
+// therefore computed again from the visible keys alone.
+#include "kda_attn_rows.cuh"
+#include "kda_attn_tc.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kRows = 2 * kTileRows;
+constexpr int kThreads = 384;  // two softmax warpgroups; MMA, load and two idle warps
+// 384 threads start with 168 registers; the softmax keeps a row of 128 scores.
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
+constexpr float kRescale = 8.f;  // log2 of the growth that moves the reference
+
+struct FwdParams {
+    CUtensorMap q, k, v;
+    AttnProblem p;
+    const AttnTile *tiles;  // null: uniform sequences
+    __nv_bfloat16 *o;
+    float *lse;
+    int *status;
+    uint32_t spin;
+    int starve;
+};
+
+template <int D>
+struct FwdShape {
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr uint32_t kTile = TileShape<D>::kBytes;
+    static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = kK + kStages * kTile;
+    static constexpr uint32_t kBars = kV + kStages * kTile;
+    static constexpr uint32_t kBytes = kBars + 256 + 1024;  // and the base's alignment
+    static constexpr uint32_t kTmemS = 0, kTmemO = 256;     // columns
+};
+
+enum : int { kErrQ = 101, kErrK, kErrV, kErrEmpty, kErrS, kErrP, kErrO, kErrDrain };
+
+template <int D>
+__device__ __noinline__ void recompute_row(const FwdParams &f, int row, int start, int h)
+{
+    attn_row_fwd<__nv_bfloat16, D>(f.p, row, start, h, f.o, f.lse);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdParams f)
+{
+    using S = FwdShape<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kBars);
+    uint64_t *q_full = bars;
+    uint64_t *k_full = bars + 1, *k_free = k_full + S::kStages;
+    uint64_t *v_full = k_free + S::kStages, *v_free = v_full + S::kStages;
+    uint64_t *s_full = v_free + S::kStages;   // [2] scores of a query tile are in TMEM
+    uint64_t *p_full = s_full + 2;            // [2] its probabilities are (one arrival per warp)
+    uint64_t *o_full = p_full + 2;            // all products are done
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_full + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x % f.p.Hq;
+    const AttnTile t = attn_tile(f.tiles, blockIdx.x / f.p.Hq, kRows, f.p.B, f.p.T);
+    if (t.first >= t.seq_end) return;  // the list's unused end
+    if (!f.tiles && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
+
+    // query tiles, and the key tiles from the last one down: step it reads key tile
+    // last - it; tile w takes part from step begin[w] on
+    const bool two = t.first + kTileRows < t.seq_end;
+    const int diag0 = (t.first - t.seq_start) / kTileRows;
+    const int last = diag0 + two, steps = last + 1;
+
+    if (warp == 8) tc::tmem_alloc(tmem_slot, 512);
+    if (threadIdx.x == 0) {
+        tc::mbar_init(q_full, 1);
+        for (int i = 0; i < S::kStages; ++i) {
+            tc::mbar_init(k_full + i, 1);
+            tc::mbar_init(k_free + i, 1);
+            tc::mbar_init(v_full + i, 1);
+            tc::mbar_init(v_free + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(s_full + i, 1);
+            tc::mbar_init(p_full + i, 4);
+        }
+        tc::mbar_init(o_full, 1);
+        *abort = 0;
+        tc::fence_mbar_init();
+    }
+    tc::tc_fence_before_sync();
+    __syncthreads();
+    tc::tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp >= 8) {
+        tc::fewer_registers<kRegsOther>();
+        if (warp == 9 && lane == 0 && !f.starve) {
+            const int hk = h / (f.p.Hq / f.p.Hkv);
+            tc::mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * S::kTile);
+            for (int w = 0; w <= two; ++w)
+                tc::load_tile<D>(sm + S::kQ + w * S::kTile, &f.q, h, t.first + w * kTileRows, q_full);
+            int it = 0;
+            for (; it < steps; ++it) {
+                const int st = it % S::kStages, use = it / S::kStages;
+                const int token = t.seq_start + (last - it) * kTileRows;
+                if (use && !tc::mbar_wait(k_free + st, (use - 1) & 1, abort, f.status, kErrEmpty, f.spin)) break;
+                tc::mbar_arrive_expect_tx(k_full + st, S::kTile);
+                tc::load_tile<D>(sm + S::kK + st * S::kTile, &f.k, hk, token, k_full + st);
+                if (use && !tc::mbar_wait(v_free + st, (use - 1) & 1, abort, f.status, kErrEmpty, f.spin)) {
+                    tc::mbar_drain(k_full + st, use & 1, f.status, kErrDrain);
+                    break;
+                }
+                tc::mbar_arrive_expect_tx(v_full + st, S::kTile);
+                tc::load_tile<D>(sm + S::kV + st * S::kTile, &f.v, hk, token, v_full + st);
+            }
+            // whatever the other warps do, the copies land before the memory is let go
+            tc::mbar_drain(q_full, 0, f.status, kErrDrain);
+            for (int i = max(0, it - S::kStages); i < it; ++i) {
+                tc::mbar_drain(k_full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
+                tc::mbar_drain(v_full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
+            }
+        }
+        if (warp == 8 && lane == 0) {
+            const uint32_t q = tc::smem_u32(sm + S::kQ), k = tc::smem_u32(sm + S::kK),
+                           v = tc::smem_u32(sm + S::kV);
+            bool go = tc::mbar_wait(q_full, 0, abort, f.status, kErrQ, f.spin);
+            // O_w += P_w(it) V(it)
+            auto pv = [&](int w, int begin, int it) {
+                const int st = it % S::kStages;
+                go = go && tc::mbar_wait(v_full + st, (it / S::kStages) & 1, abort, f.status, kErrV, f.spin) &&
+                     tc::mbar_wait(p_full + w, (it - begin) & 1, abort, f.status, kErrP, f.spin);
+                if (!go) return;
+                tc::tc_fence_after_sync();
+                tc::mma_weights_rows<D>(tmem + S::kTmemO + w * D, tmem + S::kTmemS + w * 128,
+                                        v + st * S::kTile, it > begin);
+            };
+            for (int it = 0; it < steps && go; ++it) {
+                const int st = it % S::kStages;
+                go = tc::mbar_wait(k_full + st, (it / S::kStages) & 1, abort, f.status, kErrK, f.spin);
+                for (int w = 0; w <= two && go; ++w) {
+                    const int begin = two && w == 0;
+                    if (it < begin) continue;
+                    if (it > begin) pv(w, begin, it - 1);
+                    if (!go) break;
+                    tc::mma_rows_rows<D>(tmem + S::kTmemS + w * 128, q + w * S::kTile, k + st * S::kTile);
+                    tc::mma_commit(s_full + w);
+                }
+                if (!go) break;
+                tc::mma_commit(k_free + st);
+                if (it > 0) tc::mma_commit(v_free + (it - 1) % S::kStages);
+            }
+            for (int w = 0; w <= two && go; ++w) pv(w, two && w == 0, steps - 1);
+            tc::mma_commit(o_full);
+            tc::mbar_drain(o_full, 0, f.status, kErrDrain);
+        }
+    } else {
+        tc::more_registers<kRegsSoftmax>();
+        if (warp < (two ? 8 : 4)) {
+            const int w = warp >> 2, begin = two && w == 0;
+            const int in_tile = threadIdx.x & 127, row = t.first + w * kTileRows + in_tile;
+            const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's TMEM lanes (32 each, bits 16 up)
+            const uint32_t ts = tmem + lanes + S::kTmemS + w * 128;
+            const uint32_t to = tmem + lanes + S::kTmemO + w * D;
+            const float c = f.p.scale * 1.44269504088896340736f;
+            float m = -INFINITY, l = 0.f;  // reference (unscaled score) and sum
+            bool go = true;
+            for (int it = begin; it < steps; ++it) {
+                go = __all_sync(0xffffffffu,
+                                tc::mbar_wait(s_full + w, (it - begin) & 1, abort, f.status, kErrS, f.spin));
+                if (!go) break;
+                tc::tc_fence_after_sync();
+                float s[128];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tc::tmem_start(ts + 32 * i, s + 32 * i);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tc::tmem_ready(s + 32 * i);
+                if (it == begin) {  // the diagonal tile
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) s[i] = i <= in_tile ? s[i] : -INFINITY;
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int i = 4; i < 124; i += 8) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mx[j] = tc::max3(mx[j], s[i + j], s[i + j + 4]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[124 + j]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const bool grown = (top - m) * c > kRescale || m == -INFINITY;
+                if (it == begin) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, grown)) {
+                    // the products so far were complete before these scores were
+                    const float m_new = fmaxf(m, top);
+                    const float keep = m_new == -INFINITY ? 1.f : tc::exp2_fast((m - m_new) * c);
+                    m = m_new;
+                    l *= keep;
+#pragma unroll
+                    for (int i = 0; i < D; i += 16) {
+                        float x[16];
+                        tc::tmem_ld16_sync(to + i, x);
+                        uint32_t y[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(x[j] * keep);
+                        tc::tmem_st16(to + i, y);
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : m * c;
+                const tc::f32x2 c2 = tc::pack2(c, c), r2 = tc::pack2(-ref, -ref);
+                tc::f32x2 sum = 0;
+#pragma unroll
+                for (int i = 0; i < 128; i += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        float a, b;
+                        tc::unpack2(tc::fma2(tc::pack2(s[i + j], s[i + j + 1]), c2, r2), a, b);
+                        a = tc::exp2_fast(a);
+                        b = tc::exp2_fast(b);
+                        sum = tc::add2(sum, tc::pack2(a, b));
+                        pk[j / 2] = tc::bf16x2(a, b);
+                    }
+                    tc::tmem_st16(ts + i / 2, pk);
+                }
+                float sa, sb;
+                tc::unpack2(sum, sa, sb);
+                l += sa + sb;
+                tc::tmem_st_wait();
+                tc::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(p_full + w);
+            }
+            go = __all_sync(0xffffffffu, go && tc::mbar_wait(o_full, 0, abort, f.status, kErrO, f.spin));
+            if (go && !*abort) {
+                tc::tc_fence_after_sync();
+                const bool mine = row < t.seq_end;
+                const float inv = 1.f / l;
+                __nv_bfloat16 *out = f.o + ((size_t)row * f.p.Hq + h) * D;
+                float odd = 0.f;  // NaN if any value is not finite
+#pragma unroll
+                for (int i = 0; i < D; i += 32) {
+                    float x[32];
+                    tc::tmem_start(to + i, x);
+                    tc::tmem_ready(x);
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        x[j] *= inv;
+                        x[j + 1] *= inv;
+                        odd = fmaf(x[j], 0.f, fmaf(x[j + 1], 0.f, odd));
+                        pk[j / 2] = tc::bf16x2(x[j], x[j + 1]);
+                    }
+                    if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            *reinterpret_cast<uint4 *>(out + i + 2 * j) =
+                                make_uint4(pk[j], pk[j + 1], pk[j + 2], pk[j + 3]);
+                    }
+                }
+                if (mine && f.lse) f.lse[(size_t)row * f.p.Hq + h] = m * f.p.scale + logf(l);
+                __syncwarp();
+                unsigned bad = __ballot_sync(0xffffffffu, mine && !(odd == 0.f));
+                for (; bad; bad &= bad - 1)
+                    recompute_row<D>(f, row - lane + __ffs(bad) - 1, t.seq_start, h);
+            }
+            tc::tc_fence_before_sync();
+        }
+    }
+    __syncthreads();
+    if (warp == 8) {
+        tc::tc_fence_after_sync();
+        tc::tmem_relinquish();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch(const AttnProblem &p, void *o, float *lse, void *workspace, cudaStream_t st)
+{
+    char *ws = static_cast<char *>(workspace);
+    FwdParams f{};
+    f.p = p;
+    f.o = static_cast<__nv_bfloat16 *>(o);
+    f.lse = lse;
+    f.status = reinterpret_cast<int *>(ws);
+    const DebugKnobs dbg = debug_knobs();
+    f.spin = dbg.wait_limit ? dbg.wait_limit : tc::kSpinLimit;
+    f.starve = dbg.starve_carry;
+    if (!encode_attn_map(&f.q, p.q, p.Hq, D, p.tokens) ||
+        !encode_attn_map(&f.k, p.k, p.Hkv, D, p.tokens) ||
+        !encode_attn_map(&f.v, p.v, p.Hkv, D, p.tokens))
+        return cudaErrorInvalidValue;
+    if (p.cu_seqlens) {
+        f.tiles = reinterpret_cast<const AttnTile *>(
+            ws + attn_workspace_layout(p, kRows, false).tiles);
+        const cudaError_t e = launch_attn_plan(p, kRows, workspace, st);
+        if (e != cudaSuccess) return e;
+    }
+    const cudaError_t e = cudaFuncSetAttribute(
+        attn_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdShape<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    attn_fwd_kernel<D><<<(unsigned)(attn_tiles(p, kRows) * p.Hq), kThreads, FwdShape<D>::kBytes,
+                         st>>>(f);
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool encode_attn_map(CUtensorMap *tm, const void *base, int H, int D, long long tokens)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)kTileRows};
+    cuuint32_t estride[3] = {1, 1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+               box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+int attn_tc_fwd_rows() { return kRows; }
+
+cudaError_t launch_attn_tc_fwd(const AttnProblem &p, void *o, float *lse, void *workspace,
+                               cudaStream_t st)
+{
+    if (p.d == 32) return launch<32>(p, o, lse, workspace, st);
+    if (p.d == 64) return launch<64>(p, o, lse, workspace, st);
+    return launch<128>(p, o, lse, workspace, st);
+}
+
+}  // namespace kda

@@ -89,19 +89,18 @@ cudaError_t bwd(const AttnProblem &p, const void *o, const float *lse, const voi
 
 }  // namespace
 
-int attn_fwd_rows(const AttnProblem &) { return kRows; }
+int attn_fwd_rows(const AttnProblem &p)
+{
+    return p.dtype == KDA_DTYPE_BF16 ? attn_tc_fwd_rows() : kRows;
+}
 int attn_bwd_rows(const AttnProblem &) { return kRows; }
 
 cudaError_t launch_attn_fwd(const AttnProblem &p, void *o, float *lse, void *ws, cudaStream_t st)
 {
-    if (p.dtype == KDA_DTYPE_F32) {
-        if (p.d == 32) return fwd<float, 32>(p, o, lse, ws, st);
-        if (p.d == 64) return fwd<float, 64>(p, o, lse, ws, st);
-        return fwd<float, 128>(p, o, lse, ws, st);
-    }
-    if (p.d == 32) return fwd<__nv_bfloat16, 32>(p, o, lse, ws, st);
-    if (p.d == 64) return fwd<__nv_bfloat16, 64>(p, o, lse, ws, st);
-    return fwd<__nv_bfloat16, 128>(p, o, lse, ws, st);
+    if (p.dtype == KDA_DTYPE_BF16) return launch_attn_tc_fwd(p, o, lse, ws, st);
+    if (p.d == 32) return fwd<float, 32>(p, o, lse, ws, st);
+    if (p.d == 64) return fwd<float, 64>(p, o, lse, ws, st);
+    return fwd<float, 128>(p, o, lse, ws, st);
 }
 
 cudaError_t launch_attn_bwd(const AttnProblem &p, const void *o, const float *lse, const void *dO,
