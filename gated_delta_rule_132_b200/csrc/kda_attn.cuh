@@ -34,7 +34,7 @@ inline long long attn_tiles(const AttnProblem &p, int rows)
 
 // Workspace of a prompt call: the header (status word), the plan (varlen calls:
 // sanitised starts, longest-first order, tile offsets; the tile list) and, for the
-// backward, D_r = <dO_r, o_r>.
+// backward, per query head and token D_r = <dO_r, o_r> and then lse_r log2 e.
 struct AttnWorkspace {
     size_t starts, order, tiles, delta, total;
 };
@@ -48,7 +48,7 @@ inline AttnWorkspace attn_workspace_layout(const AttnProblem &p, int rows, bool 
     at = align_up(at, 16);
     w.tiles = at; at += sizeof(AttnTile) * (size_t)attn_tiles(p, rows);
     at = align_up(at, 256);
-    w.delta = at; if (bwd) at += sizeof(float) * (size_t)p.tokens * p.Hq;
+    w.delta = at; if (bwd) at += 2 * sizeof(float) * (size_t)p.tokens * p.Hq;
     w.total = align_up(at, 256);
     return w;
 }
@@ -67,8 +67,15 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, const void *o, const float *ls
 
 // The tensor-core path (bf16).
 int attn_tc_fwd_rows();
+int attn_tc_bwd_rows();
 cudaError_t launch_attn_tc_fwd(const AttnProblem &p, void *o, float *lse, void *workspace,
                                cudaStream_t st);
+cudaError_t launch_attn_tc_bwd(const AttnProblem &p, const void *o, const float *lse,
+                               const void *dO, void *gq, void *gk, void *gv, void *workspace,
+                               cudaStream_t st);
+// D_r = <dO_r, o_r> and lse_r log2 e of every token and query head.
+cudaError_t launch_attn_delta(const AttnProblem &p, const void *o, const float *lse,
+                              const void *dO, float *delta, float *lse2, cudaStream_t st);
 
 // A tree-attention call after host-side validation.
 struct TreeProblem {

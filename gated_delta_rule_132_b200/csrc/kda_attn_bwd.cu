@@ -1,0 +1,630 @@
+// kda_attn_bwd.cu — gradients of causal prompt attention on the tensor cores (bf16).
+//
+// Two kernels recompute P from q, k and lse: one CTA per (128 keys, kv head) sums
+// dK and dV over the query tiles behind it and the group's query heads, one CTA per
+// (128 queries, head) sums dQ over the key tiles before it. Each output is written by
+// one CTA in a fixed order, so results do not depend on timing and no fp32 gradient
+// is accumulated in memory; the price is that S and dO V^T are formed twice (7
+// products per tile pair instead of 5).
+//
+// In both, two products give S and dP in TMEM (transposed in the first kernel: a row
+// is a key); eight warps turn them into P and dS = P (dP - D) in registers, two
+// threads per row with 64 columns each, and write them in bf16 over S and dP, from
+// where the gradient products read them as their TMEM operand. scale is applied to
+// the finished sums.
+//
+// Rows whose result is not finite are computed again from the visible pairs alone, as
+// in the forward (0 times what a masked place holds may be NaN).
+#include "kda_attn_rows.cuh"
+#include "kda_attn_tc.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRegsCompute = 216, kRegsOther = 72;
+static_assert(256 * kRegsCompute + 128 * kRegsOther <= kThreads * 168, "register split");
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct BwdParams {
+    CUtensorMap q, k, v, dO;
+    AttnProblem p;
+    const AttnTile *tiles;  // null: uniform sequences
+    const float *lse, *lse2, *delta;
+    const __nv_bfloat16 *dO_raw;
+    __nv_bfloat16 *gq, *gk, *gv;
+    int *status;
+    uint32_t spin;
+    int starve;
+};
+
+// Shared memory: two tiles that stay (k, v or q, dO), and a ring of stages of the two
+// tiles that pass (q, dO with their rows' lse2 and D, or k, v).
+template <int D, bool kKeys>
+struct BwdShape {
+    // The first ring's tile is held to the end of its step and read at the next one's
+    // beginning: dQ has room for a third.
+    static constexpr int kStages = D == 128 ? 2 : 4, kStages0 = D == 128 && !kKeys ? 3 : kStages;
+    static constexpr uint32_t kTile = TileShape<D>::kBytes;
+    static constexpr uint32_t kStay = 0, kRing0 = 2 * kTile, kRing1 = kRing0 + kStages0 * kTile;
+    static constexpr uint32_t kStats = kRing1 + kStages * kTile;  // [stage][lse2, D][128]
+    static constexpr uint32_t kBars = kStats + (kKeys ? kStages * 1024 : 0);
+    static constexpr uint32_t kBytes = kBars + 256 + 1024;
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+enum : int { kErrStay = 111, kErrA, kErrB, kErrFree, kErrS, kErrDp, kErrP, kErrDs, kErrAcc,
+             kErrBwdDrain };
+
+struct Bars {
+    uint64_t *stay, *full0, *free0, *full1, *free1, *s_full, *dp_full, *p_full, *ds_full, *acc;
+    uint32_t *tmem_slot;
+    volatile int *abort;
+    uint32_t *bad;  // [4] rows to compute again
+    __device__ Bars(uint8_t *at)
+    {
+        constexpr int kMost = 4;  // stages
+        stay = reinterpret_cast<uint64_t *>(at);
+        full0 = stay + 1; free0 = full0 + kMost;
+        full1 = free0 + kMost; free1 = full1 + kMost;
+        s_full = free1 + kMost; dp_full = s_full + 2; p_full = dp_full + 1;
+        ds_full = p_full + 1; acc = ds_full + 1;
+        tmem_slot = reinterpret_cast<uint32_t *>(acc + 1);
+        abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+        bad = tmem_slot + 2;
+    }
+};
+
+__device__ __forceinline__ uint32_t start_cta(const Bars &b, int full0_count)
+{
+    const int warp = threadIdx.x >> 5;
+    if (warp == 8) tc::tmem_alloc(b.tmem_slot, 512);
+    if (threadIdx.x == 0) {
+        tc::mbar_init(b.stay, 1);
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(b.full0 + i, full0_count);
+            tc::mbar_init(b.free0 + i, 1);
+            tc::mbar_init(b.full1 + i, 1);
+            tc::mbar_init(b.free1 + i, 1);
+        }
+        tc::mbar_init(b.s_full, 1);
+        tc::mbar_init(b.s_full + 1, 1);
+        tc::mbar_init(b.dp_full, 1);
+        tc::mbar_init(b.p_full, 8);
+        tc::mbar_init(b.ds_full, 8);
+        tc::mbar_init(b.acc, 1);
+        *b.abort = 0;
+        for (int i = 0; i < 4; ++i) b.bad[i] = 0;
+        tc::fence_mbar_init();
+    }
+    tc::tc_fence_before_sync();
+    __syncthreads();
+    tc::tc_fence_after_sync();
+    return *b.tmem_slot;
+}
+
+__device__ __forceinline__ void end_cta(uint32_t tmem)
+{
+    tc::tc_fence_before_sync();
+    __syncthreads();
+    if (threadIdx.x >> 5 == 8) {
+        tc::tc_fence_after_sync();
+        tc::tmem_relinquish();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// 64 fp32 values of a row as bf16 over 32 columns.
+__device__ __forceinline__ void store_weights(uint32_t taddr, const float *x)
+{
+#pragma unroll
+    for (int i = 0; i < 64; i += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) pk[j] = tc::bf16x2(x[i + 2 * j], x[i + 2 * j + 1]);
+        tc::tmem_st16(taddr + i / 2, pk);
+    }
+}
+
+// A warp's share of a weights tile is in TMEM.
+__device__ __forceinline__ void weights_done(uint64_t *bar)
+{
+    tc::tmem_st_wait();
+    tc::tc_fence_before_sync();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+
+// Row `mine` of an accumulator [128 x D] times `by`, in bf16 to `out` (null: nowhere).
+// Returns whether all of it is finite.
+template <int D>
+__device__ __forceinline__ bool store_sums(uint32_t taddr, float by, __nv_bfloat16 *out)
+{
+    float odd = 0.f;
+#pragma unroll
+    for (int i = 0; i < D; i += 32) {
+        float x[32];
+        tc::tmem_start(taddr + i, x);
+        tc::tmem_ready(x);
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            x[j] *= by;
+            x[j + 1] *= by;
+            odd = fmaf(x[j], 0.f, fmaf(x[j + 1], 0.f, odd));
+            pk[j / 2] = tc::bf16x2(x[j], x[j + 1]);
+        }
+        if (out) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+                *reinterpret_cast<uint4 *>(out + i + 2 * j) =
+                    make_uint4(pk[j], pk[j + 1], pk[j + 2], pk[j + 3]);
+        }
+    }
+    return odd == 0.f;
+}
+
+// The rows that a thread of their own flagged, one warp each, after all stores. All eight
+// warps come here, also where the CTA has given up.
+template <typename F>
+__device__ __forceinline__ void redo_rows(const Bars &b, bool mine_bad, F redo)
+{
+    const int warp = threadIdx.x >> 5;  // 0..7, two warps per 32 rows
+    const unsigned bad = __ballot_sync(0xffffffffu, mine_bad);
+    if ((threadIdx.x & 31) == 0 && bad) atomicOr(b.bad + (warp & 3), bad);
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    unsigned todo = *const_cast<volatile uint32_t *>(b.bad + (warp & 3));
+    for (; todo; todo &= todo - 1) {
+        const int i = __ffs(todo) - 1;
+        if ((i & 1) == (warp >> 2)) redo((warp & 3) * 32 + i);
+    }
+}
+
+template <int D>
+__device__ __noinline__ void redo_dkv(const BwdParams &f, int col, int end, int hk)
+{
+    attn_row_dkv<__nv_bfloat16, D>(f.p, col, end, hk, f.lse, f.delta, f.dO_raw, f.gk, f.gv);
+}
+
+template <int D>
+__device__ __noinline__ void redo_dq(const BwdParams &f, int row, int start, int h)
+{
+    attn_row_dq<__nv_bfloat16, D>(f.p, row, start, h, f.lse, f.delta, f.dO_raw, f.gq);
+}
+
+// ---------------------------------------------------------------- dK and dV
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_constant__ BwdParams f)
+{
+    using S = BwdShape<D, true>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const Bars b(sm + S::kBars);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int hk = blockIdx.x % f.p.Hkv, G = f.p.Hq / f.p.Hkv;
+    AttnTile t = attn_tile(f.tiles, blockIdx.x / f.p.Hkv, kTileRows, f.p.B, f.p.T);
+    if (t.first >= t.seq_end) return;
+    if (!f.tiles && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
+    // the list begins with a sequence's last tile; here the first one has most work
+    const int count = (t.seq_end - t.seq_start + kTileRows - 1) / kTileRows;
+    const int tile = count - 1 - (t.first - t.seq_start) / kTileRows;
+    t.first = t.seq_start + tile * kTileRows;
+    const int per_head = count - tile, steps = per_head * G;  // step = (head, query tile)
+
+    const uint32_t tmem = start_cta(b, 1 + 32);
+    constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 256 + D;
+    const float *stats = reinterpret_cast<const float *>(sm + S::kStats);
+
+    if (warp >= 8) {
+        tc::fewer_registers<kRegsOther>();
+        if (warp == 9 && !f.starve) {
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(b.stay, 2 * S::kTile);
+                tc::load_tile<D>(sm + S::kStay, &f.k, hk, t.first, b.stay);
+                tc::load_tile<D>(sm + S::kStay + S::kTile, &f.v, hk, t.first, b.stay);
+            }
+            int it = 0;
+            for (; it < steps; ++it) {
+                const int st = it % S::kStages, use = it / S::kStages;
+                const int h = hk * G + it / per_head, token = t.first + it % per_head * kTileRows;
+                bool go = !use || (tc::mbar_wait(b.free0 + st, (use - 1) & 1, b.abort, f.status, kErrFree, f.spin) &&
+                                   tc::mbar_wait(b.free1 + st, (use - 1) & 1, b.abort, f.status, kErrFree, f.spin));
+                if (!__all_sync(0xffffffffu, go)) break;
+                float *to = reinterpret_cast<float *>(sm + S::kStats) + st * 256;
+                const size_t base = (size_t)h * f.p.tokens;
+#pragma unroll
+                for (int i = lane; i < kTileRows; i += 32) {
+                    const size_t at = base + min(token + i, (int)f.p.tokens - 1);
+                    tc::cp_async4(to + i, f.lse2 + at);
+                    tc::cp_async4(to + 128 + i, f.delta + at);
+                }
+                tc::cp_async_arrive(b.full0 + st);
+                if (lane == 0) {
+                    tc::mbar_arrive_expect_tx(b.full0 + st, S::kTile);
+                    tc::load_tile<D>(sm + S::kRing0 + st * S::kTile, &f.q, h, token, b.full0 + st);
+                    tc::mbar_arrive_expect_tx(b.full1 + st, S::kTile);
+                    tc::load_tile<D>(sm + S::kRing1 + st * S::kTile, &f.dO, h, token, b.full1 + st);
+                }
+                __syncwarp();
+            }
+            if (lane == 0) {  // whatever the other warps do, the copies land before the memory is let go
+                tc::mbar_drain(b.stay, 0, f.status, kErrBwdDrain);
+                for (int i = max(0, it - S::kStages); i < it; ++i) {
+                    tc::mbar_drain(b.full0 + i % S::kStages, (i / S::kStages) & 1, f.status, kErrBwdDrain);
+                    tc::mbar_drain(b.full1 + i % S::kStages, (i / S::kStages) & 1, f.status, kErrBwdDrain);
+                }
+            }
+        }
+        if (warp == 8 && lane == 0) {
+            const uint32_t k = tc::smem_u32(sm + S::kStay), v = k + S::kTile;
+            const uint32_t q = tc::smem_u32(sm + S::kRing0), dO = tc::smem_u32(sm + S::kRing1);
+            auto wait = [&](uint64_t *bar, int n, int code) {
+                return tc::mbar_wait(bar, n & 1, b.abort, f.status, code, f.spin);
+            };
+            auto s_step = [&](int it) {
+                const int st = it % S::kStages;
+                if (!wait(b.full0 + st, it / S::kStages, kErrA)) return false;
+                tc::mma_rows_rows<D>(tmem + kS, k, q + st * S::kTile);
+                tc::mma_commit(b.s_full);
+                return true;
+            };
+            auto dp_step = [&](int it) {
+                const int st = it % S::kStages;
+                if (!wait(b.full1 + st, it / S::kStages, kErrB)) return false;
+                tc::mma_rows_rows<D>(tmem + kDp, v, dO + st * S::kTile);
+                tc::mma_commit(b.dp_full);
+                return true;
+            };
+            bool go = wait(b.stay, 0, kErrStay) && s_step(0) && dp_step(0);
+            for (int it = 0; it < steps && go; ++it) {
+                const int st = it % S::kStages;
+                go = wait(b.p_full, it, kErrP);
+                if (!go) break;
+                tc::tc_fence_after_sync();
+                tc::mma_weights_rows<D, 64>(tmem + kDv, tmem + kS, dO + st * S::kTile, it > 0);
+                tc::mma_commit(b.free1 + st);
+                if (it + 1 < steps) go = s_step(it + 1);
+                if (!go) break;
+                go = wait(b.ds_full, it, kErrDs);
+                if (!go) break;
+                tc::tc_fence_after_sync();
+                tc::mma_weights_rows<D, 64>(tmem + kDk, tmem + kDp, q + st * S::kTile, it > 0);
+                tc::mma_commit(b.free0 + st);
+                if (it + 1 < steps) go = dp_step(it + 1);
+            }
+            tc::mma_commit(b.acc);
+            tc::mbar_drain(b.acc, 0, f.status, kErrBwdDrain);
+        }
+    } else {
+        tc::more_registers<kRegsCompute>();
+        const int half = warp >> 2, in_tile = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t ts = tmem + lanes + kS + half * 64, td = tmem + lanes + kDp + half * 64;
+        const float c = f.p.scale * kLog2e;
+        const tc::f32x2 c2 = tc::pack2(c, c);
+        bool go = true;
+        for (int it = 0; it < steps; ++it) {
+            const int st = it % S::kStages, i0 = it % per_head;
+            const float *lse2 = stats + st * 256 + half * 64, *del = lse2 + 128;
+            go = __all_sync(0xffffffffu,
+                            tc::mbar_wait(b.s_full, it & 1, b.abort, f.status, kErrS, f.spin) &&
+                            tc::mbar_wait(b.full0 + st, (it / S::kStages) & 1, b.abort, f.status, kErrA, f.spin));
+            if (!go) break;
+            tc::tc_fence_after_sync();
+            float x[64];
+            tc::tmem_start(ts, x);
+            tc::tmem_start(ts + 32, x + 32);
+            tc::tmem_ready(x);
+            tc::tmem_ready(x + 32);
+#pragma unroll
+            for (int j = 0; j < 64; j += 4) {
+                const float4 z = *reinterpret_cast<const float4 *>(lse2 + j);
+                tc::unpack2(tc::fma2(tc::pack2(x[j], x[j + 1]), c2, tc::pack2(-z.x, -z.y)), x[j], x[j + 1]);
+                tc::unpack2(tc::fma2(tc::pack2(x[j + 2], x[j + 3]), c2, tc::pack2(-z.z, -z.w)), x[j + 2], x[j + 3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[j + e] = tc::exp2_fast(x[j + e]);
+            }
+            // queries before the key, or behind the sequence
+            const int behind = t.seq_end - (t.first + i0 * kTileRows) - half * 64;
+            const int before = i0 == 0 ? in_tile - half * 64 : 0;
+            if (i0 == 0 || behind < 64) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) x[j] = j >= before && j < behind ? x[j] : 0.f;
+            }
+            store_weights(ts, x);
+            weights_done(b.p_full);
+            go = __all_sync(0xffffffffu, tc::mbar_wait(b.dp_full, it & 1, b.abort, f.status, kErrDp, f.spin));
+            if (!go) break;
+            tc::tc_fence_after_sync();
+            float y[64];
+            tc::tmem_start(td, y);
+            tc::tmem_start(td + 32, y + 32);
+            tc::tmem_ready(y);
+            tc::tmem_ready(y + 32);
+#pragma unroll
+            for (int j = 0; j < 64; j += 4) {
+                const float4 z = *reinterpret_cast<const float4 *>(del + j);
+                tc::unpack2(tc::mul2(tc::pack2(x[j], x[j + 1]),
+                                     tc::add2(tc::pack2(y[j], y[j + 1]), tc::pack2(-z.x, -z.y))), x[j], x[j + 1]);
+                tc::unpack2(tc::mul2(tc::pack2(x[j + 2], x[j + 3]),
+                                     tc::add2(tc::pack2(y[j + 2], y[j + 3]), tc::pack2(-z.z, -z.w))),
+                            x[j + 2], x[j + 3]);
+            }
+            store_weights(td, x);
+            weights_done(b.ds_full);
+        }
+        go = __all_sync(0xffffffffu, go && tc::mbar_wait(b.acc, 0, b.abort, f.status, kErrAcc, f.spin));
+        const int col = t.first + in_tile;
+        bool bad = false;
+        if (go && !*b.abort) {
+            tc::tc_fence_after_sync();
+            // the first four warps write dV, the others dK
+            const bool mine = col < t.seq_end;
+            __nv_bfloat16 *out = (half ? f.gk : f.gv) + ((size_t)col * f.p.Hkv + hk) * D;
+            bad = !store_sums<D>(tmem + lanes + (half ? kDk : kDv), half ? f.p.scale : 1.f,
+                                 mine ? out : nullptr) && mine;
+        }
+        redo_rows(b, bad, [&](int i) { redo_dkv<D>(f, t.first + i, t.seq_end, hk); });
+    }
+    end_cta(tmem);
+}
+
+// ---------------------------------------------------------------- dQ
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_constant__ BwdParams f)
+{
+    using S = BwdShape<D, false>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const Bars b(sm + S::kBars);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x % f.p.Hq;
+    const AttnTile t = attn_tile(f.tiles, blockIdx.x / f.p.Hq, kTileRows, f.p.B, f.p.T);
+    if (t.first >= t.seq_end) return;
+    const int last = (t.first - t.seq_start) / kTileRows, steps = last + 1;  // key tiles, diagonal first
+
+    const uint32_t tmem = start_cta(b, 1);
+    constexpr uint32_t kS = 0, kDp = 256, kDq = 384;  // two score tiles in turn
+
+    if (warp >= 8) {
+        tc::fewer_registers<kRegsOther>();
+        if (warp == 9 && lane == 0 && !f.starve) {
+            const int hk = h / (f.p.Hq / f.p.Hkv);
+            tc::mbar_arrive_expect_tx(b.stay, 2 * S::kTile);
+            tc::load_tile<D>(sm + S::kStay, &f.q, h, t.first, b.stay);
+            tc::load_tile<D>(sm + S::kStay + S::kTile, &f.dO, h, t.first, b.stay);
+            int it = 0;
+            for (; it < steps; ++it) {
+                const int st0 = it % S::kStages0, use0 = it / S::kStages0;
+                const int st = it % S::kStages, use = it / S::kStages;
+                const int token = t.seq_start + (last - it) * kTileRows;
+                if (use0 && !tc::mbar_wait(b.free0 + st0, (use0 - 1) & 1, b.abort, f.status, kErrFree, f.spin)) break;
+                tc::mbar_arrive_expect_tx(b.full0 + st0, S::kTile);
+                tc::load_tile<D>(sm + S::kRing0 + st0 * S::kTile, &f.k, hk, token, b.full0 + st0);
+                if (use && !tc::mbar_wait(b.free1 + st, (use - 1) & 1, b.abort, f.status, kErrFree, f.spin)) {
+                    tc::mbar_drain(b.full0 + st0, use0 & 1, f.status, kErrBwdDrain);
+                    break;
+                }
+                tc::mbar_arrive_expect_tx(b.full1 + st, S::kTile);
+                tc::load_tile<D>(sm + S::kRing1 + st * S::kTile, &f.v, hk, token, b.full1 + st);
+            }
+            tc::mbar_drain(b.stay, 0, f.status, kErrBwdDrain);
+            for (int i = max(0, it - S::kStages0); i < it; ++i)
+                tc::mbar_drain(b.full0 + i % S::kStages0, (i / S::kStages0) & 1, f.status, kErrBwdDrain);
+            for (int i = max(0, it - S::kStages); i < it; ++i)
+                tc::mbar_drain(b.full1 + i % S::kStages, (i / S::kStages) & 1, f.status, kErrBwdDrain);
+        }
+        if (warp == 8 && lane == 0) {
+            const uint32_t q = tc::smem_u32(sm + S::kStay), dO = q + S::kTile;
+            const uint32_t k = tc::smem_u32(sm + S::kRing0), v = tc::smem_u32(sm + S::kRing1);
+            auto wait = [&](uint64_t *bar, int n, int code) {
+                return tc::mbar_wait(bar, n & 1, b.abort, f.status, code, f.spin);
+            };
+            auto s_step = [&](int it) {
+                const int st = it % S::kStages0;
+                if (!wait(b.full0 + st, it / S::kStages0, kErrA)) return false;
+                tc::mma_rows_rows<D>(tmem + kS + (it & 1) * 128, q, k + st * S::kTile);
+                tc::mma_commit(b.s_full + (it & 1));
+                return true;
+            };
+            auto dp_step = [&](int it) {
+                const int st = it % S::kStages;
+                if (!wait(b.full1 + st, it / S::kStages, kErrB)) return false;
+                tc::mma_rows_rows<D>(tmem + kDp, dO, v + st * S::kTile);
+                tc::mma_commit(b.dp_full);
+                tc::mma_commit(b.free1 + st);
+                return true;
+            };
+            bool go = wait(b.stay, 0, kErrStay) && s_step(0) && dp_step(0) && (steps < 2 || s_step(1));
+            for (int it = 0; it < steps && go; ++it) {
+                const int st = it % S::kStages0;
+                go = wait(b.ds_full, it, kErrDs);
+                if (!go) break;
+                tc::tc_fence_after_sync();
+                tc::mma_weights_rows<D, 64>(tmem + kDq, tmem + kDp, k + st * S::kTile, it > 0);
+                tc::mma_commit(b.free0 + st);
+                if (it + 1 < steps) go = dp_step(it + 1);
+                if (go && it + 2 < steps) go = s_step(it + 2);
+            }
+            tc::mma_commit(b.acc);
+            tc::mbar_drain(b.acc, 0, f.status, kErrBwdDrain);
+        }
+    } else {
+        tc::more_registers<kRegsCompute>();
+        const int half = warp >> 2, in_tile = threadIdx.x & 127, row = t.first + in_tile;
+        const bool mine = row < t.seq_end;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t ts = tmem + lanes + kS + half * 64, td = tmem + lanes + kDp + half * 64;
+        const float c = f.p.scale * kLog2e;
+        const size_t at = (size_t)h * f.p.tokens + min(row, (int)f.p.tokens - 1);
+        const float z = f.lse2[at], del = f.delta[at];
+        const tc::f32x2 c2 = tc::pack2(c, c), z2 = tc::pack2(-z, -z), d2 = tc::pack2(-del, -del);
+        bool go = true;
+        for (int it = 0; it < steps; ++it) {
+            go = __all_sync(0xffffffffu, tc::mbar_wait(b.s_full + (it & 1), (it >> 1) & 1, b.abort, f.status,
+                                                       kErrS, f.spin));
+            if (!go) break;
+            tc::tc_fence_after_sync();
+            float x[64];
+            tc::tmem_start(ts + (it & 1) * 128, x);
+            tc::tmem_start(ts + (it & 1) * 128 + 32, x + 32);
+            tc::tmem_ready(x);
+            tc::tmem_ready(x + 32);
+#pragma unroll
+            for (int j = 0; j < 64; j += 2) {
+                tc::unpack2(tc::fma2(tc::pack2(x[j], x[j + 1]), c2, z2), x[j], x[j + 1]);
+                x[j] = tc::exp2_fast(x[j]);
+                x[j + 1] = tc::exp2_fast(x[j + 1]);
+            }
+            if (it == 0) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) x[j] = j + half * 64 <= in_tile ? x[j] : 0.f;
+            }
+            go = __all_sync(0xffffffffu, tc::mbar_wait(b.dp_full, it & 1, b.abort, f.status, kErrDp, f.spin));
+            if (!go) break;
+            tc::tc_fence_after_sync();
+            float y[64];
+            tc::tmem_start(td, y);
+            tc::tmem_start(td + 32, y + 32);
+            tc::tmem_ready(y);
+            tc::tmem_ready(y + 32);
+#pragma unroll
+            for (int j = 0; j < 64; j += 2)
+                tc::unpack2(tc::mul2(tc::pack2(x[j], x[j + 1]), tc::add2(tc::pack2(y[j], y[j + 1]), d2)),
+                            x[j], x[j + 1]);
+            store_weights(td, x);
+            weights_done(b.ds_full);
+        }
+        go = __all_sync(0xffffffffu, go && tc::mbar_wait(b.acc, 0, b.abort, f.status, kErrAcc, f.spin));
+        bool bad = false;
+        if (go && !*b.abort) {
+            tc::tc_fence_after_sync();
+            // each half of the warps writes half of the row's channels
+            __nv_bfloat16 *out = f.gq + ((size_t)row * f.p.Hq + h) * D;
+            constexpr int kPart = D == 32 ? 32 : D / 2;
+            if (D > 32 || half == 0)
+                bad = !store_sums<kPart>(tmem + lanes + kDq + half * kPart, f.p.scale,
+                                         mine ? out + half * kPart : nullptr) && mine;
+        }
+        redo_rows(b, bad, [&](int i) { redo_dq<D>(f, t.first + i, t.seq_start, h); });
+    }
+    end_cta(tmem);
+}
+
+// ---------------------------------------------------------------- D and lse log2 e
+// D / 8 threads (or D / 4, fp32) per row, 16 bytes each.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+attn_delta_kernel(const T *o, const float *lse, const T *dO, long long tokens, int Hq,
+                  float *delta, float *lse2)
+{
+    constexpr int kPer = 16 / sizeof(T), kLanes = D / kPer;
+    const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
+    const int part = threadIdx.x % kLanes;
+    const bool in = row < tokens * Hq;
+    float s = 0.f;
+    if (in) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(o) + row * kLanes + part);
+        const uint4 g = __ldg(reinterpret_cast<const uint4 *>(dO) + row * kLanes + part);
+        const T *x = reinterpret_cast<const T *>(&a), *y = reinterpret_cast<const T *>(&g);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) s = fmaf(to_f32(x[i]), to_f32(y[i]), s);
+    }
+#pragma unroll
+    for (int m = kLanes / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (in && part == 0) {
+        const long long at = row % Hq * tokens + row / Hq;
+        delta[at] = s;
+        lse2[at] = lse[row] * kLog2e;
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_delta(const AttnProblem &p, const void *o, const float *lse, const void *dO,
+                         float *delta, float *lse2, cudaStream_t st)
+{
+    constexpr int kLanes = D * sizeof(T) / 16;
+    const long long threads = p.tokens * p.Hq * kLanes;
+    attn_delta_kernel<T, D><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(
+        static_cast<const T *>(o), lse, static_cast<const T *>(dO), p.tokens, p.Hq, delta, lse2);
+    note_launch();
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch(const AttnProblem &p, const void *o, const float *lse, const void *dO,
+                   void *gq, void *gk, void *gv, void *workspace, cudaStream_t st)
+{
+    char *ws = static_cast<char *>(workspace);
+    const AttnWorkspace w = attn_workspace_layout(p, kTileRows, true);
+    BwdParams f{};
+    f.p = p;
+    float *delta = reinterpret_cast<float *>(ws + w.delta);
+    f.delta = delta;
+    f.lse2 = delta + (size_t)p.tokens * p.Hq;
+    f.lse = lse;
+    f.dO_raw = static_cast<const __nv_bfloat16 *>(dO);
+    f.gq = static_cast<__nv_bfloat16 *>(gq);
+    f.gk = static_cast<__nv_bfloat16 *>(gk);
+    f.gv = static_cast<__nv_bfloat16 *>(gv);
+    f.status = reinterpret_cast<int *>(ws);
+    const DebugKnobs dbg = debug_knobs();
+    f.spin = dbg.wait_limit ? dbg.wait_limit : tc::kSpinLimit;
+    f.starve = dbg.starve_carry;
+    if (!encode_attn_map(&f.q, p.q, p.Hq, D, p.tokens) ||
+        !encode_attn_map(&f.k, p.k, p.Hkv, D, p.tokens) ||
+        !encode_attn_map(&f.v, p.v, p.Hkv, D, p.tokens) ||
+        !encode_attn_map(&f.dO, dO, p.Hq, D, p.tokens))
+        return cudaErrorInvalidValue;
+    cudaError_t e;
+    if (p.cu_seqlens) {
+        f.tiles = reinterpret_cast<const AttnTile *>(ws + w.tiles);
+        if ((e = launch_attn_plan(p, kTileRows, workspace, st)) != cudaSuccess) return e;
+    }
+    e = launch_attn_delta(p, o, lse, dO, delta, delta + (size_t)p.tokens * p.Hq, st);
+    if (e != cudaSuccess) return e;
+    const unsigned tiles = (unsigned)attn_tiles(p, kTileRows);
+    constexpr uint32_t dkv_smem = BwdShape<D, true>::kBytes, dq_smem = BwdShape<D, false>::kBytes;
+    e = cudaFuncSetAttribute(attn_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             dkv_smem);
+    if (e != cudaSuccess) return e;
+    attn_dkv_kernel<D><<<tiles * p.Hkv, kThreads, dkv_smem, st>>>(f);
+    note_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(attn_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             dq_smem);
+    if (e != cudaSuccess) return e;
+    attn_dq_kernel<D><<<tiles * p.Hq, kThreads, dq_smem, st>>>(f);
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int attn_tc_bwd_rows() { return kTileRows; }
+
+cudaError_t launch_attn_delta(const AttnProblem &p, const void *o, const float *lse,
+                              const void *dO, float *delta, float *lse2, cudaStream_t st)
+{
+    if (p.dtype == KDA_DTYPE_F32) {
+        if (p.d == 32) return launch_delta<float, 32>(p, o, lse, dO, delta, lse2, st);
+        if (p.d == 64) return launch_delta<float, 64>(p, o, lse, dO, delta, lse2, st);
+        return launch_delta<float, 128>(p, o, lse, dO, delta, lse2, st);
+    }
+    if (p.d == 32) return launch_delta<__nv_bfloat16, 32>(p, o, lse, dO, delta, lse2, st);
+    if (p.d == 64) return launch_delta<__nv_bfloat16, 64>(p, o, lse, dO, delta, lse2, st);
+    return launch_delta<__nv_bfloat16, 128>(p, o, lse, dO, delta, lse2, st);
+}
+
+cudaError_t launch_attn_tc_bwd(const AttnProblem &p, const void *o, const float *lse,
+                               const void *dO, void *gq, void *gk, void *gv, void *workspace,
+                               cudaStream_t st)
+{
+    if (p.d == 32) return launch<32>(p, o, lse, dO, gq, gk, gv, workspace, st);
+    if (p.d == 64) return launch<64>(p, o, lse, dO, gq, gk, gv, workspace, st);
+    return launch<128>(p, o, lse, dO, gq, gk, gv, workspace, st);
+}
+
+}  // namespace kda

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                      tc::mbar_wait(p_full + w, (it - begin) & 1, abort, f.status, kErrP, f.spin);
                 if (!go) return;
                 tc::tc_fence_after_sync();
-                tc::mma_weights_rows<D>(tmem + S::kTmemO + w * D, tmem + S::kTmemS + w * 128,
+                tc::mma_weights_rows<D, 32>(tmem + S::kTmemO + w * D, tmem + S::kTmemS + w * 128,
                                         v + st * S::kTile, it > begin);
             };
             for (int it = 0; it < steps && go; ++it) {

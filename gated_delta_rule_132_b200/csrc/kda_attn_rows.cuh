@@ -92,7 +92,7 @@ __device__ void attn_row_fwd(const AttnProblem &p, int row, int start, int h, T 
     if (lse && (threadIdx.x & 31) == 0) lse[(size_t)row * p.Hq + h] = sm.m + logf(sm.l);
 }
 
-// Query gradient of one row.
+// Query gradient of one row. delta [Hq, tokens]: D_r = <dO_r, o_r>.
 template <typename T, int D>
 __device__ void attn_row_dq(const AttnProblem &p, int row, int start, int h, const float *lse,
                             const float *delta, const T *dO, T *gq)
@@ -106,7 +106,7 @@ __device__ void attn_row_dq(const AttnProblem &p, int row, int start, int h, con
     float q[V], g[V], x[V], y[V], acc[V] = {};
     load_row<T, D>(static_cast<const T *>(p.q) + at, q);
     load_row<T, D>(dO + at, g);
-    const float z = lse[(size_t)row * p.Hq + h], del = delta[(size_t)row * p.Hq + h];
+    const float z = lse[(size_t)row * p.Hq + h], del = delta[(size_t)h * p.tokens + row];
     for (int c = start; c <= row; ++c) {
         load_row<T, D>(k + c * kv, x);
         load_row<T, D>(v + c * kv, y);
@@ -136,7 +136,7 @@ __device__ void attn_row_dkv(const AttnProblem &p, int col, int seq_end, int hk,
             load_row<T, D>(q + i0 * D, x);
             load_row<T, D>(dO + i0 * D, g);
             const float pr = expf(row_dot(x, k) * p.scale - lse[i0]);
-            const float ds = pr * (row_dot(g, v) - delta[i0]) * p.scale;
+            const float ds = pr * (row_dot(g, v) - delta[(size_t)h * p.tokens + r]) * p.scale;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 ak[i] = fmaf(ds, x[i], ak[i]);

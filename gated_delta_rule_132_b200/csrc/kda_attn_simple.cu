@@ -20,21 +20,6 @@ rows_fwd_kernel(AttnProblem p, const AttnTile *tiles, T *o, float *lse)
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-rows_delta_kernel(AttnProblem p, const T *o, const T *dO, float *delta)
-{
-    const size_t rows = (size_t)p.tokens * p.Hq;
-    for (size_t r = (size_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < rows;
-         r += (size_t)gridDim.x * (kThreads / 32)) {
-        float a[D / 32], b[D / 32];
-        load_row<T, D>(o + r * D, a);
-        load_row<T, D>(dO + r * D, b);
-        const float s = row_dot(a, b);
-        if ((threadIdx.x & 31) == 0) delta[r] = s;
-    }
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
 rows_bwd_kernel(AttnProblem p, const AttnTile *tiles, const float *lse, const float *delta,
                 const T *dO, T *gq, T *gk, T *gv)
 {
@@ -74,10 +59,7 @@ cudaError_t bwd(const AttnProblem &p, const void *o, const float *lse, const voi
     float *delta = reinterpret_cast<float *>(ws + w.delta);
     cudaError_t e = launch_attn_plan(p, kRows, workspace, st);
     if (e != cudaSuccess) return e;
-    rows_delta_kernel<T, D><<<1184, kThreads, 0, st>>>(p, static_cast<const T *>(o),
-                                                       static_cast<const T *>(dO), delta);
-    note_launch();
-    e = cudaGetLastError();
+    e = launch_attn_delta(p, o, lse, dO, delta, delta + (size_t)p.tokens * p.Hq, st);
     if (e != cudaSuccess) return e;
     rows_bwd_kernel<T, D>
         <<<(unsigned)(attn_tiles(p, kRows) * (p.Hq + p.Hkv)), kThreads, 0, st>>>(
@@ -93,7 +75,10 @@ int attn_fwd_rows(const AttnProblem &p)
 {
     return p.dtype == KDA_DTYPE_BF16 ? attn_tc_fwd_rows() : kRows;
 }
-int attn_bwd_rows(const AttnProblem &) { return kRows; }
+int attn_bwd_rows(const AttnProblem &p)
+{
+    return p.dtype == KDA_DTYPE_BF16 ? attn_tc_bwd_rows() : kRows;
+}
 
 cudaError_t launch_attn_fwd(const AttnProblem &p, void *o, float *lse, void *ws, cudaStream_t st)
 {
@@ -106,14 +91,11 @@ cudaError_t launch_attn_fwd(const AttnProblem &p, void *o, float *lse, void *ws,
 cudaError_t launch_attn_bwd(const AttnProblem &p, const void *o, const float *lse, const void *dO,
                             void *gq, void *gk, void *gv, void *ws, cudaStream_t st)
 {
-    if (p.dtype == KDA_DTYPE_F32) {
-        if (p.d == 32) return bwd<float, 32>(p, o, lse, dO, gq, gk, gv, ws, st);
-        if (p.d == 64) return bwd<float, 64>(p, o, lse, dO, gq, gk, gv, ws, st);
-        return bwd<float, 128>(p, o, lse, dO, gq, gk, gv, ws, st);
-    }
-    if (p.d == 32) return bwd<__nv_bfloat16, 32>(p, o, lse, dO, gq, gk, gv, ws, st);
-    if (p.d == 64) return bwd<__nv_bfloat16, 64>(p, o, lse, dO, gq, gk, gv, ws, st);
-    return bwd<__nv_bfloat16, 128>(p, o, lse, dO, gq, gk, gv, ws, st);
+    if (p.dtype == KDA_DTYPE_BF16)
+        return launch_attn_tc_bwd(p, o, lse, dO, gq, gk, gv, ws, st);
+    if (p.d == 32) return bwd<float, 32>(p, o, lse, dO, gq, gk, gv, ws, st);
+    if (p.d == 64) return bwd<float, 64>(p, o, lse, dO, gq, gk, gv, ws, st);
+    return bwd<float, 128>(p, o, lse, dO, gq, gk, gv, ws, st);
 }
 
 }  // namespace kda

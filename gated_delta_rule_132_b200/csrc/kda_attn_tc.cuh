@@ -88,16 +88,16 @@ __device__ __forceinline__ void mma_rows_rows(uint32_t acc, uint32_t x, uint32_t
     }
 }
 
-// acc[128 x D] (+)= W Y over 128 tokens: W [128 x 128] bf16 in TMEM (64 columns), Y a
-// tile read along its tokens.
-template <int D>
+// acc[128 x D] (+)= W Y over 128 tokens: W [128 x 128] bf16 in TMEM, 32 columns for the
+// first 64 tokens and 32 more that begin kHalf columns on; Y a tile read along its tokens.
+template <int D, int kHalf>
 __device__ __forceinline__ void mma_weights_rows(uint32_t acc, uint32_t w, uint32_t y,
                                                  bool accumulate)
 {
     const uint64_t b = smem_desc(y, kBlockBytes, 1024);
 #pragma unroll
     for (int k = 0; k < kTileRows / 16; ++k)
-        mma_bf16_ta(acc, w + k * 8, b + ((k * 2048) >> 4), idesc_bf16(128, D, 0, 1),
+        mma_bf16_ta(acc, w + (k >> 2) * kHalf + (k & 3) * 8, b + ((k * 2048) >> 4), idesc_bf16(128, D, 0, 1),
                     accumulate || k > 0);
 }
 
@@ -186,6 +186,17 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// 4-byte asynchronous copy global -> shared, and an arrival on `bar` once this thread's
+// copies so far have landed (the barrier counts it like any arrival).
+__device__ __forceinline__ void cp_async4(void *dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c)
