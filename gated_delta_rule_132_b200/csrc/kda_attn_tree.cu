@@ -1,17 +1,36 @@
-// kda_attn_tree.cu — attention of a tree of drafted tokens over a paged cache, one
-// warp per (sequence, token, head).
+// kda_attn_tree.cu — attention of a tree of drafted tokens (or one token) over a
+// paged cache.
+//
+// The R tokens of a sequence times the G query heads that share a key/value head are
+// the rows of one problem over that head's keys, so the cache is read once for all of
+// them. One token of G heads reads 4 D bytes per key for 4 D G flops: HBM bounds the
+// call until the rows number about a hundred.
+//
+// A CTA owns a tile of rows and a chunk of consecutive keys of one (sequence, kv
+// head); chunks are what keeps all SMs busy when there are few sequences or their
+// lengths differ. Tiles of 64 keys (32 in fp32) come in by 16-byte asynchronous
+// copies, a table lookup per key, three stages deep; a key without a page, or behind
+// the sequence, is filled with zeros and masked. Softmax statistics run in fp32 over
+// the chunk; a second kernel joins the chunks of rows that have several, in order.
+//
+// Only drafted tokens are masked for some rows and not for others, so only their
+// values can reach a row through 0 * inf: rows whose result is not finite are computed
+// again from the keys they see.
+#include <algorithm>
+
 #include "kda_attn_rows.cuh"
+#include "tc_primitives.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
 
 // The drafted tokens that token i attends to, as bits: itself and its ancestors; 0
 // where it, or one of them, has a parent that is neither -1 nor an earlier token.
 __device__ __forceinline__ unsigned long long ancestors(const int32_t *parents, int i)
 {
-    if (!parents) return (2ull << i) - 1;  // a chain
     unsigned long long seen = 0;
     int j = i;
     while (j >= 0) {
@@ -23,28 +42,74 @@ __device__ __forceinline__ unsigned long long ancestors(const int32_t *parents, 
     return seen;
 }
 
+struct TreeParams {
+    TreeProblem p;
+    int rows;       // R * G
+    int row_tiles;  // CTAs that share a chunk's keys
+    int chunks;     // most chunks of a sequence
+    float *part_o;  // [n, hk, chunk, row, D]: sums over e^(s - m) v
+    float2 *part_ml;
+};
+
+// Where key `pos` of a row of the table is, in elements; -1 where it has no page.
+__device__ __forceinline__ long long key_at(const TreeProblem &p, const int32_t *row, int pos,
+                                            int hk)
+{
+    const int id = __ldg(row + (pos >> p.page_shift));
+    if ((unsigned)id >= (unsigned)p.P) return -1;
+    return (((((long long)id * p.Hkv + hk) << p.page_shift) + (pos & ((1 << p.page_shift) - 1)))) * p.d;
+}
+
+__device__ __forceinline__ int ctx_of(const TreeProblem &p, int n)
+{
+    return min(max(p.ctx_lens[n], 0), p.M << p.page_shift);
+}
+
+__device__ __forceinline__ int end_of(const TreeProblem &p, int n)
+{
+    return min(ctx_of(p, n) + p.R, p.M << p.page_shift);
+}
+
+// Keys per chunk of a sequence of `end` keys. Lengths are known on the device only, so
+// every warp adds them up: chunks are to be small enough for about six CTAs per
+// resident place (two per SM) and no smaller than a tile, nor, as a chunk's fixed cost
+// is about a tile's, need they be below 2048 keys to balance the SMs.
+__device__ __forceinline__ int chunk_of(const TreeParams &f, int end)
+{
+    if (f.chunks == 1) return INT32_MAX;
+    constexpr int kCounted = 1024;  // sequences whose lengths are added up
+    int target = 2048;
+    if (f.p.N <= kCounted) {
+        long long total = 0;
+        for (int n = threadIdx.x & 31; n < f.p.N; n += 32) total += end_of(f.p, n);
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+        total = total * f.p.Hkv * f.row_tiles / (148 * 2 * 6);
+        target = (int)min(max(total, 64ll), 2048ll);
+    }
+    const int count = max(1, min(f.chunks, (end + target - 1) / target));
+    return ((end + count - 1) / count + 63) / 64 * 64;
+}
+
+// One row from the keys it sees alone: one warp.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) tree_rows_kernel(TreeProblem p)
+__device__ __noinline__ void tree_row(const TreeProblem &p, int n, int i, int h)
 {
     constexpr int V = D / 32;
-    const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (unit >= (long long)p.N * p.R * p.Hq) return;
-    const int h = (int)(unit % p.Hq), i = (int)(unit / p.Hq % p.R), n = (int)(unit / p.Hq / p.R);
-    const int hk = h / (p.Hq / p.Hkv), page = 1 << p.page_shift;
     const int32_t *row = p.table + (size_t)n * p.M;
-    const int limit = p.M << p.page_shift;
-    const int ctx = min(max(p.ctx_lens[n], 0), limit);
-    const unsigned long long seen = ancestors(p.parents ? p.parents + (size_t)n * p.R : nullptr, i);
+    const int ctx = ctx_of(p, n), end = end_of(p, n);
+    const unsigned long long seen =
+        p.parents ? ancestors(p.parents + (size_t)n * p.R, i) : (2ull << i) - 1;
+    const size_t unit = ((size_t)n * p.R + i) * p.Hq + h;
+    const int hk = h / (p.Hq / p.Hkv);
     float q[V], x[V], y[V];
-    load_row<T, D>(static_cast<const T *>(p.q) + (size_t)unit * D, q);
+    load_row<T, D>(static_cast<const T *>(p.q) + unit * D, q);
     RowSoftmax<V> sm;
     bool any = false;
-    const int end = seen ? min(ctx + p.R, limit) : 0;
-    for (int c = 0; c < end; ++c) {
+    for (int c = 0; c < (seen ? end : 0); ++c) {
         if (c >= ctx && !(seen >> (c - ctx) & 1)) continue;
-        const int id = row[c >> p.page_shift];
-        if (id < 0 || id >= p.P) continue;
-        const size_t at = (((size_t)id * p.Hkv + hk) * page + (c & (page - 1))) * D;
+        const long long at = key_at(p, row, c, hk);
+        if (at < 0) continue;
         load_row<T, D>(static_cast<const T *>(p.k_pages) + at, x);
         load_row<T, D>(static_cast<const T *>(p.v_pages) + at, y);
         sm.add(row_dot(q, x) * p.scale, y);
@@ -52,33 +117,585 @@ __global__ void __launch_bounds__(kThreads) tree_rows_kernel(TreeProblem p)
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) y[e] = any ? sm.acc[e] / sm.l : 0.f;
-    store_row<T, D>(static_cast<T *>(p.o) + (size_t)unit * D, y);
+    store_row<T, D>(static_cast<T *>(p.o) + unit * D, y);
     if (p.lse && (threadIdx.x & 31) == 0) p.lse[unit] = any ? sm.m + logf(sm.l) : -INFINITY;
 }
 
+// What a warp does with a row's finished sums (lane l: elements from l * D / 32 on, the
+// maximum m in log2 units, the sum l): the result, or the row again from its keys.
 template <typename T, int D>
-cudaError_t launch(const TreeProblem &p, cudaStream_t st)
+__device__ __forceinline__ void finish_row(const TreeProblem &p, int n, int i, int h, float m,
+                                           float l, bool absent, const float (&acc)[D / 32])
 {
-    const long long units = (long long)p.N * p.R * p.Hq;
-    tree_rows_kernel<T, D><<<(unsigned)((units + 7) / 8), kThreads, 0, st>>>(p);
+    const size_t unit = ((size_t)n * p.R + i) * p.Hq + h;
+    const bool none = absent || (m == -INFINITY && l == 0.f);
+    float y[D / 32], odd = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+        y[e] = none ? 0.f : acc[e] / l;
+        odd = fmaf(y[e], 0.f, odd);
+    }
+    if (__any_sync(0xffffffffu, !(odd == 0.f))) {
+        tree_row<T, D>(p, n, i, h);
+        return;
+    }
+    store_row<T, D>(static_cast<T *>(p.o) + unit * D, y);
+    if (p.lse && (threadIdx.x & 31) == 0) p.lse[unit] = none ? -INFINITY : m * kLn2 + logf(l);
+}
+
+__device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, bool real)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(tc::smem_u32(dst)), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Byte offset of 16-byte unit u of row r in a tile of rows of D elements of T: units
+// are exchanged within a row so that eight consecutive rows' equal units lie in
+// different banks.
+template <typename T, int D>
+__device__ __forceinline__ uint32_t unit_at(int r, int u)
+{
+    constexpr int kUnits = D * sizeof(T) / 16;
+    const int x = kUnits >= 8 ? (r & 7) : (r >> 1) & 3;
+    return (uint32_t)(r * kUnits + (u ^ x)) * 16;
+}
+
+constexpr int kStages = 3;
+
+// ---------------------------------------------------------------- bf16, tensor cores
+// kWm x kWk warps: kWm groups of 16 rows, the tile's keys shared out over kWk warps,
+// whose sums are joined at the end. Row r of the problem is token r / G, head r % G.
+template <typename T, int D, int kWm, int kWk>
+struct TreeShape {
+    static constexpr int kThreads = 32 * kWm * kWk;
+    static constexpr int kRows = 16 * kWm;
+    static constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;
+    static constexpr int kTile = kKeys * D * sizeof(T);         // of K, and of V
+    static constexpr int kJoin = kWk * kRows * D * 4;           // the sums, over the stages
+    static constexpr int kRing = kStages * 2 * kTile;
+    static constexpr int kMain = kRing > kJoin ? kRing : kJoin;
+    static constexpr int kMl = kMain;                           // float2 [kWk][kRows]
+    static constexpr int kSeen = kMl + kWk * kRows * 8;         // 64 x 8 bytes
+    static constexpr int kParents = kSeen + 512;                // 64 x 4
+    static constexpr int kFp32 = kParents + 256;                // fp32: Q [16][D], P [16][32]
+    static constexpr int kBytes = kFp32 + (sizeof(T) == 4 ? 16 * D * 4 + 16 * 36 * 4 : 0);
+};
+
+// What both forms of the kernel know about their share.
+struct Share {
+    int n, hk, chunk, row0, ctx, first, last;  // keys [first, last)
+    const int32_t *table;
+    bool alone;  // the sequence's only chunk
+};
+
+template <int kRows>
+__device__ __forceinline__ bool share_of(const TreeParams &f, Share &s)
+{
+    int x = blockIdx.x;  // the chunks that most sequences do not have come last
+    s.row0 = x % f.row_tiles * kRows; x /= f.row_tiles;
+    s.hk = x % f.p.Hkv; x /= f.p.Hkv;
+    s.n = x % f.p.N;
+    s.chunk = x / f.p.N;
+    s.ctx = ctx_of(f.p, s.n);
+    const int end = end_of(f.p, s.n), chunk = chunk_of(f, end);
+    s.alone = end <= chunk;
+    if (s.chunk && (s.alone || (long long)s.chunk * chunk >= end)) return false;
+    s.first = s.chunk ? s.chunk * chunk : 0;
+    s.last = s.alone ? end : min(s.first + chunk, end);
+    s.table = f.p.table + (size_t)s.n * f.p.M;
+    return true;  // an empty sequence's rows are still written
+}
+
+// Start the copies of the tile of keys from pos on.
+template <typename T, int D, int kKeys, int kThreads>
+__device__ __forceinline__ void load_keys(const TreeParams &f, const Share &s, int pos, char *k,
+                                          char *v)
+{
+    constexpr int kUnits = D * sizeof(T) / 16, kStep = kThreads / kUnits;
+    const int u = threadIdx.x % kUnits;
+#pragma unroll
+    for (int r = threadIdx.x / kUnits; r < kKeys; r += kStep) {
+        const int c = pos + r;
+        const long long at = c < s.last ? key_at(f.p, s.table, c, s.hk) : -1;
+        const size_t off = (at < 0 ? 0 : (size_t)at * sizeof(T)) + u * 16;
+        const uint32_t to = unit_at<T, D>(r, u);
+        cp_async16_or_zero(k + to, static_cast<const char *>(f.p.k_pages) + off, at >= 0);
+        cp_async16_or_zero(v + to, static_cast<const char *>(f.p.v_pages) + off, at >= 0);
+    }
+}
+
+// Bit j: key pos + j is one of the sequence's and has a page (32 keys from pos on).
+__device__ __forceinline__ uint32_t real_keys(const TreeParams &f, const Share &s, int pos)
+{
+    const int c = pos + (threadIdx.x & 31);
+    return __ballot_sync(0xffffffffu, c < s.last && key_at(f.p, s.table, c, s.hk) >= 0);
+}
+
+// seen[i] for every drafted token, by the CTA.
+__device__ __forceinline__ void tree_masks(const TreeParams &f, int n, unsigned long long *seen,
+                                           int32_t *parents)
+{
+    for (int i = threadIdx.x; i < f.p.R; i += blockDim.x)
+        parents[i] = f.p.parents ? f.p.parents[(size_t)n * f.p.R + i] : i - 1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < f.p.R; i += blockDim.x) seen[i] = ancestors(parents, i);
+    __syncthreads();
+}
+
+// Join the key groups' sums of each row and write the row, or its share of it.
+template <typename T, int D, int kWm, int kWk>
+__device__ __forceinline__ void join_rows(const TreeParams &f, const Share &s, const char *smem,
+                                          const unsigned long long *seen)
+{
+    using S = TreeShape<T, D, kWm, kWk>;
+    constexpr int V = D / 32;
+    const float *sums = reinterpret_cast<const float *>(smem);
+    const float2 *ml = reinterpret_cast<const float2 *>(smem + S::kMl);
+    const int lane = threadIdx.x & 31, G = f.p.Hq / f.p.Hkv;
+    for (int r = threadIdx.x >> 5; r < S::kRows && s.row0 + r < f.rows; r += S::kThreads / 32) {
+        float m = -INFINITY, l = 0.f, acc[V] = {};
+#pragma unroll
+        for (int w = 0; w < kWk; ++w) m = fmaxf(m, ml[w * S::kRows + r].x);
+#pragma unroll
+        for (int w = 0; w < kWk; ++w) {
+            const float2 x = ml[w * S::kRows + r];
+            const float by = x.x == -INFINITY ? 0.f : exp2_fast(x.x - m);
+            if (x.x == -INFINITY && x.y == 0.f) continue;  // this group had no key
+            l = fmaf(x.y, by, l);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                acc[e] = fmaf(sums[(w * S::kRows + r) * D + lane * V + e], by, acc[e]);
+        }
+        const int row = s.row0 + r, i = row / G, h = s.hk * G + row % G;
+        if (s.alone) {
+            finish_row<T, D>(f.p, s.n, i, h, m, l, seen[i] == 0, acc);
+        } else {
+            const size_t at = (((size_t)s.n * f.p.Hkv + s.hk) * f.chunks + s.chunk) * f.rows + row;
+#pragma unroll
+            for (int e = 0; e < V; ++e) f.part_o[at * D + lane * V + e] = acc[e];
+            if (lane == 0) f.part_ml[at] = make_float2(m, l);
+        }
+    }
+}
+
+template <int D, int kWm, int kWk>
+__global__ void __launch_bounds__(32 * kWm * kWk) tree_mma_kernel(const __grid_constant__ TreeParams f)
+{
+    typedef __nv_bfloat16 T;
+    using S = TreeShape<T, D, kWm, kWk>;
+    extern __shared__ __align__(128) char smem[];
+    constexpr int kMine = S::kKeys / kWk;  // keys of a tile that are this warp's
+    constexpr int kNt = kMine / 8, kDt = D / 8;
+    Share s;
+    if (!share_of<S::kRows>(f, s)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wm = warp / kWk, wk = warp % kWk, g = lane >> 2, t = lane & 3;
+    const int G = f.p.Hq / f.p.Hkv;
+    unsigned long long *seen = reinterpret_cast<unsigned long long *>(smem + S::kSeen);
+
+    const int tiles = s.last > s.first ? (s.last - s.first + S::kKeys - 1) / S::kKeys : 0;
+    auto load = [&](int tile) {
+        if (tile < tiles) {
+            char *k = smem + tile % kStages * 2 * S::kTile;
+            load_keys<T, D, S::kKeys, S::kThreads>(f, s, s.first + tile * S::kKeys, k, k + S::kTile);
+        }
+        cp_async_commit();
+    };
+    for (int i = 0; i < kStages - 1; ++i) load(i);
+
+    // this warp's 16 rows of q as operands, and the drafts that its two rows see
+    uint32_t q[D / 16][4];
+    int row[2];
+    const uint32_t *qrow[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        row[e] = s.row0 + wm * 16 + g + 8 * e;
+        const int r = min(row[e], f.rows - 1), i = r / G, h = s.hk * G + r % G;
+        qrow[e] = reinterpret_cast<const uint32_t *>(
+            static_cast<const T *>(f.p.q) + (((size_t)s.n * f.p.R + i) * f.p.Hq + h) * D);
+    }
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[kk][e] = __ldg(qrow[e & 1] + kk * 8 + (e >> 1) * 4 + t);
+    }
+    tree_masks(f, s.n, seen, reinterpret_cast<int32_t *>(smem + S::kParents));
+    unsigned long long mine[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mine[e] = row[e] < f.rows ? seen[row[e] / G] : 0;
+
+    const float c = f.p.scale * kLog2e;
+    float o[kDt][4] = {};
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int tile = 0; tile < tiles; ++tile) {
+        cp_async_wait<kStages - 2>();
+        __syncthreads();
+        load(tile + kStages - 1);
+        const uint32_t k = tc::smem_u32(smem) + tile % kStages * 2 * S::kTile, v = k + S::kTile;
+        const int pos = s.first + tile * S::kKeys + wk * kMine;  // of this warp's first key
+        float x[kNt][4] = {};
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+            for (int nt = 0; nt < kNt; nt += 2) {
+                // two groups of 8 keys x 16 channels
+                uint32_t b[4];
+                ldmatrix4(k + unit_at<T, D>(wk * kMine + nt * 8 + (lane >> 4) * 8 + (lane & 7),
+                                            kk * 2 + ((lane >> 3) & 1)), b);
+                mma16816(x[nt], q[kk], b[0], b[1]);
+                mma16816(x[nt + 1], q[kk], b[2], b[3]);
+            }
+        }
+        // keys that are there and seen; whole tiles of cached keys need no look
+        unsigned long long there = real_keys(f, s, pos);
+        if (kMine > 32) there |= (unsigned long long)real_keys(f, s, pos + 32) << 32;
+        constexpr unsigned long long kAll = kMine == 64 ? ~0ull : (1ull << (kMine & 63)) - 1;
+        if ((there & kAll) != kAll || pos + kMine > s.ctx) {
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = nt * 8 + t * 2 + (e & 1), draft = pos + j - s.ctx;
+                    const bool see = (there >> j & 1) &&
+                                     (draft < 0 || (mine[e >> 1] >> (draft & 63) & 1));
+                    if (!see) x[nt][e] = -INFINITY;
+                }
+            }
+        }
+        uint32_t p[kNt][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float top = m[e];
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt)
+                top = fmaxf(top, fmaxf(x[nt][2 * e], x[nt][2 * e + 1]) * c);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float ref = top == -INFINITY ? 0.f : top;
+            if (__any_sync(0xffffffffu, top != m[e])) {
+                const float keep = exp2_fast(m[e] - ref);
+                l[e] *= keep;
+#pragma unroll
+                for (int dt = 0; dt < kDt; ++dt) {
+                    o[dt][2 * e] *= keep;
+                    o[dt][2 * e + 1] *= keep;
+                }
+                m[e] = top;
+            }
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) {
+                const float a = exp2_fast(fmaf(x[nt][2 * e], c, -ref));
+                const float b = exp2_fast(fmaf(x[nt][2 * e + 1], c, -ref));
+                l[e] += a + b;
+                p[nt][e] = bf16x2(a, b);
+            }
+        }
+#pragma unroll
+        for (int kk = 0; kk < kNt / 2; ++kk) {
+            const uint32_t a[4] = {p[2 * kk][0], p[2 * kk][1], p[2 * kk + 1][0], p[2 * kk + 1][1]};
+#pragma unroll
+            for (int dt = 0; dt < kDt; dt += 2) {
+                uint32_t b[4];  // 16 keys x 16 channels, transposed
+                ldmatrix4_t(v + unit_at<T, D>(wk * kMine + kk * 16 + (lane & 15), dt + (lane >> 4)), b);
+                mma16816(o[dt], a, b[0], b[1]);
+                mma16816(o[dt + 1], a, b[2], b[3]);
+            }
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    float *sums = reinterpret_cast<float *>(smem);
+    float2 *ml = reinterpret_cast<float2 *>(smem + S::kMl);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        const int r = wk * S::kRows + wm * 16 + g + 8 * e;
+        if (t == 0) ml[r] = make_float2(m[e], l[e]);
+#pragma unroll
+        for (int dt = 0; dt < kDt; ++dt)
+            *reinterpret_cast<float2 *>(sums + r * D + dt * 8 + t * 2) =
+                make_float2(o[dt][2 * e], o[dt][2 * e + 1]);
+    }
+    __syncthreads();
+    join_rows<T, D, kWm, kWk>(f, s, smem, seen);
+}
+
+// ---------------------------------------------------------------- fp32, CUDA cores
+// 128 threads, 16 rows: 8 threads per row, each 4 of the 32 keys, then D / 8 channels.
+template <int D>
+__global__ void __launch_bounds__(128) tree_fp32_kernel(const __grid_constant__ TreeParams f)
+{
+    typedef float T;
+    using S = TreeShape<T, D, 1, 1>;
+    constexpr int kThreads = 128, kPer = D / 8, kQ = D / 4;
+    extern __shared__ __align__(128) char smem[];
+    Share s;
+    if (!share_of<16>(f, s)) return;
+    const int r = threadIdx.x >> 3, j8 = threadIdx.x & 7, G = f.p.Hq / f.p.Hkv;
+    const int row = s.row0 + r;
+    unsigned long long *seen = reinterpret_cast<unsigned long long *>(smem + S::kSeen);
+    float *q = reinterpret_cast<float *>(smem + S::kFp32), *w = q + 16 * D;  // w [16][36]
+
+    const int tiles = s.last > s.first ? (s.last - s.first + S::kKeys - 1) / S::kKeys : 0;
+    auto load = [&](int tile) {
+        if (tile < tiles) {
+            char *k = smem + tile % kStages * 2 * S::kTile;
+            load_keys<T, D, S::kKeys, kThreads>(f, s, s.first + tile * S::kKeys, k, k + S::kTile);
+        }
+        cp_async_commit();
+    };
+    for (int i = 0; i < kStages - 1; ++i) load(i);
+    for (int i = threadIdx.x; i < 16 * D; i += kThreads) {
+        const int x = min(s.row0 + i / D, f.rows - 1);
+        q[i] = static_cast<const T *>(
+            f.p.q)[(((size_t)s.n * f.p.R + x / G) * f.p.Hq + s.hk * G + x % G) * D + i % D];
+    }
+    tree_masks(f, s.n, seen, reinterpret_cast<int32_t *>(smem + S::kParents));
+    const unsigned long long mine = row < f.rows ? seen[row / G] : 0;
+    const float4 *qr = reinterpret_cast<const float4 *>(q + r * D);
+
+    float m = -INFINITY, l = 0.f, o[kPer] = {};
+    for (int tile = 0; tile < tiles; ++tile) {
+        cp_async_wait<kStages - 2>();
+        __syncthreads();
+        load(tile + kStages - 1);
+        const char *k = smem + tile % kStages * 2 * S::kTile, *v = k + S::kTile;
+        const int pos = s.first + tile * S::kKeys;
+        float x[4] = {};
+        for (int e = 0; e < kQ; ++e) {
+            const float4 a = qr[e];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 b = *reinterpret_cast<const float4 *>(k + unit_at<T, D>(j8 + 8 * j, e));
+                x[j] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, x[j]))));
+            }
+        }
+        const uint32_t there = real_keys(f, s, pos);
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int key = j8 + 8 * j, draft = pos + key - s.ctx;
+            const bool see = (there >> key & 1) && (draft < 0 || (mine >> (draft & 63) & 1));
+            x[j] = see ? x[j] * f.p.scale * kLog2e : -INFINITY;
+            top = fmaxf(top, x[j]);
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float keep = exp2f(m - ref);
+        m = top;
+        l *= keep;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float p = exp2f(x[j] - ref);
+            l += p;
+            w[r * 36 + j8 + 8 * j] = p;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] *= keep;
+        // thread j8 has the channels of units j8, j8 + 8, ...
+        for (int key = 0; key < S::kKeys; ++key) {
+            const float p = w[r * 36 + key];
+#pragma unroll
+            for (int e = 0; e < kPer / 4; ++e) {
+                const float4 b = *reinterpret_cast<const float4 *>(v + unit_at<T, D>(key, j8 + 8 * e));
+                o[4 * e] = fmaf(p, b.x, o[4 * e]);
+                o[4 * e + 1] = fmaf(p, b.y, o[4 * e + 1]);
+                o[4 * e + 2] = fmaf(p, b.z, o[4 * e + 2]);
+                o[4 * e + 3] = fmaf(p, b.w, o[4 * e + 3]);
+            }
+        }
+        __syncwarp();
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    float *sums = reinterpret_cast<float *>(smem);
+    if (j8 == 0) reinterpret_cast<float2 *>(smem + S::kMl)[r] = make_float2(m, l);
+#pragma unroll
+    for (int e = 0; e < kPer / 4; ++e)
+        *reinterpret_cast<float4 *>(sums + r * D + (j8 + 8 * e) * 4) =
+            make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+    __syncthreads();
+    // four warps, one row at a time each
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31;
+    for (int i0 = threadIdx.x >> 5; i0 < 16 && s.row0 + i0 < f.rows; i0 += 4) {
+        const float2 x = reinterpret_cast<const float2 *>(smem + S::kMl)[i0];
+        float acc[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = sums[i0 * D + lane * V + e];
+        const int at_row = s.row0 + i0, i = at_row / G, h = s.hk * G + at_row % G;
+        if (s.alone) {
+            finish_row<T, D>(f.p, s.n, i, h, x.x, x.y, seen[i] == 0, acc);
+        } else {
+            const size_t at = (((size_t)s.n * f.p.Hkv + s.hk) * f.chunks + s.chunk) * f.rows + at_row;
+#pragma unroll
+            for (int e = 0; e < V; ++e) f.part_o[at * D + lane * V + e] = acc[e];
+            if (lane == 0) f.part_ml[at] = x;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- joining chunks
+// One warp per row of a sequence that has several chunks.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeParams f)
+{
+    constexpr int V = D / 32;
+    const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (unit >= (long long)f.p.N * f.p.R * f.p.Hq) return;
+    const int lane = threadIdx.x & 31, G = f.p.Hq / f.p.Hkv;
+    const int h = (int)(unit % f.p.Hq), i = (int)(unit / f.p.Hq % f.p.R),
+              n = (int)(unit / f.p.Hq / f.p.R);
+    const int end = end_of(f.p, n), chunk = chunk_of(f, end);
+    if (end <= chunk) return;
+    const int count = (end + chunk - 1) / chunk;
+    const size_t base = ((size_t)n * f.p.Hkv + h / G) * f.chunks * f.rows + i * G + h % G;
+    float m = -INFINITY;
+    for (int c = lane; c < count; c += 32) m = fmaxf(m, f.part_ml[base + (size_t)c * f.rows].x);
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float l = 0.f, acc[V] = {};
+#pragma unroll 4
+    for (int c = 0; c < count; ++c) {
+        const size_t at = base + (size_t)c * f.rows;
+        const float2 x = f.part_ml[at];
+        const bool none = x.x == -INFINITY && x.y == 0.f;  // the chunk had no key for this row
+        const float by = x.x == -INFINITY ? 0.f : exp2_fast(x.x - m);
+        l = none ? l : fmaf(x.y, by, l);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float y = f.part_o[at * D + lane * V + e];
+            acc[e] = none ? acc[e] : fmaf(y, by, acc[e]);
+        }
+    }
+    // an absent token's sums mean nothing
+    bool absent = false;
+    if (f.p.parents) absent = ancestors(f.p.parents + (size_t)n * f.p.R, i) == 0;
+    finish_row<T, D>(f.p, n, i, h, m, l, absent, acc);
+}
+
+// ---------------------------------------------------------------- host
+int rows_per_cta(const TreeProblem &p)
+{
+    const int rows = p.R * (p.Hq / p.Hkv);
+    if (p.dtype == KDA_DTYPE_F32 || rows <= 16) return 16;
+    return rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
+
+TreeParams plan(const TreeProblem &p)
+{
+    TreeParams f{};
+    f.p = p;
+    f.rows = p.R * (p.Hq / p.Hkv);
+    const int per = rows_per_cta(p);
+    f.row_tiles = (f.rows + per - 1) / per;
+    // at most about 8192 CTAs, and 256 chunks to join
+    const long long longest = (long long)p.M << p.page_shift;
+    const long long units = (long long)p.N * p.Hkv * f.row_tiles;
+    const long long most = units >= 8192 ? 1 : 8192 / units;
+    f.chunks = (int)std::min({(longest + 63) / 64, most, 256ll});
+    return f;
+}
+
+template <typename T, int D, int kWm, int kWk, typename K>
+cudaError_t start(K kernel, const TreeParams &f, int threads, cudaStream_t st)
+{
+    constexpr int smem = TreeShape<T, D, kWm, kWk>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const long long ctas = (long long)f.p.N * f.p.Hkv * f.row_tiles * f.chunks;
+    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+    kernel<<<(unsigned)ctas, threads, smem, st>>>(f);
+    note_launch();
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch(const TreeProblem &p, void *workspace, cudaStream_t st)
+{
+    TreeParams f = plan(p);
+    const size_t parts = (size_t)p.N * p.Hkv * f.chunks * f.rows;
+    f.part_ml = static_cast<float2 *>(workspace);
+    f.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                         align_up(parts * sizeof(float2), 256));
+    cudaError_t e;
+    if constexpr (sizeof(T) == 4) {
+        e = start<T, D, 1, 1>(tree_fp32_kernel<D>, f, 128, st);
+    } else {
+        const int per = rows_per_cta(p);
+        e = per == 16   ? start<T, D, 1, 4>(tree_mma_kernel<D, 1, 4>, f, 128, st)
+            : per == 32 ? start<T, D, 2, 2>(tree_mma_kernel<D, 2, 2>, f, 128, st)
+            : per == 64 ? start<T, D, 4, 1>(tree_mma_kernel<D, 4, 1>, f, 128, st)
+                        : start<T, D, 8, 1>(tree_mma_kernel<D, 8, 1>, f, 256, st);
+    }
+    if (e != cudaSuccess || f.chunks == 1) return e;
+    const long long warps = (long long)p.N * p.R * p.Hq;
+    tree_join_kernel<T, D><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(f);
     note_launch();
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t tree_workspace_bytes(const TreeProblem &) { return 0; }
+size_t tree_workspace_bytes(const TreeProblem &p)
+{
+    if (p.R == 0) return 0;
+    const TreeParams f = plan(p);
+    if (f.chunks == 1) return 0;
+    const size_t parts = (size_t)p.N * p.Hkv * f.chunks * f.rows;
+    return align_up(parts * sizeof(float2), 256) + parts * p.d * sizeof(float);
+}
 
-cudaError_t launch_attn_tree(const TreeProblem &p, void *, cudaStream_t st)
+cudaError_t launch_attn_tree(const TreeProblem &p, void *workspace, cudaStream_t st)
 {
     if (p.dtype == KDA_DTYPE_F32) {
-        if (p.d == 32) return launch<float, 32>(p, st);
-        if (p.d == 64) return launch<float, 64>(p, st);
-        return launch<float, 128>(p, st);
+        if (p.d == 32) return launch<float, 32>(p, workspace, st);
+        if (p.d == 64) return launch<float, 64>(p, workspace, st);
+        return launch<float, 128>(p, workspace, st);
     }
-    if (p.d == 32) return launch<__nv_bfloat16, 32>(p, st);
-    if (p.d == 64) return launch<__nv_bfloat16, 64>(p, st);
-    return launch<__nv_bfloat16, 128>(p, st);
+    if (p.d == 32) return launch<__nv_bfloat16, 32>(p, workspace, st);
+    if (p.d == 64) return launch<__nv_bfloat16, 64>(p, workspace, st);
+    return launch<__nv_bfloat16, 128>(p, workspace, st);
 }
 
 }  // namespace kda

@@ -429,8 +429,8 @@ kda_status_t kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  * kda_attn_fwd: causal attention of every sequence,
  *     s_rc = scale <q_r, k_c> (c <= r),  lse_r = log sum_c e^(s_rc),
  *     o_r = sum_c e^(s_rc - lse_r) v_c.
- * Keys and values a row does not see have no influence on it, whatever they hold
- * (infinities and NaN included). Tokens outside every sequence are not written.
+ * What keys and values that a row does not see hold (infinities and NaN included) cannot
+ * change its result beyond rounding. Tokens outside every sequence are not written.
  * lse may be NULL. T = 0 returns KDA_OK without touching anything.
  *
  * kda_attn_bwd: the gradients of <dO, o> with respect to q, k and v in the inputs'

@@ -104,7 +104,11 @@ def test_masked_places_do_not_matter(bad, dtype):
     kp, vp = (torch.where(used[:, None, :, None], x, bad) for x in (kp, vp))
     o2, lse2 = api().kda_attn_tree(q, kp, vp, table, c, parents=parents)
     keep = [0, 2, 3, 5]
-    assert torch.equal(o[:, keep], o2[:, keep]) and torch.equal(lse[:, keep], lse2[:, keep])
+    # The exact result is the same, so both runs are within its bound; they need not be the
+    # same bits, as a row that met a bad value is computed again without rounding P.
+    ro, rl, to, tl = R.attn_tree(q, kp, vp, table, c, parents, 64 ** -0.5)
+    for got, want, tol in ((o, ro, to), (o2, ro, to), (lse, rl, tl), (lse2, rl, tl)):
+        R.close(got[:, keep], want[:, keep], tol[:, keep])
     assert not torch.isfinite(o2[:, [1, 4]]).any()
 
 
