@@ -1,0 +1,488 @@
+// kda_attn_fp32.cu — causal prompt attention and its gradients in fp32 (CUDA cores),
+// and the choice between this path and the tensor-core path.
+//
+// Tiles of 64 tokens, 256 threads as 16 x 16. A product of two tiles over the channels
+// gives each thread 4 x 4 pairs (rows 4 ty + i, columns tx + 16 j), a product of a
+// 64 x 64 weight tile with a tile of rows 4 rows x D / 16 channels; both read shared
+// memory 16 bytes at a time, the first from swizzled rows. The FMA rate bounds the
+// kernels: per four channels a warp issues 64 FMAs (16 cycles of the SM) for 12 cycles
+// of shared memory reads.
+//
+// The gradients follow the tensor-core path's split: one CTA per key tile for dK and
+// dV, one per query tile for dQ, every result written once. Rows that are not finite
+// are computed again from what they see (0 times a masked infinity is NaN).
+#include "kda_attn_rows.cuh"
+#include "tc_primitives.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kRows = 64;
+constexpr int kThreads = 256;
+constexpr int kW = 68;  // row length of a weight tile
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Element offset of 4-channel unit u of row r of a tile: units are exchanged within a
+// row so that eight consecutive rows' equal units lie in different banks.
+template <int D> __device__ __forceinline__ int unit_at(int r, int u)
+{
+    return r * D + (u ^ (r & 7)) * 4;
+}
+
+// Start the copies of 64 tokens of one head from `first` on; tokens from `end` on are
+// filled with zeros.
+template <int D>
+__device__ __forceinline__ void load_tile(float *dst, const float *src, int heads, int h,
+                                          int first, int end)
+{
+    constexpr int kUnits = D / 4;
+    const int u = threadIdx.x % kUnits;
+#pragma unroll
+    for (int r = threadIdx.x / kUnits; r < kRows; r += kThreads / kUnits) {
+        const bool real = first + r < end;
+        const float *from = src + ((size_t)(real ? first + r : first) * heads + h) * D + u * 4;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     ::"r"(tc::smem_u32(dst + unit_at<D>(r, u))), "l"(from), "r"(real ? 16 : 0)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// All but the last N groups of copies have landed, for every thread of the CTA.
+template <int N> __device__ __forceinline__ void landed()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    __syncthreads();
+}
+
+// x[i][j] = <row 4 ty + i of a, row tx + 16 j of b>.
+template <int D>
+__device__ __forceinline__ void dot_tiles(const float *a, const float *b, float (&x)[4][4])
+{
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+    }
+#pragma unroll 4
+    for (int u = 0; u < D / 4; ++u) {
+        float4 p[4], q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(a + unit_at<D>(4 * ty + i, u));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const float4 *>(b + unit_at<D>(tx + 16 * j, u));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x[i][j] = fmaf(p[i].x, q[j].x, fmaf(p[i].y, q[j].y, fmaf(p[i].z, q[j].z, fmaf(p[i].w, q[j].w, x[i][j]))));
+        }
+    }
+}
+
+// A thread's channels of a row: groups of kVec from tx * kVec + 16 kVec e on.
+template <int D> struct Cols {
+    static constexpr int kVec = D >= 64 ? 4 : 2, kGroups = D / 16 / kVec;
+    static __device__ __forceinline__ int at(int r, int e)
+    {
+        const int c = ((threadIdx.x & 15) + 16 * e) * kVec;
+        return unit_at<D>(r, c >> 2) + (c & 3);
+    }
+    static __device__ __forceinline__ int channel(int e) { return ((threadIdx.x & 15) + 16 * e) * kVec; }
+};
+
+// acc[i] += sum over 64 tokens r of w(4 ty + i, r) * row r of y; w is read along its rows
+// (kT false) or its columns (true).
+template <int D, bool kT>
+__device__ __forceinline__ void add_weighted(const float *w, const float *y, float (&acc)[4][D / 16])
+{
+    using C = Cols<D>;
+    const int ty = threadIdx.x >> 4;
+#pragma unroll 2
+    for (int r = 0; r < kRows; r += 4) {
+        float p[4][4];  // [i][token]
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 x = *reinterpret_cast<const float4 *>(kT ? w + (r + i) * kW + 4 * ty
+                                                                  : w + (4 * ty + i) * kW + r);
+            const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) (kT ? p[j][i] : p[i][j]) = v[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int e = 0; e < C::kGroups; ++e) {
+                float v[C::kVec];
+                if (C::kVec == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(y + C::at(r + j, e));
+                    v[0] = x.x; v[1] = x.y; v[C::kVec - 2] = x.z; v[C::kVec - 1] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(y + C::at(r + j, e));
+                    v[0] = x.x; v[1] = x.y;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int a = 0; a < C::kVec; ++a)
+                        acc[i][e * C::kVec + a] = fmaf(p[i][j], v[a], acc[i][e * C::kVec + a]);
+                }
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void store_weights(float *w, const float (&x)[4][4])
+{
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[(4 * ty + i) * kW + tx + 16 * j] = x[i][j];
+    }
+}
+
+// A thread's rows times `by[i]` to out (row 0 of the tile, rows `stride` apart), below
+// `rows`; flags rows that are not finite.
+template <int D>
+__device__ __forceinline__ void store_rows(const float (&acc)[4][D / 16], const float (&by)[4],
+                                           float *out, size_t stride, int rows, unsigned *bad)
+{
+    using C = Cols<D>;
+    const int ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        if (r >= rows) continue;
+        float odd = 0.f;
+#pragma unroll
+        for (int e = 0; e < C::kGroups; ++e) {
+            float *to = out + r * stride + C::channel(e);
+#pragma unroll
+            for (int a = 0; a < C::kVec; ++a) {
+                const float v = acc[i][e * C::kVec + a] * by[i];
+                odd = fmaf(v, 0.f, odd);
+                to[a] = v;
+            }
+        }
+        if (!(odd == 0.f)) atomicOr(bad + (r >> 5), 1u << (r & 31));
+    }
+}
+
+// After all stores: the flagged rows again, one warp each.
+template <typename F> __device__ __forceinline__ void redo_rows(const unsigned *bad, F redo)
+{
+    __syncthreads();
+    for (int r = threadIdx.x >> 5; r < kRows; r += kThreads / 32)
+        if (bad[r >> 5] >> (r & 31) & 1) redo(r);
+}
+
+struct F32Params {
+    AttnProblem p;
+    const AttnTile *tiles;  // null: uniform sequences
+    const float *lse, *lse2, *delta, *dO;
+    float *o, *lse_out, *gq, *gk, *gv;
+    int *status;  // of the workspace: nothing here can fail, the first CTA clears it
+};
+
+__device__ __forceinline__ AttnTile tile_of(const F32Params &f, int idx)
+{
+    if (f.tiles) return f.tiles[idx];
+    const int count = (f.p.T + kRows - 1) / kRows, b = idx % f.p.B, t = count - 1 - idx / f.p.B;
+    return AttnTile{b * f.p.T + t * kRows, b * f.p.T, (b + 1) * f.p.T, 0};
+}
+
+template <int D> __device__ __noinline__ void redo_fwd(const F32Params &f, int row, int start, int h)
+{
+    attn_row_fwd<float, D>(f.p, row, start, h, f.o, f.lse_out);
+}
+template <int D> __device__ __noinline__ void redo_dq(const F32Params &f, int row, int start, int h)
+{
+    attn_row_dq<float, D>(f.p, row, start, h, f.lse, f.delta, f.dO, f.gq);
+}
+template <int D> __device__ __noinline__ void redo_dkv(const F32Params &f, int col, int end, int hk)
+{
+    attn_row_dkv<float, D>(f.p, col, end, hk, f.lse, f.delta, f.dO, f.gk, f.gv);
+}
+
+// ---------------------------------------------------------------- forward
+template <int D>
+__global__ void __launch_bounds__(kThreads) fwd_kernel(const __grid_constant__ F32Params f)
+{
+    extern __shared__ __align__(16) float smem[];
+    __shared__ unsigned bad[2];
+    float *q = smem, *k = q + kRows * D, *v = k + kRows * D, *w = v + kRows * D;
+    const AttnTile t = tile_of(f, blockIdx.x / f.p.Hq);
+    if (t.first >= t.seq_end) return;
+    const int h = blockIdx.x % f.p.Hq, hk = h / (f.p.Hq / f.p.Hkv);
+    if (!f.tiles && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const float *gk = static_cast<const float *>(f.p.k), *gv = static_cast<const float *>(f.p.v);
+    if (threadIdx.x < 2) bad[threadIdx.x] = 0;
+    load_tile<D>(q, static_cast<const float *>(f.p.q), f.p.Hq, h, t.first, t.seq_end);
+    load_tile<D>(k, gk, f.p.Hkv, hk, t.first, t.seq_end);
+    const float c = f.p.scale * kLog2e;
+    float m[4], l[4] = {}, acc[4][D / 16] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = -INFINITY;
+    // key tiles from the diagonal down
+    for (int at = t.first; at >= t.seq_start; at -= kRows) {
+        load_tile<D>(v, gv, f.p.Hkv, hk, at, t.seq_end);
+        landed<1>();
+        float x[4][4];
+        dot_tiles<D>(q, k, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float top = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool see = at < t.first || tx + 16 * j <= 4 * ty + i;
+                x[i][j] = see ? x[i][j] * c : -INFINITY;
+                top = fmaxf(top, x[i][j]);
+            }
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float ref = top == -INFINITY ? 0.f : top, keep = exp2f(m[i] - ref);
+            m[i] = top;
+            l[i] *= keep;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[i][j] = exp2f(x[i][j] - ref);
+                l[i] += x[i][j];
+            }
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) acc[i][e] *= keep;
+        }
+        store_weights(w, x);
+        landed<0>();  // the values, the weights, and k is free
+        if (at > t.seq_start) load_tile<D>(k, gk, f.p.Hkv, hk, at - kRows, t.seq_end);
+        add_weighted<D, false>(w, v, acc);
+        __syncthreads();
+    }
+    float by[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+        by[i] = 1.f / l[i];
+        const int row = t.first + 4 * ty + i;
+        if (f.lse_out && tx == 0 && row < t.seq_end)
+            f.lse_out[(size_t)row * f.p.Hq + h] = m[i] * 0.693147180559945309417f + logf(l[i]);
+    }
+    store_rows<D>(acc, by, f.o + ((size_t)t.first * f.p.Hq + h) * D, (size_t)f.p.Hq * D,
+                  t.seq_end - t.first, bad);
+    redo_rows(bad, [&](int r) { redo_fwd<D>(f, t.first + r, t.seq_start, h); });
+}
+
+// p = 2^(c s - lse2 of the row) where the pair is visible, from raw scores.
+__device__ __forceinline__ void weights_of(float (&x)[4][4], float c, const float *lse2, bool diag)
+{
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float z = lse2[4 * ty + i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool see = !diag || tx + 16 * j <= 4 * ty + i;
+            x[i][j] = see ? exp2f(fmaf(x[i][j], c, -z)) : 0.f;
+        }
+    }
+}
+
+// lse2 and D of 64 query rows; rows behind the sequence get weights of zero.
+__device__ __forceinline__ void load_stats(const F32Params &f, float *lse2, float *del, int h,
+                                           int first, int end)
+{
+    if (threadIdx.x < kRows) {
+        const int r = first + threadIdx.x;
+        const size_t at = (size_t)h * f.p.tokens + r;
+        lse2[threadIdx.x] = r < end ? f.lse2[at] : INFINITY;
+        del[threadIdx.x] = r < end ? f.delta[at] : 0.f;
+    }
+}
+
+// ---------------------------------------------------------------- dQ
+template <int D>
+__global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ F32Params f)
+{
+    extern __shared__ __align__(16) float smem[];
+    __shared__ float lse2[kRows], del[kRows];
+    __shared__ unsigned bad[2];
+    float *q = smem, *g = q + kRows * D, *k = g + kRows * D, *v = k + kRows * D, *w = v + kRows * D;
+    const AttnTile t = tile_of(f, blockIdx.x / f.p.Hq);
+    if (t.first >= t.seq_end) return;
+    const int h = blockIdx.x % f.p.Hq, hk = h / (f.p.Hq / f.p.Hkv), ty = threadIdx.x >> 4;
+    if (threadIdx.x < 2) bad[threadIdx.x] = 0;
+    load_stats(f, lse2, del, h, t.first, t.seq_end);
+    load_tile<D>(q, static_cast<const float *>(f.p.q), f.p.Hq, h, t.first, t.seq_end);
+    load_tile<D>(g, f.dO, f.p.Hq, h, t.first, t.seq_end);
+    const float c = f.p.scale * kLog2e;
+    float acc[4][D / 16] = {};
+    for (int at = t.first; at >= t.seq_start; at -= kRows) {
+        load_tile<D>(k, static_cast<const float *>(f.p.k), f.p.Hkv, hk, at, t.seq_end);
+        load_tile<D>(v, static_cast<const float *>(f.p.v), f.p.Hkv, hk, at, t.seq_end);
+        landed<1>();
+        float x[4][4], y[4][4];
+        dot_tiles<D>(q, k, x);
+        weights_of(x, c, lse2, at == t.first);
+        landed<0>();
+        dot_tiles<D>(g, v, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float dl = del[4 * ty + i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[i][j] *= y[i][j] - dl;
+        }
+        store_weights(w, x);
+        __syncthreads();
+        add_weighted<D, false>(w, k, acc);
+        __syncthreads();
+    }
+    const float by[4] = {f.p.scale, f.p.scale, f.p.scale, f.p.scale};
+    store_rows<D>(acc, by, f.gq + ((size_t)t.first * f.p.Hq + h) * D, (size_t)f.p.Hq * D,
+                  t.seq_end - t.first, bad);
+    redo_rows(bad, [&](int r) { redo_dq<D>(f, t.first + r, t.seq_start, h); });
+}
+
+// ---------------------------------------------------------------- dK and dV
+template <int D>
+__global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ F32Params f)
+{
+    extern __shared__ __align__(16) float smem[];
+    __shared__ float lse2[kRows], del[kRows];
+    __shared__ unsigned bad[2];
+    float *q = smem, *g = q + kRows * D, *k = g + kRows * D, *v = k + kRows * D;
+    float *w = v + kRows * D, *ws = w + kRows * kW;
+    AttnTile t = tile_of(f, blockIdx.x / f.p.Hkv);
+    if (t.first >= t.seq_end) return;
+    if (!f.tiles && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
+    // the list begins with a sequence's last tile; here the first one has most work
+    const int count = (t.seq_end - t.seq_start + kRows - 1) / kRows;
+    t.first = t.seq_start + (count - 1 - (t.first - t.seq_start) / kRows) * kRows;
+    const int hk = blockIdx.x % f.p.Hkv, G = f.p.Hq / f.p.Hkv, ty = threadIdx.x >> 4;
+    if (threadIdx.x < 2) bad[threadIdx.x] = 0;
+    load_tile<D>(k, static_cast<const float *>(f.p.k), f.p.Hkv, hk, t.first, t.seq_end);
+    load_tile<D>(v, static_cast<const float *>(f.p.v), f.p.Hkv, hk, t.first, t.seq_end);
+    const float c = f.p.scale * kLog2e;
+    float ak[4][D / 16] = {}, av[4][D / 16] = {};
+    for (int h = hk * G; h < (hk + 1) * G; ++h)
+        for (int at = t.first; at < t.seq_end; at += kRows) {
+            load_stats(f, lse2, del, h, at, t.seq_end);
+            load_tile<D>(q, static_cast<const float *>(f.p.q), f.p.Hq, h, at, t.seq_end);
+            load_tile<D>(g, f.dO, f.p.Hq, h, at, t.seq_end);
+            landed<1>();
+            float x[4][4], y[4][4];
+            dot_tiles<D>(q, k, x);
+            weights_of(x, c, lse2, at == t.first);
+            store_weights(w, x);
+            landed<0>();
+            dot_tiles<D>(g, v, y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float dl = del[4 * ty + i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[i][j] *= y[i][j] - dl;
+            }
+            store_weights(ws, x);
+            add_weighted<D, true>(w, g, av);
+            __syncthreads();
+            add_weighted<D, true>(ws, q, ak);
+            __syncthreads();
+        }
+    const size_t out = ((size_t)t.first * f.p.Hkv + hk) * D, stride = (size_t)f.p.Hkv * D;
+    const float one[4] = {1.f, 1.f, 1.f, 1.f};
+    const float by[4] = {f.p.scale, f.p.scale, f.p.scale, f.p.scale};
+    store_rows<D>(av, one, f.gv + out, stride, t.seq_end - t.first, bad);
+    store_rows<D>(ak, by, f.gk + out, stride, t.seq_end - t.first, bad);
+    redo_rows(bad, [&](int r) { redo_dkv<D>(f, t.first + r, t.seq_end, hk); });
+}
+
+template <typename K>
+cudaError_t start(K kernel, const F32Params &f, long long ctas, int smem, cudaStream_t st)
+{
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)ctas, kThreads, smem, st>>>(f);
+    note_launch();
+    return cudaGetLastError();
+}
+
+// The tile list, or none for uniform sequences.
+cudaError_t prepare(const AttnProblem &p, bool bwd, void *workspace, F32Params &f, cudaStream_t st)
+{
+    f.status = static_cast<int *>(workspace);
+    if (!p.cu_seqlens) return cudaSuccess;
+    f.tiles = reinterpret_cast<const AttnTile *>(
+        static_cast<char *>(workspace) + attn_workspace_layout(p, kRows, bwd).tiles);
+    return launch_attn_plan(p, kRows, workspace, st);
+}
+
+template <int D>
+cudaError_t fwd(const AttnProblem &p, void *o, float *lse, void *workspace, cudaStream_t st)
+{
+    F32Params f{};
+    f.p = p;
+    f.o = static_cast<float *>(o);
+    f.lse_out = lse;
+    const cudaError_t e = prepare(p, false, workspace, f, st);
+    if (e != cudaSuccess) return e;
+    return start(fwd_kernel<D>, f, attn_tiles(p, kRows) * p.Hq, (3 * kRows * D + kRows * kW) * 4, st);
+}
+
+template <int D>
+cudaError_t bwd(const AttnProblem &p, const void *o, const float *lse, const void *dO, void *gq,
+                void *gk, void *gv, void *workspace, cudaStream_t st)
+{
+    F32Params f{};
+    f.p = p;
+    float *delta = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                             attn_workspace_layout(p, kRows, true).delta);
+    float *lse2 = delta + (size_t)p.tokens * p.Hq;
+    f.lse = lse; f.lse2 = lse2; f.delta = delta;
+    f.dO = static_cast<const float *>(dO);
+    f.gq = static_cast<float *>(gq);
+    f.gk = static_cast<float *>(gk);
+    f.gv = static_cast<float *>(gv);
+    cudaError_t e = prepare(p, true, workspace, f, st);
+    if (e == cudaSuccess) e = launch_attn_delta(p, o, lse, dO, delta, lse2, st);
+    const long long tiles = attn_tiles(p, kRows);
+    if (e == cudaSuccess)
+        e = start(dkv_kernel<D>, f, tiles * p.Hkv, (4 * kRows * D + 2 * kRows * kW) * 4, st);
+    if (e == cudaSuccess)
+        e = start(dq_kernel<D>, f, tiles * p.Hq, (4 * kRows * D + kRows * kW) * 4, st);
+    return e;
+}
+
+}  // namespace
+
+int attn_fwd_rows(const AttnProblem &p)
+{
+    return p.dtype == KDA_DTYPE_BF16 ? attn_tc_fwd_rows() : kRows;
+}
+
+int attn_bwd_rows(const AttnProblem &p)
+{
+    return p.dtype == KDA_DTYPE_BF16 ? attn_tc_bwd_rows() : kRows;
+}
+
+cudaError_t launch_attn_fwd(const AttnProblem &p, void *o, float *lse, void *ws, cudaStream_t st)
+{
+    if (p.dtype == KDA_DTYPE_BF16) return launch_attn_tc_fwd(p, o, lse, ws, st);
+    if (p.d == 32) return fwd<32>(p, o, lse, ws, st);
+    if (p.d == 64) return fwd<64>(p, o, lse, ws, st);
+    return fwd<128>(p, o, lse, ws, st);
+}
+
+cudaError_t launch_attn_bwd(const AttnProblem &p, const void *o, const float *lse, const void *dO,
+                            void *gq, void *gk, void *gv, void *ws, cudaStream_t st)
+{
+    if (p.dtype == KDA_DTYPE_BF16)
+        return launch_attn_tc_bwd(p, o, lse, dO, gq, gk, gv, ws, st);
+    if (p.d == 32) return bwd<32>(p, o, lse, dO, gq, gk, gv, ws, st);
+    if (p.d == 64) return bwd<64>(p, o, lse, dO, gq, gk, gv, ws, st);
+    return bwd<128>(p, o, lse, dO, gq, gk, gv, ws, st);
+}
+
+}  // namespace kda
