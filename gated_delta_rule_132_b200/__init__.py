@@ -22,8 +22,8 @@ _ATTN_EXPORTS = ("kda_attn_fwd", "kda_attn_bwd", "kda_attn_tree", "kda_attn_stat
 
 
 def __getattr__(name):
-    if name in _EXPORTS:
-        return getattr(importlib.import_module(".kda", __name__), name)
-    if name in _ATTN_EXPORTS:
-        return getattr(importlib.import_module(".attn", __name__), name)
-    raise AttributeError(name)
+    module = ".kda" if name in _EXPORTS else ".attn" if name in _ATTN_EXPORTS else None
+    if module is None:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(importlib.import_module(module, __name__), name)
+    return value

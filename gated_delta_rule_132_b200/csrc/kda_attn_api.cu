@@ -230,6 +230,7 @@ kda_status_t kda_attn_tree(const void *q, const void *k_pages, const void *v_pag
     kda_status_t st = describe_tree(N, R, Hq, Hkv, d, M, page_size, dt, &p);
     if (st != KDA_OK) return st;
     if (P < 1 || !scale_ok(scale)) return KDA_ERR_INVALID_ARG;
+    if ((long long)P * Hkv * page_size > (long long)INT32_MAX) return KDA_ERR_UNSUPPORTED;
     if (R == 0) return KDA_OK;
     if (!q || !k_pages || !v_pages || !block_table || !ctx_lens || !o) return KDA_ERR_INVALID_ARG;
     for (const void *ptr : {q, k_pages, v_pages, (const void *)o, (const void *)workspace})
@@ -241,7 +242,10 @@ kda_status_t kda_attn_tree(const void *q, const void *k_pages, const void *v_pag
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     p.q = q; p.k_pages = k_pages; p.v_pages = v_pages; p.table = block_table;
     p.ctx_lens = ctx_lens; p.parents = parents; p.P = P; p.scale = scale; p.o = o; p.lse = lse;
-    return from_cuda(kda::launch_attn_tree(p, workspace, static_cast<cudaStream_t>(stream)));
+    st = from_cuda(kda::launch_attn_tree(p, workspace, static_cast<cudaStream_t>(stream)));
+    if (st != KDA_OK || !attn_debug_sync()) return st;
+    int code = 0;
+    return kda_attn_status(workspace, workspace_bytes, &code, stream);
 }
 
 kda_status_t kda_cache_fork(int32_t *refs, const int32_t *block_table, const int32_t *lens,

@@ -440,7 +440,7 @@ kda_status_t kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  * (grad_k and grad_v summed over the group's query heads in fp32 before rounding).
  *
  * Errors as for kda_chunk_fwd. kda_attn_status reads the status word of the last
- * kda_attn_fwd / kda_attn_bwd on a workspace, as kda_chunk_fwd_status does.
+ * kda_attn_fwd, kda_attn_bwd or kda_attn_tree on a workspace, as kda_chunk_fwd_status does.
  */
 size_t kda_attn_fwd_workspace_size(int B, int T, int Hq, int Hkv, int d, int n_seqs,
                                    kda_dtype_t dtype);
