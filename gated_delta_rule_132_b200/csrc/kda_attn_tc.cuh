@@ -75,6 +75,16 @@ __device__ __forceinline__ void tma_load_2d(void *dst_smem, const void *tmap, in
                  : "memory");
 }
 
+// 4-D tiled copy, as tma_load_3d.
+__device__ __forceinline__ void tma_load_4d(void *dst_smem, const void *tmap, int x, int y, int z,
+                                            int w, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 ::"r"(smem_u32(dst_smem)), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w),
+                   "r"(smem_u32(bar)) : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem desc], bf16 inputs, fp32 accumulate.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                             uint32_t idesc, uint32_t accumulate)

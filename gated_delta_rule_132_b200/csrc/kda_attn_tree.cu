@@ -25,142 +25,11 @@
 // again from the keys they see.
 #include <algorithm>
 
-#include "kda_attn_rows.cuh"
-#include "kda_attn_tc.cuh"
+#include "kda_attn_tree.cuh"
 
 namespace kda {
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.693147180559945309417f;
-
-// The drafted tokens that token i attends to, as bits: itself and its ancestors; 0
-// where it, or one of them, has a parent that is neither -1 nor an earlier token.
-__device__ __forceinline__ unsigned long long ancestors(const int32_t *parents, int i)
-{
-    unsigned long long seen = 0;
-    int j = i;
-    while (j >= 0) {
-        seen |= 1ull << j;
-        const int up = parents[j];
-        if (up < -1 || up >= j) return 0;
-        j = up;
-    }
-    return seen;
-}
-
-struct TreeParams {
-    TreeProblem p;
-    int rows;       // R * G
-    int row_tiles;  // CTAs that share a chunk's keys
-    int chunks;     // most chunks of a sequence
-    float *part_o;  // [n, hk, chunk, row, D]: sums over e^(s - m) v
-    float2 *part_ml;
-    // bf16: the pools as rows of a head's channels, and where the waits report
-    CUtensorMap k, v;
-    int pool_rows;
-    int *status;
-    uint32_t spin;
-    int starve;
-};
-
-// Where key `pos` of a row of the table is, in elements; -1 where it has no page.
-__device__ __forceinline__ long long key_at(const TreeProblem &p, const int32_t *row, int pos,
-                                            int hk)
-{
-    const int id = __ldg(row + (pos >> p.page_shift));
-    if ((unsigned)id >= (unsigned)p.P) return -1;
-    return (((((long long)id * p.Hkv + hk) << p.page_shift) + (pos & ((1 << p.page_shift) - 1)))) * p.d;
-}
-
-__device__ __forceinline__ int ctx_of(const TreeProblem &p, int n)
-{
-    return min(max(p.ctx_lens[n], 0), p.M << p.page_shift);
-}
-
-__device__ __forceinline__ int end_of(const TreeProblem &p, int n)
-{
-    return min(ctx_of(p, n) + p.R, p.M << p.page_shift);
-}
-
-// Keys per chunk of a sequence of `end` keys. Lengths are known on the device only, so
-// every warp adds them up: chunks are to be small enough for about six CTAs per
-// resident place (two per SM) and no smaller than a tile, nor, as a chunk's fixed cost
-// is about a tile's, need they be below 2048 keys to balance the SMs.
-__device__ __forceinline__ int chunk_of(const TreeParams &f, int end)
-{
-    if (f.chunks == 1) return INT32_MAX;
-    constexpr int kCounted = 1024;  // sequences whose lengths are added up
-    int target = 2048;
-    if (f.p.N <= kCounted) {
-        long long total = 0;
-        for (int n = threadIdx.x & 31; n < f.p.N; n += 32) total += end_of(f.p, n);
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-        total = total * f.p.Hkv * f.row_tiles / (148 * 2 * 6);
-        target = (int)min(max(total, 64ll), 2048ll);
-    }
-    const int count = max(1, min(f.chunks, (end + target - 1) / target));
-    return ((end + count - 1) / count + 63) / 64 * 64;
-}
-
-// One row from the keys it sees alone: one warp.
-template <typename T, int D>
-__device__ __noinline__ void tree_row(const TreeProblem &p, int n, int i, int h)
-{
-    constexpr int V = D / 32;
-    const int32_t *row = p.table + (size_t)n * p.M;
-    const int ctx = ctx_of(p, n), end = end_of(p, n);
-    const unsigned long long seen =
-        p.parents ? ancestors(p.parents + (size_t)n * p.R, i) : (2ull << i) - 1;
-    const size_t unit = ((size_t)n * p.R + i) * p.Hq + h;
-    const int hk = h / (p.Hq / p.Hkv);
-    float q[V], x[V], y[V];
-    load_row<T, D>(static_cast<const T *>(p.q) + unit * D, q);
-    RowSoftmax<V> sm;
-    bool any = false;
-    for (int c = 0; c < (seen ? end : 0); ++c) {
-        if (c >= ctx && !(seen >> (c - ctx) & 1)) continue;
-        const long long at = key_at(p, row, c, hk);
-        if (at < 0) continue;
-        load_row<T, D>(static_cast<const T *>(p.k_pages) + at, x);
-        load_row<T, D>(static_cast<const T *>(p.v_pages) + at, y);
-        sm.add(row_dot(q, x) * p.scale, y);
-        any = true;
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) y[e] = any ? sm.acc[e] / sm.l : 0.f;
-    store_row<T, D>(static_cast<T *>(p.o) + unit * D, y);
-    if (p.lse && (threadIdx.x & 31) == 0) p.lse[unit] = any ? sm.m + logf(sm.l) : -INFINITY;
-}
-
-// What a warp does with a row's finished sums (lane l: elements from l * D / 32 on, the
-// maximum m in log2 units, the sum l): the result, or the row again from its keys.
-template <typename T, int D>
-__device__ __forceinline__ void finish_row(const TreeProblem &p, int n, int i, int h, float m,
-                                           float l, bool absent, const float (&acc)[D / 32])
-{
-    const size_t unit = ((size_t)n * p.R + i) * p.Hq + h;
-    const bool none = absent || (m == -INFINITY && l == 0.f);
-    float y[D / 32], odd = 0.f;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-        y[e] = none ? 0.f : acc[e] / l;
-        odd = fmaf(y[e], 0.f, odd);
-    }
-    if (__any_sync(0xffffffffu, !(odd == 0.f))) {
-        tree_row<T, D>(p, n, i, h);
-        return;
-    }
-    store_row<T, D>(static_cast<T *>(p.o) + unit * D, y);
-    if (p.lse && (threadIdx.x & 31) == 0) p.lse[unit] = none ? -INFINITY : m * kLn2 + logf(l);
-}
-
-__device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, bool real)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                 ::"r"(tc::smem_u32(dst)), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait()
 {
@@ -215,31 +84,6 @@ struct F32Shape {
     static constexpr int kBytes = kP + kRows * 36 * 4;
 };
 
-// What both forms of the kernel know about their share.
-struct Share {
-    int n, hk, chunk, row0, ctx, first, last;  // keys [first, last)
-    const int32_t *table;
-    bool alone;  // the sequence's only chunk
-};
-
-template <int kRows>
-__device__ __forceinline__ bool share_of(const TreeParams &f, Share &s)
-{
-    int x = blockIdx.x;  // the chunks that most sequences do not have come last
-    s.row0 = x % f.row_tiles * kRows; x /= f.row_tiles;
-    s.hk = x % f.p.Hkv; x /= f.p.Hkv;
-    s.n = x % f.p.N;
-    s.chunk = x / f.p.N;
-    s.ctx = ctx_of(f.p, s.n);
-    const int end = end_of(f.p, s.n), chunk = chunk_of(f, end);
-    s.alone = end <= chunk;
-    if (s.chunk && (s.alone || (long long)s.chunk * chunk >= end)) return false;
-    s.first = s.chunk ? s.chunk * chunk : 0;
-    s.last = s.alone ? end : min(s.first + chunk, end);
-    s.table = f.p.table + (size_t)s.n * f.p.M;
-    return true;  // an empty sequence's rows are still written
-}
-
 // fp32: byte offset of 16-byte unit u of row r in a tile; units are exchanged within a
 // row so that eight consecutive rows' equal units lie in different banks.
 template <int D> __device__ __forceinline__ uint32_t unit_at(int r, int u)
@@ -270,24 +114,6 @@ __device__ __forceinline__ uint32_t real_keys(const TreeParams &f, const Share &
 {
     const int c = pos + (threadIdx.x & 31);
     return __ballot_sync(0xffffffffu, c < s.last && key_at(f.p, s.table, c, s.hk) >= 0);
-}
-
-// The drafts that every drafted token sees, by the CTA's first S::kMaskThreads threads
-// (they meet in barrier 1).
-template <typename S>
-__device__ __forceinline__ const unsigned long long *tree_masks(const TreeParams &f, int n, char *smem)
-{
-    unsigned long long *seen = reinterpret_cast<unsigned long long *>(smem + S::kSeen);
-    int32_t *parents = reinterpret_cast<int32_t *>(smem + S::kParents);
-    const int i = threadIdx.x;
-    if (i < f.p.R) {
-        parents[i] = f.p.parents ? f.p.parents[(size_t)n * f.p.R + i] : -1;
-        if (!f.p.parents) seen[i] = (2ull << i) - 1;  // a chain
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(S::kMaskThreads) : "memory");
-    if (f.p.parents && i < f.p.R) seen[i] = ancestors(parents, i);
-    asm volatile("bar.sync 1, %0;" ::"n"(S::kMaskThreads) : "memory");
-    return seen;
 }
 
 // Join the key groups' sums of each row (in shared memory) and write the row, or its
@@ -394,7 +220,7 @@ tree_mma_kernel(const __grid_constant__ TreeParams f)
     if (blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
     asm volatile("griddepcontrol.launch_dependents;");
     Share s;
-    if (!share_of<S::kRows>(f, s)) return;
+    if (!share_of(f, s)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = s.last > s.first ? (s.last - s.first + S::kKeys - 1) / S::kKeys : 0;
     if (threadIdx.x == 0) {
@@ -449,7 +275,7 @@ tree_mma_kernel(const __grid_constant__ TreeParams f)
         const uint32_t v_lane = (wk * kMine + (lane & 15)) * 128;
         const uint32_t v_unit = ((lane >> 4) ^ (lane & 7)) * 16;
 
-        const float c = f.p.scale * kLog2e;
+        const float c = f.p.scale * kTreeLog2e;
         float o[kDt][4] = {};
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         for (int tile = 0; tile < tiles; ++tile) {
@@ -573,7 +399,7 @@ __global__ void __launch_bounds__(128) tree_fp32_kernel(const __grid_constant__ 
     if (blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
     asm volatile("griddepcontrol.launch_dependents;");
     Share s;
-    if (!share_of<S::kRows>(f, s)) return;
+    if (!share_of(f, s)) return;
     const int r = threadIdx.x >> 3, j8 = threadIdx.x & 7, G = f.p.Hq / f.p.Hkv;
     const int row = s.row0 + r;
     float *q = reinterpret_cast<float *>(smem + S::kQ), *w = reinterpret_cast<float *>(smem + S::kP);
@@ -618,7 +444,7 @@ __global__ void __launch_bounds__(128) tree_fp32_kernel(const __grid_constant__ 
         for (int j = 0; j < 4; ++j) {
             const int key = j8 + 8 * j, draft = pos + key - s.ctx;
             const bool see = (there >> key & 1) && (draft < 0 || (mine >> (draft & 63) & 1));
-            x[j] = see ? x[j] * f.p.scale * kLog2e : -INFINITY;
+            x[j] = see ? x[j] * f.p.scale * kTreeLog2e : -INFINITY;
             top = fmaxf(top, x[j]);
         }
 #pragma unroll
@@ -723,11 +549,15 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- host
+// More than 64 rows go to the tensor cores' kernel, where HBM bounds the call again
+// (96 rows over 33,000 cached tokens: 1.21 ms by mma.sync, whose rate bounds it).
+bool many_rows(const TreeProblem &p) { return p.R * (p.Hq / p.Hkv) > 64 && tree_tc_rows(p) > 0; }
+
 int rows_per_cta(const TreeProblem &p)
 {
     const int rows = p.R * (p.Hq / p.Hkv);
     if (p.dtype == KDA_DTYPE_F32 || rows <= 16) return 16;
-    return rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    return rows <= 32 ? 32 : many_rows(p) ? tree_tc_rows(p) : 64;
 }
 
 TreeParams plan(const TreeProblem &p)
@@ -735,13 +565,14 @@ TreeParams plan(const TreeProblem &p)
     TreeParams f{};
     f.p = p;
     f.rows = p.R * (p.Hq / p.Hkv);
-    const int per = rows_per_cta(p);
-    f.row_tiles = (f.rows + per - 1) / per;
+    f.tile_rows = rows_per_cta(p);
+    f.row_tiles = (f.rows + f.tile_rows - 1) / f.tile_rows;
+    f.tile_keys = many_rows(p) ? 128 : 64;
     // at most about 8192 CTAs, and 256 chunks to join
     const long long longest = (long long)p.M << p.page_shift;
     const long long units = (long long)p.N * p.Hkv * f.row_tiles;
     const long long most = units >= 8192 ? 1 : 8192 / units;
-    f.chunks = (int)std::min({(longest + 63) / 64, most, 256ll});
+    f.chunks = (int)std::min({(longest + f.tile_keys - 1) / f.tile_keys, most, 256ll});
     return f;
 }
 
@@ -814,15 +645,14 @@ cudaError_t launch(const TreeProblem &p, void *workspace, cudaStream_t st)
     } else {
         const int page = 1 << p.page_shift;
         f.pool_rows = p.P * p.Hkv * page;
-        if (page >= 8 &&
-            (!encode_pool_map(&f.k, p.k_pages, D, f.pool_rows, page < 64 ? page : 64) ||
-             !encode_pool_map(&f.v, p.v_pages, D, f.pool_rows, page < 64 ? page : 64)))
+        const int box = page < f.tile_keys ? page : f.tile_keys;
+        if (page >= 8 && (!encode_pool_map(&f.k, p.k_pages, D, f.pool_rows, box) ||
+                          !encode_pool_map(&f.v, p.v_pages, D, f.pool_rows, box)))
             return cudaErrorInvalidValue;
-        const int per = rows_per_cta(p);
-        e = per == 16   ? start_mma<D, 1, 4>(f, ctas, st)
-            : per == 32 ? start_mma<D, 2, 2>(f, ctas, st)
-            : per == 64 ? start_mma<D, 4, 1>(f, ctas, st)
-                        : start_mma<D, 8, 1>(f, ctas, st);
+        e = f.tile_rows == 16   ? start_mma<D, 1, 4>(f, ctas, st)
+            : f.tile_rows == 32 ? start_mma<D, 2, 2>(f, ctas, st)
+            : many_rows(p)      ? launch_tree_tc(f, ctas, st)
+                                : start_mma<D, 4, 1>(f, ctas, st);
     }
     if (e != cudaSuccess || f.chunks == 1) return e;
     const long long rows = (long long)p.N * p.R * p.Hq;

@@ -1,0 +1,190 @@
+// kda_attn_tree.cuh — what the kernels of tree attention share: the problem, a CTA's
+// share of it, which drafts a token sees, and how a row is finished.
+#pragma once
+
+#include "kda_attn_rows.cuh"
+#include "kda_attn_tc.cuh"
+
+namespace kda {
+
+constexpr float kTreeLog2e = 1.44269504088896340736f;
+constexpr float kTreeLn2 = 0.693147180559945309417f;
+
+// The drafted tokens that token i attends to, as bits: itself and its ancestors; 0
+// where it, or one of them, has a parent that is neither -1 nor an earlier token.
+__device__ __forceinline__ unsigned long long ancestors(const int32_t *parents, int i)
+{
+    unsigned long long seen = 0;
+    int j = i;
+    while (j >= 0) {
+        seen |= 1ull << j;
+        const int up = parents[j];
+        if (up < -1 || up >= j) return 0;
+        j = up;
+    }
+    return seen;
+}
+
+struct TreeParams {
+    TreeProblem p;
+    int rows;       // R * G
+    int tile_rows;  // of them per CTA
+    int row_tiles;  // CTAs that share a chunk's keys
+    int tile_keys;  // chunks are multiples of this
+    int chunks;     // most chunks of a sequence
+    float *part_o;  // [n, hk, chunk, row, D]: sums over e^(s - m) v
+    float2 *part_ml;
+    // bf16: the pools as rows of a head's channels, q as tokens of a kv head's G heads
+    // (tensor-core path for many rows), and where the waits report
+    CUtensorMap k, v, q;
+    int pool_rows;
+    int *status;
+    uint32_t spin;
+    int starve;
+};
+
+// Where key `pos` of a row of the table is, in elements; -1 where it has no page.
+__device__ __forceinline__ long long key_at(const TreeProblem &p, const int32_t *row, int pos,
+                                            int hk)
+{
+    const int id = __ldg(row + (pos >> p.page_shift));
+    if ((unsigned)id >= (unsigned)p.P) return -1;
+    return (((((long long)id * p.Hkv + hk) << p.page_shift) + (pos & ((1 << p.page_shift) - 1)))) * p.d;
+}
+
+__device__ __forceinline__ int ctx_of(const TreeProblem &p, int n)
+{
+    return min(max(p.ctx_lens[n], 0), p.M << p.page_shift);
+}
+
+__device__ __forceinline__ int end_of(const TreeProblem &p, int n)
+{
+    return min(ctx_of(p, n) + p.R, p.M << p.page_shift);
+}
+
+// Keys per chunk of a sequence of `end` keys. Lengths are known on the device only, so
+// every warp adds them up: chunks are to be small enough for about six CTAs per
+// resident place (two per SM) and no smaller than a tile, nor, as a chunk's fixed cost
+// is about a tile's, need they be below 2048 keys to balance the SMs.
+__device__ __forceinline__ int chunk_of(const TreeParams &f, int end)
+{
+    if (f.chunks == 1) return INT32_MAX;
+    constexpr int kCounted = 1024;  // sequences whose lengths are added up
+    int target = 2048;
+    if (f.p.N <= kCounted) {
+        long long total = 0;
+        for (int n = threadIdx.x & 31; n < f.p.N; n += 32) total += end_of(f.p, n);
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+        total = total * f.p.Hkv * f.row_tiles / (148 * 2 * 6);
+        target = (int)min(max(total, 64ll), 2048ll);
+    }
+    const int count = max(1, min(f.chunks, (end + target - 1) / target));
+    return ((end + count - 1) / count + f.tile_keys - 1) / f.tile_keys * f.tile_keys;
+}
+
+// One row from the keys it sees alone: one warp.
+template <typename T, int D>
+__device__ __noinline__ void tree_row(const TreeProblem &p, int n, int i, int h)
+{
+    constexpr int V = D / 32;
+    const int32_t *row = p.table + (size_t)n * p.M;
+    const int ctx = ctx_of(p, n), end = end_of(p, n);
+    const unsigned long long seen =
+        p.parents ? ancestors(p.parents + (size_t)n * p.R, i) : (2ull << i) - 1;
+    const size_t unit = ((size_t)n * p.R + i) * p.Hq + h;
+    const int hk = h / (p.Hq / p.Hkv);
+    float q[V], x[V], y[V];
+    load_row<T, D>(static_cast<const T *>(p.q) + unit * D, q);
+    RowSoftmax<V> sm;
+    bool any = false;
+    for (int c = 0; c < (seen ? end : 0); ++c) {
+        if (c >= ctx && !(seen >> (c - ctx) & 1)) continue;
+        const long long at = key_at(p, row, c, hk);
+        if (at < 0) continue;
+        load_row<T, D>(static_cast<const T *>(p.k_pages) + at, x);
+        load_row<T, D>(static_cast<const T *>(p.v_pages) + at, y);
+        sm.add(row_dot(q, x) * p.scale, y);
+        any = true;
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) y[e] = any ? sm.acc[e] / sm.l : 0.f;
+    store_row<T, D>(static_cast<T *>(p.o) + unit * D, y);
+    if (p.lse && (threadIdx.x & 31) == 0) p.lse[unit] = any ? sm.m + logf(sm.l) : -INFINITY;
+}
+
+// What a warp does with a row's finished sums (lane l: elements from l * D / 32 on, the
+// maximum m in log2 units, the sum l): the result, or the row again from its keys.
+template <typename T, int D>
+__device__ __forceinline__ void finish_row(const TreeProblem &p, int n, int i, int h, float m,
+                                           float l, bool absent, const float (&acc)[D / 32])
+{
+    const size_t unit = ((size_t)n * p.R + i) * p.Hq + h;
+    const bool none = absent || (m == -INFINITY && l == 0.f);
+    float y[D / 32], odd = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+        y[e] = none ? 0.f : acc[e] / l;
+        odd = fmaf(y[e], 0.f, odd);
+    }
+    if (__any_sync(0xffffffffu, !(odd == 0.f))) {
+        tree_row<T, D>(p, n, i, h);
+        return;
+    }
+    store_row<T, D>(static_cast<T *>(p.o) + unit * D, y);
+    if (p.lse && (threadIdx.x & 31) == 0) p.lse[unit] = none ? -INFINITY : m * kTreeLn2 + logf(l);
+}
+
+__device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, bool real)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(tc::smem_u32(dst)), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+
+// What both forms of the kernel know about their share.
+struct Share {
+    int n, hk, chunk, row0, ctx, first, last;  // keys [first, last)
+    const int32_t *table;
+    bool alone;  // the sequence's only chunk
+};
+
+__device__ __forceinline__ bool share_of(const TreeParams &f, Share &s)
+{
+    int x = blockIdx.x;  // the chunks that most sequences do not have come last
+    s.row0 = x % f.row_tiles * f.tile_rows; x /= f.row_tiles;
+    s.hk = x % f.p.Hkv; x /= f.p.Hkv;
+    s.n = x % f.p.N;
+    s.chunk = x / f.p.N;
+    s.ctx = ctx_of(f.p, s.n);
+    const int end = end_of(f.p, s.n), chunk = chunk_of(f, end);
+    s.alone = end <= chunk;
+    if (s.chunk && (s.alone || (long long)s.chunk * chunk >= end)) return false;
+    s.first = s.chunk ? s.chunk * chunk : 0;
+    s.last = s.alone ? end : min(s.first + chunk, end);
+    s.table = f.p.table + (size_t)s.n * f.p.M;
+    return true;  // an empty sequence's rows are still written
+}
+
+// The drafts that every drafted token sees, by the CTA's first S::kMaskThreads threads
+// (they meet in barrier 1).
+template <typename S>
+__device__ __forceinline__ const unsigned long long *tree_masks(const TreeParams &f, int n, char *smem)
+{
+    unsigned long long *seen = reinterpret_cast<unsigned long long *>(smem + S::kSeen);
+    int32_t *parents = reinterpret_cast<int32_t *>(smem + S::kParents);
+    const int i = threadIdx.x;
+    if (i < f.p.R) {
+        parents[i] = f.p.parents ? f.p.parents[(size_t)n * f.p.R + i] : -1;
+        if (!f.p.parents) seen[i] = (2ull << i) - 1;  // a chain
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(S::kMaskThreads) : "memory");
+    if (f.p.parents && i < f.p.R) seen[i] = ancestors(parents, i);
+    asm volatile("bar.sync 1, %0;" ::"n"(S::kMaskThreads) : "memory");
+    return seen;
+}
+
+// The tensor-core kernel for many rows (kda_attn_tree_tc.cu).
+int tree_tc_rows(const TreeProblem &p);  // rows per CTA; 0: it does not serve this problem
+cudaError_t launch_tree_tc(const TreeParams &f, long long ctas, cudaStream_t st);
+
+}  // namespace kda

@@ -133,6 +133,39 @@ def test_long_context(n_draft, dtype):
     check(x, None, scale=0.9)
 
 
+@pytest.mark.parametrize("page", [1, 4, 8, 64, 256])
+@pytest.mark.parametrize("Hq,Hkv,n_draft,d", [(8, 2, 24, 128), (8, 2, 40, 128), (6, 2, 43, 64), (3, 1, 64, 128),
+                                              (12, 1, 11, 32), (130, 1, 2, 32), (64, 1, 64, 64)])
+def test_many_rows(Hq, Hkv, n_draft, d, page):
+    """More rows than 64 per key/value head: one query tile, two, and more; short and long."""
+    ctx = [0, 3, 127, 128, 700, 4999]
+    x = cache(20, ctx, n_draft, page, Hq, Hkv, d, torch.bfloat16)
+    check(x, random_parents(21, len(ctx), n_draft, lost=0.1))
+    x[3][4, 300 // page] = -1  # a page is missing
+    x[3][5, :2 + 2000 // page] = 10 ** 6
+    check(x, None)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("n_draft", [20, 40])
+def test_many_rows_masked(n_draft, bad):
+    """As above with bad values off the path, behind the drafts and in a long chunked row."""
+    ctx, page = [5, 250, 4000], 64
+    q, kp, vp, table, c = cache(22, ctx, n_draft, page, 8, 2, 128, torch.bfloat16)
+    parents = random_parents(23, 3, n_draft)
+    parents[:, 1:] = torch.where(parents[:, 1:] == 1, 0, parents[:, 1:])  # nobody descends from draft 1
+    used = torch.zeros(kp.shape[0], page, dtype=torch.bool, device="cuda")
+    for n, x in enumerate(ctx):
+        for t in range(x + n_draft):
+            used[table[n, t // page].long(), t % page] = t != x + 1
+    kp, vp = (torch.where(used[:, None, :, None], x, bad) for x in (kp, vp))
+    o, lse = api().kda_attn_tree(q, kp, vp, table, c, parents=parents)
+    ro, rl, to, tl = R.attn_tree(q, kp, vp, table, c, parents, 128 ** -0.5)
+    assert torch.isfinite(ro[:, 2:]).all() and not torch.isfinite(ro[:, 1]).any()
+    R.close(o, ro, to)
+    R.close(lse, rl, tl)
+
+
 def test_late_maximum():
     q, kp, vp, table, ctx = cache(12, [3000], 2, 16, 2, 1, 64, torch.bfloat16)
     q[..., 0] = 6.0
