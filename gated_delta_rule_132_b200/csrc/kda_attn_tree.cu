@@ -153,55 +153,56 @@ __device__ __forceinline__ void join_rows(const TreeParams &f, const Share &s, c
 }
 
 // ---------------------------------------------------------------- bf16
-// The loading warp: 64 keys from pos on into a stage. Lane l looks up keys l and 32 + l;
-// returns which keys are the sequence's and have a page.
+// The loading warp: 64 keys from pos on into a stage, and which of them are there. By a
+// box per page (`page`: this lane's), or by 16-byte copies where pages have fewer than
+// eight tokens.
 template <int D, typename S>
-__device__ __forceinline__ void load_stage(const TreeParams &f, const Share &s, int pos, char *k,
+__device__ __forceinline__ void load_boxes(const TreeParams &f, const Share &s, int pos, int page,
+                                           char *k, uint64_t *full, unsigned long long *there)
+{
+    const Boxes<64> boxes(f);
+    const int lane = threadIdx.x & 31, row = boxes.row(f, s, pos, page);
+    const uint32_t lo = boxes.there(f, s, pos, row, 0), hi = boxes.there(f, s, pos, row, 1);
+    if (lane == 0) {
+        *there = (unsigned long long)hi << 32 | lo;
+        tc::mbar_arrive_expect_tx(full, 2 * S::kTile);
+    }
+    __syncwarp();
+    if (lane < boxes.count()) {
+#pragma unroll
+        for (int b = 0; b < S::kBlocks; ++b) {
+            char *to = k + b * S::kBlock + boxes.key() * 128;
+            tc::tma_load_2d(to, &f.k, b * 64, row, full);
+            tc::tma_load_2d(to + S::kTile, &f.v, b * 64, row, full);
+        }
+    }
+}
+
+template <int D, typename S>
+__device__ __forceinline__ void load_units(const TreeParams &f, const Share &s, int pos, char *k,
                                            uint64_t *full, unsigned long long *there)
 {
-    const int lane = threadIdx.x & 31, shift = f.p.page_shift;
-    int row[2];  // of the pool
+    constexpr int kUnits = D / 8;
+    const int lane = threadIdx.x & 31;
+    unsigned long long real = 0;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int c = pos + 32 * e + lane;
-        const long long at = c < s.last ? key_at(f.p, s.table, c, s.hk) : -1;
-        row[e] = at < 0 ? f.pool_rows : (int)(at / D);
+        real |= (unsigned long long)__ballot_sync(0xffffffffu, c < s.last && key_at(f.p, s.table, c, s.hk) >= 0)
+                << 32 * e;
     }
-    const unsigned lo = __ballot_sync(0xffffffffu, row[0] < f.pool_rows);
-    const unsigned hi = __ballot_sync(0xffffffffu, row[1] < f.pool_rows);
-    if (lane == 0) *there = (unsigned long long)hi << 32 | lo;
-    if (shift >= 3) {
-        // a box is the tile's part of a page; without a page it lies outside the pool
-        const int per = min(1 << shift, 64), boxes = 64 / per;
-        const int key = lane < boxes ? lane * per : 0;
-        const int low = __shfl_sync(0xffffffffu, row[0], key & 31);
-        const int high = __shfl_sync(0xffffffffu, row[1], key & 31);
-        if (lane == 0) tc::mbar_arrive_expect_tx(full, 2 * S::kTile);
-        __syncwarp();
-        if (lane < boxes) {
-            const int at = key < 32 ? low : high;
-#pragma unroll
-            for (int b = 0; b < S::kBlocks; ++b) {
-                char *to = k + b * S::kBlock + key * 128;
-                tc::tma_load_2d(to, &f.k, b * 64, at, full);
-                tc::tma_load_2d(to + S::kTile, &f.v, b * 64, at, full);
-            }
-        }
-    } else {
-        constexpr int kUnits = D / 8;
-        for (int i = lane; i < 64 * kUnits; i += 32) {
-            const int r = i / kUnits, u = i % kUnits;
-            const int c = pos + r;
-            const long long at = c < s.last ? key_at(f.p, s.table, c, s.hk) : -1;
-            const size_t from = (at < 0 ? 0 : (size_t)at * 2) + u * 16;
-            char *to = k + (u >> 3) * S::kBlock + tc::sw128(r, (u & 7) * 16);
-            cp_async16_or_zero(to, static_cast<const char *>(f.p.k_pages) + from, at >= 0);
-            cp_async16_or_zero(to + S::kTile, static_cast<const char *>(f.p.v_pages) + from, at >= 0);
-        }
-        tc::cp_async_arrive(full);
-        if (lane == 0) tc::mbar_arrive(full);
-        __syncwarp();
+    if (lane == 0) *there = real;
+    for (int i = lane; i < 64 * kUnits; i += 32) {
+        const int r = i / kUnits, u = i % kUnits;
+        const bool is = real >> r & 1;
+        const size_t from = (is ? (size_t)key_at(f.p, s.table, pos + r, s.hk) * 2 : 0) + u * 16;
+        char *to = k + (u >> 3) * S::kBlock + tc::sw128(r, (u & 7) * 16);
+        cp_async16_or_zero(to, static_cast<const char *>(f.p.k_pages) + from, is);
+        cp_async16_or_zero(to + S::kTile, static_cast<const char *>(f.p.v_pages) + from, is);
     }
+    tc::cp_async_arrive(full);
+    if (lane == 0) tc::mbar_arrive(full);
+    __syncwarp();
 }
 
 template <int D, int kWm, int kWk>
@@ -235,12 +236,17 @@ tree_mma_kernel(const __grid_constant__ TreeParams f)
 
     if (warp == S::kWarps) {
         if (!f.starve) {
-            int tile = 0;
+            const bool by_page = f.p.page_shift >= 3;
+            int tile = 0, page = by_page && tiles ? Boxes<64>(f).page(f, s, s.first) : 0;
             for (; tile < tiles; ++tile) {
-                const int st = tile % kStages, use = tile / kStages;
+                const int st = tile % kStages, use = tile / kStages, pos = s.first + tile * S::kKeys;
+                char *to = smem + st * 2 * S::kTile;
+                const int next = by_page ? Boxes<64>(f).page(f, s, pos + S::kKeys) : 0;
                 const bool go = !use || tc::mbar_wait(free + st, (use - 1) & 1, abort, f.status, kErrTreeFree, f.spin);
                 if (!__all_sync(0xffffffffu, go)) break;
-                load_stage<D, S>(f, s, s.first + tile * S::kKeys, smem + st * 2 * S::kTile, full + st, there_of + st);
+                if (by_page) load_boxes<D, S>(f, s, pos, page, to, full + st, there_of + st);
+                else load_units<D, S>(f, s, pos, to, full + st, there_of + st);
+                page = next;
             }
             // whatever the other warps do, the copies land before the memory is used again
             for (int i = max(0, tile - kStages); i < tile; ++i)
@@ -568,11 +574,16 @@ TreeParams plan(const TreeProblem &p)
     f.tile_rows = rows_per_cta(p);
     f.row_tiles = (f.rows + f.tile_rows - 1) / f.tile_rows;
     f.tile_keys = many_rows(p) ? 128 : 64;
-    // at most about 8192 CTAs, and 256 chunks to join
+    // mma.sync: two CTAs to an SM, a chunk's fixed cost is about a tile's: six rounds of
+    // them balance the SMs. Many rows: one CTA to an SM, whose beginning and end cost four
+    // tiles or so: three rounds (24 drafts over 16 contexts of 1024..65536: XX us; chunks
+    // of 2048 keys 731 us).
     const long long longest = (long long)p.M << p.page_shift;
     const long long units = (long long)p.N * p.Hkv * f.row_tiles;
-    const long long most = units >= 8192 ? 1 : 8192 / units;
-    f.chunks = (int)std::min({(longest + f.tile_keys - 1) / f.tile_keys, most, 256ll});
+    const long long ctas = many_rows(p) ? 148 * 8 : 8192;
+    f.places = many_rows(p) ? 148 * 3 : 148 * 2 * 6;
+    f.most_keys = many_rows(p) ? 1 << 20 : 2048;
+    f.chunks = (int)std::min({(longest + f.tile_keys - 1) / f.tile_keys, std::max(ctas / units, 1ll), 256ll});
     return f;
 }
 

@@ -32,6 +32,8 @@ struct TreeParams {
     int row_tiles;  // CTAs that share a chunk's keys
     int tile_keys;  // chunks are multiples of this
     int chunks;     // most chunks of a sequence
+    int places;     // CTAs that a call should have
+    int most_keys;  // of a chunk, where there is a choice
     float *part_o;  // [n, hk, chunk, row, D]: sums over e^(s - m) v
     float2 *part_ml;
     // bf16: the pools as rows of a head's channels, q as tokens of a kv head's G heads
@@ -63,9 +65,8 @@ __device__ __forceinline__ int end_of(const TreeProblem &p, int n)
 }
 
 // Keys per chunk of a sequence of `end` keys. Lengths are known on the device only, so
-// every warp adds them up: chunks are to be small enough for about six CTAs per
-// resident place (two per SM) and no smaller than a tile, nor, as a chunk's fixed cost
-// is about a tile's, need they be below 2048 keys to balance the SMs.
+// every warp adds them up: chunks are to give about f.places CTAs, no smaller than a
+// tile and no larger than f.most_keys.
 __device__ __forceinline__ int chunk_of(const TreeParams &f, int end)
 {
     if (f.chunks == 1) return INT32_MAX;
@@ -76,8 +77,8 @@ __device__ __forceinline__ int chunk_of(const TreeParams &f, int end)
         for (int n = threadIdx.x & 31; n < f.p.N; n += 32) total += end_of(f.p, n);
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-        total = total * f.p.Hkv * f.row_tiles / (148 * 2 * 6);
-        target = (int)min(max(total, 64ll), 2048ll);
+        total = total * f.p.Hkv * f.row_tiles / f.places;
+        target = (int)min(max(total, (long long)f.tile_keys), (long long)f.most_keys);
     }
     const int count = max(1, min(f.chunks, (end + target - 1) / target));
     return ((end + count - 1) / count + f.tile_keys - 1) / f.tile_keys * f.tile_keys;
@@ -182,6 +183,38 @@ __device__ __forceinline__ const unsigned long long *tree_masks(const TreeParams
     asm volatile("bar.sync 1, %0;" ::"n"(S::kMaskThreads) : "memory");
     return seen;
 }
+
+// The pages of a tile of kKeys keys, as a loading warp sees them (pages of at least eight
+// tokens): a box per page, or one where a page covers the tile; lane b < boxes has box b.
+template <int kKeys> struct Boxes {
+    int shift;  // log2 of a box's keys
+    __device__ __forceinline__ explicit Boxes(const TreeParams &f)
+        : shift(min(f.p.page_shift, kKeys == 64 ? 6 : 7)) {}
+    __device__ __forceinline__ int count() const { return kKeys >> shift; }
+    __device__ __forceinline__ int key() const { return (threadIdx.x & 31) << shift; }  // the box's first
+
+    // This lane's page of the tile at pos: a table entry, read well before it is used.
+    __device__ __forceinline__ int page(const TreeParams &f, const Share &s, int pos) const
+    {
+        const int c = pos + key();
+        return key() < kKeys && c < s.last ? __ldg(s.table + (c >> f.p.page_shift)) : -1;
+    }
+    // Its box's first row of the pool; behind the pool (reads zero) where there is no page.
+    __device__ __forceinline__ int row(const TreeParams &f, const Share &s, int pos, int page) const
+    {
+        if ((unsigned)page >= (unsigned)f.p.P) return f.pool_rows;
+        return ((page * f.p.Hkv + s.hk) << f.p.page_shift) +
+               ((pos + key()) & ((1 << f.p.page_shift) - 1));
+    }
+    // Bit l: key 32 e + l of the tile is the sequence's and has a page.
+    __device__ __forceinline__ uint32_t there(const TreeParams &f, const Share &s, int pos, int row,
+                                              int e) const
+    {
+        const int key = 32 * e + (threadIdx.x & 31);
+        const int of = __shfl_sync(0xffffffffu, row, key >> shift);
+        return __ballot_sync(0xffffffffu, of < f.pool_rows && pos + key < s.last);
+    }
+};
 
 // The tensor-core kernel for many rows (kda_attn_tree_tc.cu).
 int tree_tc_rows(const TreeProblem &p);  // rows per CTA; 0: it does not serve this problem

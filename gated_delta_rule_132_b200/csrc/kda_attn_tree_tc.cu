@@ -41,67 +41,38 @@ struct TcShape {
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-// The loading warp: 128 keys from pos on of one pool into a stage, four to a lane.
-// Returns which of them are the sequence's and have a page (lane l: keys 32 e + l).
-struct Keys {
-    int row[4];          // of the pool; pool_rows: none
-    unsigned there[4];
-};
-
+// A loading warp: 128 keys from pos on of one pool into a stage, by a box per page.
 template <int D>
-__device__ __forceinline__ Keys look_up(const TreeParams &f, const Share &s, int pos)
+__device__ __forceinline__ void load_boxes(const Boxes<kTileRows> &boxes, int row, const CUtensorMap *map,
+                                           uint8_t *to, uint64_t *full)
 {
-    Keys k;
     const int lane = threadIdx.x & 31;
+    if (lane == 0) tc::mbar_arrive_expect_tx(full, TileShape<D>::kBytes);
+    __syncwarp();
+    if (lane < boxes.count()) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int c = pos + 32 * e + lane;
-        const long long at = c < s.last ? key_at(f.p, s.table, c, s.hk) : -1;
-        k.row[e] = at < 0 ? f.pool_rows : (int)(at / D);
-        k.there[e] = __ballot_sync(0xffffffffu, at >= 0);
+        for (int b = 0; b < TileShape<D>::kBlocks; ++b)
+            tc::tma_load_2d(to + b * kBlockBytes + boxes.key() * 128, map, b * 64, row, full);
     }
-    return k;
 }
 
+// The same by 16-byte copies, where pages have fewer than eight tokens.
 template <int D>
-__device__ __forceinline__ void load_keys(const TreeParams &f, const Keys &keys, const CUtensorMap *map,
-                                          const void *pool, uint8_t *to, uint64_t *full)
+__device__ __forceinline__ void load_units(const TreeParams &f, const Share &s, int pos, const void *pool,
+                                           uint8_t *to, uint64_t *full)
 {
-    const int lane = threadIdx.x & 31, shift = f.p.page_shift;
-    if (shift >= 3) {
-        // a box is the tile's part of a page; without a page it lies outside the pool
-        const int per = min(1 << shift, kTileRows), boxes = kTileRows / per;
-        const int key = lane < boxes ? lane * per : 0;
-        int at = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int x = __shfl_sync(0xffffffffu, keys.row[e], key & 31);
-            if (key >> 5 == e) at = x;
-        }
-        if (lane == 0) tc::mbar_arrive_expect_tx(full, TileShape<D>::kBytes);
-        __syncwarp();
-        if (lane < boxes) {
-#pragma unroll
-            for (int b = 0; b < TileShape<D>::kBlocks; ++b)
-                tc::tma_load_2d(to + b * kBlockBytes + key * 128, map, b * 64, at, full);
-        }
-    } else {
-        constexpr int kUnits = D / 8;
-        for (int r = 0; r < kTileRows; ++r) {
-            const int e = r >> 5;
-            const int row = __shfl_sync(0xffffffffu, e == 0 ? keys.row[0] : e == 1 ? keys.row[1]
-                                                     : e == 2 ? keys.row[2] : keys.row[3], r & 31);
-            const bool real = row < f.pool_rows;
-            if (lane < kUnits)
-                cp_async16_or_zero(to + (lane >> 3) * kBlockBytes + tc::sw128(r, (lane & 7) * 16),
-                                   static_cast<const char *>(pool) + ((size_t)(real ? row : 0) * D) * 2 + lane * 16,
-                                   real);
-        }
-        tc::cp_async_wait_all();
-        tc::fence_proxy_async_smem();  // the tensor cores read what these copies wrote
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(full);
+    constexpr int kUnits = D / 8;
+    const int lane = threadIdx.x & 31;
+    for (int i = lane; i < kTileRows * kUnits; i += 32) {
+        const int r = i / kUnits, u = i % kUnits;
+        const long long at = pos + r < s.last ? key_at(f.p, s.table, pos + r, s.hk) : -1;
+        cp_async16_or_zero(to + (u >> 3) * kBlockBytes + tc::sw128(r, (u & 7) * 16),
+                           static_cast<const char *>(pool) + (at < 0 ? 0 : (size_t)at * 2) + u * 16, at >= 0);
     }
+    tc::cp_async_wait_all();
+    tc::fence_proxy_async_smem();  // the tensor cores read what these copies wrote
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(full);
 }
 
 template <int D>
@@ -165,8 +136,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 
     if (warp >= 8) {
         tc::fewer_registers<kRegsOther>();
-        if (warp == 9 && !f.starve) {
-            if (lane == 0) {
+        // one warp loads the keys (and q), one the values and which keys are there
+        if ((warp == 9 || warp == 10) && !f.starve) {
+            const bool keys = warp == 9, by_page = f.p.page_shift >= 3;
+            if (keys && lane == 0) {
                 tc::mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * TileShape<D>::kBlocks * rows * 128);
                 for (int w = 0; w <= two; ++w)
                     for (int b = 0; b < TileShape<D>::kBlocks; ++b)
@@ -174,30 +147,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
                                         s.n * f.p.R + i0 + w * tokens, q_full);
             }
             __syncwarp();
-            int it = 0;
-            bool half = false;  // the keys of step `it` are under way, its values are not
+            const Boxes<kTileRows> boxes(f);
+            uint64_t *full = keys ? k_full : v_full, *free = keys ? k_free : v_free;
+            uint8_t *ring = sm + (keys ? S::kK : S::kV);
+            const CUtensorMap *map = keys ? &f.k : &f.v;
+            int it = 0, page = by_page && steps ? boxes.page(f, s, s.first) : 0;
             for (; it < steps; ++it) {
-                const int st = it % S::kStages, use = it / S::kStages;
-                const Keys keys = look_up<D>(f, s, s.first + it * kTileRows);
-                bool go = !use || tc::mbar_wait(k_free + st, (use - 1) & 1, abort, f.status, kErrFree, f.spin);
+                const int st = it % S::kStages, use = it / S::kStages, pos = s.first + it * kTileRows;
+                const int next = by_page ? boxes.page(f, s, pos + kTileRows) : 0;
+                const bool go = !use || tc::mbar_wait(free + st, (use - 1) & 1, abort, f.status, kErrFree, f.spin);
                 if (!__all_sync(0xffffffffu, go)) break;
-                load_keys<D>(f, keys, &f.k, f.p.k_pages, sm + S::kK + st * S::kTile, k_full + st);
-                go = !use || tc::mbar_wait(v_free + st, (use - 1) & 1, abort, f.status, kErrFree, f.spin);
-                half = !__all_sync(0xffffffffu, go);
-                if (half) break;
-                if (lane < 4)
-                    there_of[st * 4 + lane] = lane == 0 ? keys.there[0] : lane == 1 ? keys.there[1]
-                                              : lane == 2 ? keys.there[2] : keys.there[3];
-                __syncwarp();
-                load_keys<D>(f, keys, &f.v, f.p.v_pages, sm + S::kV + st * S::kTile, v_full + st);
+                const int row = by_page ? boxes.row(f, s, pos, page) : 0;
+                if (!keys) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t there =
+                            by_page ? boxes.there(f, s, pos, row, e)
+                                    : __ballot_sync(0xffffffffu, pos + 32 * e + lane < s.last &&
+                                                                     key_at(f.p, s.table, pos + 32 * e + lane, s.hk) >= 0);
+                        if (lane == 0) there_of[st * 4 + e] = there;
+                    }
+                }
+                if (by_page) load_boxes<D>(boxes, row, map, ring + st * S::kTile, full + st);
+                else load_units<D>(f, s, pos, keys ? f.p.k_pages : f.p.v_pages, ring + st * S::kTile, full + st);
+                page = next;
             }
             // whatever the other warps do, the copies land before the memory is let go
             if (lane == 0) {
-                tc::mbar_drain(q_full, 0, f.status, kErrDrain);
-                for (int i = max(0, it + half - S::kStages); i < it + half; ++i)
-                    tc::mbar_drain(k_full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
+                if (keys) tc::mbar_drain(q_full, 0, f.status, kErrDrain);
                 for (int i = max(0, it - S::kStages); i < it; ++i)
-                    tc::mbar_drain(v_full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
+                    tc::mbar_drain(full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
             }
         }
         if (warp == 8 && lane == 0) {
