@@ -576,7 +576,7 @@ TreeParams plan(const TreeProblem &p)
     f.tile_keys = many_rows(p) ? 128 : 64;
     // mma.sync: two CTAs to an SM, a chunk's fixed cost is about a tile's: six rounds of
     // them balance the SMs. Many rows: one CTA to an SM, whose beginning and end cost four
-    // tiles or so: three rounds (24 drafts over 16 contexts of 1024..65536: XX us; chunks
+    // tiles or so: three rounds (24 drafts over 16 contexts of 1024..65536: 599 us; chunks
     // of 2048 keys 731 us).
     const long long longest = (long long)p.M << p.page_shift;
     const long long units = (long long)p.N * p.Hkv * f.row_tiles;
