@@ -256,24 +256,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
                 }
             }
         }
-        if (warp == 8 && lane == 0) {
+        if (warp == 8) {
+            const uint32_t lead = lane == 0;
             const uint32_t k = tc::smem_u32(sm + S::kStay), v = k + S::kTile;
             const uint32_t q = tc::smem_u32(sm + S::kRing0), dO = tc::smem_u32(sm + S::kRing1);
             auto wait = [&](uint64_t *bar, int n, int code) {
-                return tc::mbar_wait(bar, n & 1, b.abort, f.status, code, f.spin);
+                return __all_sync(0xffffffffu, tc::mbar_wait(bar, n & 1, b.abort, f.status, code, f.spin));
             };
             auto s_step = [&](int it) {
                 const int st = it % S::kStages;
                 if (!wait(b.full0 + st, it / S::kStages, kErrA)) return false;
-                tc::mma_rows_rows<D>(tmem + kS, k, q + st * S::kTile);
-                tc::mma_commit(b.s_full);
+                tc::mma_rows_rows<D>(tmem + kS, k, q + st * S::kTile, lead);
+                tc::commit(b.s_full, lead);
                 return true;
             };
             auto dp_step = [&](int it) {
                 const int st = it % S::kStages;
                 if (!wait(b.full1 + st, it / S::kStages, kErrB)) return false;
-                tc::mma_rows_rows<D>(tmem + kDp, v, dO + st * S::kTile);
-                tc::mma_commit(b.dp_full);
+                tc::mma_rows_rows<D>(tmem + kDp, v, dO + st * S::kTile, lead);
+                tc::commit(b.dp_full, lead);
                 return true;
             };
             bool go = wait(b.stay, 0, kErrStay) && s_step(0) && dp_step(0);
@@ -282,18 +283,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
                 go = wait(b.p_full, it, kErrP);
                 if (!go) break;
                 tc::tc_fence_after_sync();
-                tc::mma_weights_rows<D, 64>(tmem + kDv, tmem + kS, dO + st * S::kTile, it > 0);
-                tc::mma_commit(b.free1 + st);
+                tc::mma_weights_rows<D, 64>(tmem + kDv, tmem + kS, dO + st * S::kTile, it > 0, lead);
+                tc::commit(b.free1 + st, lead);
                 if (it + 1 < steps) go = s_step(it + 1);
                 if (!go) break;
                 go = wait(b.ds_full, it, kErrDs);
                 if (!go) break;
                 tc::tc_fence_after_sync();
-                tc::mma_weights_rows<D, 64>(tmem + kDk, tmem + kDp, q + st * S::kTile, it > 0);
-                tc::mma_commit(b.free0 + st);
+                tc::mma_weights_rows<D, 64>(tmem + kDk, tmem + kDp, q + st * S::kTile, it > 0, lead);
+                tc::commit(b.free0 + st, lead);
                 if (it + 1 < steps) go = dp_step(it + 1);
             }
-            tc::mma_commit(b.acc);
+            tc::commit(b.acc, lead);
             tc::mbar_drain(b.acc, 0, f.status, kErrBwdDrain);
         }
     } else {
@@ -416,25 +417,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
             for (int i = max(0, it - S::kStages); i < it; ++i)
                 tc::mbar_drain(b.full1 + i % S::kStages, (i / S::kStages) & 1, f.status, kErrBwdDrain);
         }
-        if (warp == 8 && lane == 0) {
+        if (warp == 8) {
+            const uint32_t lead = lane == 0;
             const uint32_t q = tc::smem_u32(sm + S::kStay), dO = q + S::kTile;
             const uint32_t k = tc::smem_u32(sm + S::kRing0), v = tc::smem_u32(sm + S::kRing1);
             auto wait = [&](uint64_t *bar, int n, int code) {
-                return tc::mbar_wait(bar, n & 1, b.abort, f.status, code, f.spin);
+                return __all_sync(0xffffffffu, tc::mbar_wait(bar, n & 1, b.abort, f.status, code, f.spin));
             };
             auto s_step = [&](int it) {
                 const int st = it % S::kStages0;
                 if (!wait(b.full0 + st, it / S::kStages0, kErrA)) return false;
-                tc::mma_rows_rows<D>(tmem + kS + (it & 1) * 128, q, k + st * S::kTile);
-                tc::mma_commit(b.s_full + (it & 1));
+                tc::mma_rows_rows<D>(tmem + kS + (it & 1) * 128, q, k + st * S::kTile, lead);
+                tc::commit(b.s_full + (it & 1), lead);
                 return true;
             };
             auto dp_step = [&](int it) {
                 const int st = it % S::kStages;
                 if (!wait(b.full1 + st, it / S::kStages, kErrB)) return false;
-                tc::mma_rows_rows<D>(tmem + kDp, dO, v + st * S::kTile);
-                tc::mma_commit(b.dp_full);
-                tc::mma_commit(b.free1 + st);
+                tc::mma_rows_rows<D>(tmem + kDp, dO, v + st * S::kTile, lead);
+                tc::commit(b.dp_full, lead);
+                tc::commit(b.free1 + st, lead);
                 return true;
             };
             bool go = wait(b.stay, 0, kErrStay) && s_step(0) && dp_step(0) && (steps < 2 || s_step(1));
@@ -443,12 +445,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
                 go = wait(b.ds_full, it, kErrDs);
                 if (!go) break;
                 tc::tc_fence_after_sync();
-                tc::mma_weights_rows<D, 64>(tmem + kDq, tmem + kDp, k + st * S::kTile, it > 0);
-                tc::mma_commit(b.free0 + st);
+                tc::mma_weights_rows<D, 64>(tmem + kDq, tmem + kDp, k + st * S::kTile, it > 0, lead);
+                tc::commit(b.free0 + st, lead);
                 if (it + 1 < steps) go = dp_step(it + 1);
                 if (go && it + 2 < steps) go = s_step(it + 2);
             }
-            tc::mma_commit(b.acc);
+            tc::commit(b.acc, lead);
             tc::mbar_drain(b.acc, 0, f.status, kErrBwdDrain);
         }
     } else {

@@ -136,37 +136,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 tc::mbar_drain(v_full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
             }
         }
-        if (warp == 8 && lane == 0) {
+        if (warp == 8) {
+            const uint32_t lead = lane == 0;
             const uint32_t q = tc::smem_u32(sm + S::kQ), k = tc::smem_u32(sm + S::kK),
                            v = tc::smem_u32(sm + S::kV);
-            bool go = tc::mbar_wait(q_full, 0, abort, f.status, kErrQ, f.spin);
+            auto wait = [&](uint64_t *bar, int n, int code) {
+                return __all_sync(0xffffffffu, tc::mbar_wait(bar, n & 1, abort, f.status, code, f.spin));
+            };
+            bool go = wait(q_full, 0, kErrQ);
             // O_w += P_w(it) V(it)
             auto pv = [&](int w, int begin, int it) {
                 const int st = it % S::kStages;
-                go = go && tc::mbar_wait(v_full + st, (it / S::kStages) & 1, abort, f.status, kErrV, f.spin) &&
-                     tc::mbar_wait(p_full + w, (it - begin) & 1, abort, f.status, kErrP, f.spin);
+                go = go && wait(v_full + st, it / S::kStages, kErrV) && wait(p_full + w, it - begin, kErrP);
                 if (!go) return;
                 tc::tc_fence_after_sync();
                 tc::mma_weights_rows<D, 32>(tmem + S::kTmemO + w * D, tmem + S::kTmemS + w * 128,
-                                        v + st * S::kTile, it > begin);
+                                            v + st * S::kTile, it > begin, lead);
             };
             for (int it = 0; it < steps && go; ++it) {
                 const int st = it % S::kStages;
-                go = tc::mbar_wait(k_full + st, (it / S::kStages) & 1, abort, f.status, kErrK, f.spin);
+                go = wait(k_full + st, it / S::kStages, kErrK);
                 for (int w = 0; w <= two && go; ++w) {
                     const int begin = two && w == 0;
                     if (it < begin) continue;
                     if (it > begin) pv(w, begin, it - 1);
                     if (!go) break;
-                    tc::mma_rows_rows<D>(tmem + S::kTmemS + w * 128, q + w * S::kTile, k + st * S::kTile);
-                    tc::mma_commit(s_full + w);
+                    tc::mma_rows_rows<D>(tmem + S::kTmemS + w * 128, q + w * S::kTile, k + st * S::kTile, lead);
+                    tc::commit(s_full + w, lead);
                 }
                 if (!go) break;
-                tc::mma_commit(k_free + st);
-                if (it > 0) tc::mma_commit(v_free + (it - 1) % S::kStages);
+                tc::commit(k_free + st, lead);
+                if (it > 0) tc::commit(v_free + (it - 1) % S::kStages, lead);
             }
             for (int w = 0; w <= two && go; ++w) pv(w, two && w == 0, steps - 1);
-            tc::mma_commit(o_full);
+            tc::commit(o_full, lead);
             tc::mbar_drain(o_full, 0, f.status, kErrDrain);
         }
     } else {

@@ -85,26 +85,50 @@ __device__ __forceinline__ void tma_load_4d(void *dst_smem, const void *tmap, in
                    "r"(smem_u32(bar)) : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem desc], bf16 inputs, fp32 accumulate.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate)
+// The warp that issues the MMAs runs its loop with all lanes and lets one of them
+// (`lead`) issue by predicate: control flow and descriptors stay uniform, so they are kept
+// in uniform registers. Issued from a single-lane branch, each instruction cost the
+// moves of its operands there.
+
+// D[tmem] (+)= A[smem desc] * B[smem desc], bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate, uint32_t lead)
 {
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
                  : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc].
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate, uint32_t lead)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+                 : "memory");
+}
+
+// The lead's arrival on `bar` once all it has issued is complete.
+__device__ __forceinline__ void commit(uint64_t *bar, uint32_t lead)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 ::"r"(smem_u32(bar)), "r"(lead) : "memory");
 }
 
 // acc[128 x 128] = X Y^T over the channels of two tiles.
 template <int D>
-__device__ __forceinline__ void mma_rows_rows(uint32_t acc, uint32_t x, uint32_t y)
+__device__ __forceinline__ void mma_rows_rows(uint32_t acc, uint32_t x, uint32_t y, uint32_t lead)
 {
     const uint64_t a = smem_desc(x, 16, 1024), b = smem_desc(y, 16, 1024);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
         const uint32_t off = ((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4;
-        mma_bf16(acc, a + off, b + off, idesc_bf16(128, 128, 0, 0), k > 0);
+        mma_ss(acc, a + off, b + off, idesc_bf16(128, 128, 0, 0), k > 0, lead);
     }
 }
 
@@ -112,13 +136,13 @@ __device__ __forceinline__ void mma_rows_rows(uint32_t acc, uint32_t x, uint32_t
 // first 64 tokens and 32 more that begin kHalf columns on; Y a tile read along its tokens.
 template <int D, int kHalf>
 __device__ __forceinline__ void mma_weights_rows(uint32_t acc, uint32_t w, uint32_t y,
-                                                 bool accumulate)
+                                                 bool accumulate, uint32_t lead)
 {
     const uint64_t b = smem_desc(y, kBlockBytes, 1024);
 #pragma unroll
     for (int k = 0; k < kTileRows / 16; ++k)
-        mma_bf16_ta(acc, w + (k >> 2) * kHalf + (k & 3) * 8, b + ((k * 2048) >> 4), idesc_bf16(128, D, 0, 1),
-                    accumulate || k > 0);
+        mma_ts(acc, w + (k >> 2) * kHalf + (k & 3) * 8, b + ((k * 2048) >> 4),
+               idesc_bf16(128, D, 0, 1), accumulate || k > 0, lead);
 }
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -198,6 +222,33 @@ __device__ __forceinline__ float exp2_fast(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 2^x for two numbers on the FMA pipe, to share the exponentials with the special-function
+// unit (16 a cycle and SM, the softmax's bound). x = n + r with n the nearest integer (x + 1.5 * 2^23
+// leaves n in the low mantissa bits) and |r| <= 1/2; 2^r by the polynomial of degree 4
+// with p(0) = 1 whose largest relative error is smallest (2.9e-6, fitted by Lawson's
+// iteration); n is added to the exponent. Below 2^-127 the result is 0; a NaN or an
+// infinity gives a number that is huge or NaN, so that it shows in the row's result.
+__device__ __forceinline__ void exp2_fma(f32x2 x, float &a, float &b)
+{
+    unpack2(x, a, b);
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(a));  // -127
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(b));
+    x = pack2(a, b);
+    const f32x2 big = pack2(12582912.f, 12582912.f);
+    const f32x2 n = add2(x, big);
+    const f32x2 r = fma2(add2(n, pack2(-12582912.f, -12582912.f)), pack2(-1.f, -1.f), x);
+    f32x2 p = fma2(pack2(0.009582855738699436f, 0.009582855738699436f), r,
+                   pack2(0.05590642988681793f, 0.05590642988681793f));
+    p = fma2(p, r, pack2(0.24024099111557007f, 0.24024099111557007f));
+    p = fma2(p, r, pack2(0.6931241750717163f, 0.6931241750717163f));
+    p = fma2(p, r, pack2(1.f, 1.f));
+    float na, nb;
+    unpack2(n, na, nb);
+    unpack2(p, a, b);
+    a = __int_as_float(__float_as_int(a) + (__float_as_int(na) << 23));
+    b = __int_as_float(__float_as_int(b) + (__float_as_int(nb) << 23));
 }
 
 // lo in the lower half: the operand's element order.
