@@ -57,7 +57,7 @@ enum : int { kErrStay = 111, kErrA, kErrB, kErrFree, kErrS, kErrDp, kErrP, kErrD
              kErrBwdDrain };
 
 struct Bars {
-    uint64_t *stay, *full0, *free0, *full1, *free1, *s_full, *dp_full, *p_full, *ds_full, *acc;
+    uint64_t *stay, *full0, *free0, *full1, *free1, *s_full, *s_free, *dp_full, *p_full, *ds_full, *acc;
     uint32_t *tmem_slot;
     volatile int *abort;
     uint32_t *bad;  // [4] rows to compute again
@@ -67,7 +67,7 @@ struct Bars {
         stay = reinterpret_cast<uint64_t *>(at);
         full0 = stay + 1; free0 = full0 + kMost;
         full1 = free0 + kMost; free1 = full1 + kMost;
-        s_full = free1 + kMost; dp_full = s_full + 2; p_full = dp_full + 1;
+        s_full = free1 + kMost; s_free = s_full + 2; dp_full = s_free + 2; p_full = dp_full + 1;
         ds_full = p_full + 1; acc = ds_full + 1;
         tmem_slot = reinterpret_cast<uint32_t *>(acc + 1);
         abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -75,7 +75,9 @@ struct Bars {
     }
 };
 
-__device__ __forceinline__ uint32_t start_cta(const Bars &b, int full0_count)
+// full0_count: arrivals that fill a stage of the first ring; free1_count: that free one of
+// the second (the first is always freed by two).
+__device__ __forceinline__ uint32_t start_cta(const Bars &b, int full0_count, int free1_count)
 {
     const int warp = threadIdx.x >> 5;
     if (warp == 8) tc::tmem_alloc(b.tmem_slot, 512);
@@ -83,16 +85,18 @@ __device__ __forceinline__ uint32_t start_cta(const Bars &b, int full0_count)
         tc::mbar_init(b.stay, 1);
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(b.full0 + i, full0_count);
-            tc::mbar_init(b.free0 + i, 1);
+            tc::mbar_init(b.free0 + i, 2);
             tc::mbar_init(b.full1 + i, 1);
-            tc::mbar_init(b.free1 + i, 1);
+            tc::mbar_init(b.free1 + i, free1_count);
         }
         tc::mbar_init(b.s_full, 1);
         tc::mbar_init(b.s_full + 1, 1);
+        tc::mbar_init(b.s_free, 8);
+        tc::mbar_init(b.s_free + 1, 8);
         tc::mbar_init(b.dp_full, 1);
         tc::mbar_init(b.p_full, 8);
         tc::mbar_init(b.ds_full, 8);
-        tc::mbar_init(b.acc, 1);
+        tc::mbar_init(b.acc, 2);
         *b.abort = 0;
         for (int i = 0; i < 4; ++i) b.bad[i] = 0;
         tc::fence_mbar_init();
@@ -212,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     t.first = t.seq_start + tile * kTileRows;
     const int per_head = count - tile, steps = per_head * G;  // step = (head, query tile)
 
-    const uint32_t tmem = start_cta(b, 1 + 32);
+    const uint32_t tmem = start_cta(b, 1 + 32, 2);
     constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 256 + D;
     const float *stats = reinterpret_cast<const float *>(sm + S::kStats);
 
@@ -256,43 +260,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
                 }
             }
         }
-        if (warp == 8) {
+        // warp 8 issues S and dV, warp 10 dP and dK: what a product reads in TMEM its warp's
+        // next one overwrites, in the order of issue
+        if (warp == 8 || warp == 10) {
+            const bool first = warp == 8;
             const uint32_t lead = lane == 0;
-            const uint32_t k = tc::smem_u32(sm + S::kStay), v = k + S::kTile;
+            const uint32_t stay = tc::smem_u32(sm + S::kStay) + (first ? 0 : S::kTile);
             const uint32_t q = tc::smem_u32(sm + S::kRing0), dO = tc::smem_u32(sm + S::kRing1);
+            const uint32_t rows = first ? q : dO, back = first ? dO : q;
+            const uint32_t pair = tmem + (first ? kS : kDp), acc = tmem + (first ? kDv : kDk);
+            uint64_t *rows_full = first ? b.full0 : b.full1, *back_full = first ? b.full1 : b.full0;
+            uint64_t *back_free = first ? b.free1 : b.free0, *rows_free = first ? b.free0 : b.free1;
+            uint64_t *done = first ? b.s_full : b.dp_full, *weights = first ? b.p_full : b.ds_full;
             auto wait = [&](uint64_t *bar, int n, int code) {
                 return __all_sync(0xffffffffu, tc::mbar_wait(bar, n & 1, b.abort, f.status, code, f.spin));
             };
-            auto s_step = [&](int it) {
-                const int st = it % S::kStages;
-                if (!wait(b.full0 + st, it / S::kStages, kErrA)) return false;
-                tc::mma_rows_rows<D>(tmem + kS, k, q + st * S::kTile, lead);
-                tc::commit(b.s_full, lead);
-                return true;
-            };
-            auto dp_step = [&](int it) {
-                const int st = it % S::kStages;
-                if (!wait(b.full1 + st, it / S::kStages, kErrB)) return false;
-                tc::mma_rows_rows<D>(tmem + kDp, v, dO + st * S::kTile, lead);
-                tc::commit(b.dp_full, lead);
-                return true;
-            };
-            bool go = wait(b.stay, 0, kErrStay) && s_step(0) && dp_step(0);
-            for (int it = 0; it < steps && go; ++it) {
-                const int st = it % S::kStages;
-                go = wait(b.p_full, it, kErrP);
-                if (!go) break;
-                tc::tc_fence_after_sync();
-                tc::mma_weights_rows<D, 64>(tmem + kDv, tmem + kS, dO + st * S::kTile, it > 0, lead);
-                tc::commit(b.free1 + st, lead);
-                if (it + 1 < steps) go = s_step(it + 1);
-                if (!go) break;
-                go = wait(b.ds_full, it, kErrDs);
-                if (!go) break;
-                tc::tc_fence_after_sync();
-                tc::mma_weights_rows<D, 64>(tmem + kDk, tmem + kDp, q + st * S::kTile, it > 0, lead);
-                tc::commit(b.free0 + st, lead);
-                if (it + 1 < steps) go = dp_step(it + 1);
+            bool go = wait(b.stay, 0, kErrStay);
+            for (int it = 0; it <= steps && go; ++it) {
+                const int st = it % S::kStages, before = (it + S::kStages - 1) % S::kStages;
+                if (it < steps) go = wait(rows_full + st, it / S::kStages, kErrA);
+                if (it > 0) {
+                    go = go && wait(back_full + before, (it - 1) / S::kStages, kErrB) &&
+                         wait(weights, it - 1, first ? kErrP : kErrDs);
+                    if (!go) break;
+                    tc::tc_fence_after_sync();
+                    tc::mma_weights_rows<D, 64>(acc, pair, back + before * S::kTile, it > 1, lead);
+                    tc::commit(back_free + before, lead);
+                }
+                if (!go || it == steps) break;
+                tc::mma_rows_rows<D>(pair, stay, rows + st * S::kTile, lead);
+                tc::commit(done, lead);
+                tc::commit(rows_free + st, lead);
             }
             tc::commit(b.acc, lead);
             tc::mbar_drain(b.acc, 0, f.status, kErrBwdDrain);
@@ -386,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     if (t.first >= t.seq_end) return;
     const int last = (t.first - t.seq_start) / kTileRows, steps = last + 1;  // key tiles, diagonal first
 
-    const uint32_t tmem = start_cta(b, 1);
+    const uint32_t tmem = start_cta(b, 1, 1);
     constexpr uint32_t kS = 0, kDp = 256, kDq = 384;  // two score tiles in turn
 
     if (warp >= 8) {
@@ -417,38 +415,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
             for (int i = max(0, it - S::kStages); i < it; ++i)
                 tc::mbar_drain(b.full1 + i % S::kStages, (i / S::kStages) & 1, f.status, kErrBwdDrain);
         }
-        if (warp == 8) {
+        // warp 8 issues S, two steps ahead, warp 10 dP and dQ
+        if (warp == 8 || warp == 10) {
             const uint32_t lead = lane == 0;
             const uint32_t q = tc::smem_u32(sm + S::kStay), dO = q + S::kTile;
             const uint32_t k = tc::smem_u32(sm + S::kRing0), v = tc::smem_u32(sm + S::kRing1);
             auto wait = [&](uint64_t *bar, int n, int code) {
                 return __all_sync(0xffffffffu, tc::mbar_wait(bar, n & 1, b.abort, f.status, code, f.spin));
             };
-            auto s_step = [&](int it) {
-                const int st = it % S::kStages0;
-                if (!wait(b.full0 + st, it / S::kStages0, kErrA)) return false;
-                tc::mma_rows_rows<D>(tmem + kS + (it & 1) * 128, q, k + st * S::kTile, lead);
-                tc::commit(b.s_full + (it & 1), lead);
-                return true;
-            };
-            auto dp_step = [&](int it) {
-                const int st = it % S::kStages;
-                if (!wait(b.full1 + st, it / S::kStages, kErrB)) return false;
-                tc::mma_rows_rows<D>(tmem + kDp, dO, v + st * S::kTile, lead);
-                tc::commit(b.dp_full, lead);
-                tc::commit(b.free1 + st, lead);
-                return true;
-            };
-            bool go = wait(b.stay, 0, kErrStay) && s_step(0) && dp_step(0) && (steps < 2 || s_step(1));
-            for (int it = 0; it < steps && go; ++it) {
-                const int st = it % S::kStages0;
-                go = wait(b.ds_full, it, kErrDs);
-                if (!go) break;
-                tc::tc_fence_after_sync();
-                tc::mma_weights_rows<D, 64>(tmem + kDq, tmem + kDp, k + st * S::kTile, it > 0, lead);
-                tc::commit(b.free0 + st, lead);
-                if (it + 1 < steps) go = dp_step(it + 1);
-                if (go && it + 2 < steps) go = s_step(it + 2);
+            bool go = wait(b.stay, 0, kErrStay);
+            if (warp == 8) {
+                for (int it = 0; it < steps && go; ++it) {
+                    const int st = it % S::kStages0;
+                    go = wait(b.full0 + st, it / S::kStages0, kErrA) && (it < 2 || wait(b.s_free + (it & 1), (it >> 1) - 1, kErrS));
+                    if (!go) break;
+                    tc::tc_fence_after_sync();
+                    tc::mma_rows_rows<D>(tmem + kS + (it & 1) * 128, q, k + st * S::kTile, lead);
+                    tc::commit(b.s_full + (it & 1), lead);
+                    tc::commit(b.free0 + st, lead);
+                }
+            } else {
+                for (int it = 0; it <= steps && go; ++it) {
+                    const int st = it % S::kStages, st0 = (it + S::kStages0 - 1) % S::kStages0;
+                    if (it < steps) go = wait(b.full1 + st, it / S::kStages, kErrB);
+                    if (it > 0) {
+                        go = go && wait(b.full0 + st0, (it - 1) / S::kStages0, kErrA) && wait(b.ds_full, it - 1, kErrDs);
+                        if (!go) break;
+                        tc::tc_fence_after_sync();
+                        tc::mma_weights_rows<D, 64>(tmem + kDq, tmem + kDp, k + st0 * S::kTile, it > 1, lead);
+                        tc::commit(b.free0 + st0, lead);
+                    }
+                    if (!go || it == steps) break;
+                    tc::mma_rows_rows<D>(tmem + kDp, dO, v + st * S::kTile, lead);
+                    tc::commit(b.dp_full, lead);
+                    tc::commit(b.free1 + st, lead);
+                }
             }
             tc::commit(b.acc, lead);
             tc::mbar_drain(b.acc, 0, f.status, kErrBwdDrain);
@@ -474,6 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
             tc::tmem_start(ts + (it & 1) * 128 + 32, x + 32);
             tc::tmem_ready(x);
             tc::tmem_ready(x + 32);
+            tc::tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(b.s_free + (it & 1));
 #pragma unroll
             for (int j = 0; j < 64; j += 2) {
                 tc::unpack2(tc::fma2(tc::pack2(x[j], x[j + 1]), c2, z2), x[j], x[j + 1]);

@@ -43,13 +43,14 @@ template <int D>
 struct FwdShape {
     static constexpr int kStages = D == 128 ? 2 : 4;
     static constexpr uint32_t kTile = TileShape<D>::kBytes;
-    static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = kK + kStages * kTile;
-    static constexpr uint32_t kBars = kV + kStages * kTile;
+    // a stage: the keys of step p and the values of step p - 1, which are read together
+    static constexpr uint32_t kQ = 0, kRing = 2 * kTile;
+    static constexpr uint32_t kBars = kRing + kStages * 2 * kTile;
     static constexpr uint32_t kBytes = kBars + 256 + 1024;  // and the base's alignment
     static constexpr uint32_t kTmemS = 0, kTmemO = 256;     // columns
 };
 
-enum : int { kErrQ = 101, kErrK, kErrV, kErrEmpty, kErrS, kErrP, kErrO, kErrDrain };
+enum : int { kErrQ = 101, kErrKv, kErrFree, kErrS, kErrP, kErrO, kErrDrain };
 
 template <int D>
 __device__ __noinline__ void recompute_row(const FwdParams &f, int row, int start, int h)
@@ -66,11 +67,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kBars);
     uint64_t *q_full = bars;
-    uint64_t *k_full = bars + 1, *k_free = k_full + S::kStages;
-    uint64_t *v_full = k_free + S::kStages, *v_free = v_full + S::kStages;
-    uint64_t *s_full = v_free + S::kStages;   // [2] scores of a query tile are in TMEM
-    uint64_t *p_full = s_full + 2;            // [2] its probabilities are (one arrival per warp)
-    uint64_t *o_full = p_full + 2;            // all products are done
+    uint64_t *kv_full = bars + 1, *kv_free = kv_full + S::kStages;
+    uint64_t *s_full = kv_free + S::kStages;  // [tile][half] scores are in TMEM
+    uint64_t *p_full = s_full + 4;            // [tile][half] probabilities are (one arrival per warp)
+    uint64_t *o_full = p_full + 4;            // all products are done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_full + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -90,16 +90,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     if (threadIdx.x == 0) {
         tc::mbar_init(q_full, 1);
         for (int i = 0; i < S::kStages; ++i) {
-            tc::mbar_init(k_full + i, 1);
-            tc::mbar_init(k_free + i, 1);
-            tc::mbar_init(v_full + i, 1);
-            tc::mbar_init(v_free + i, 1);
+            tc::mbar_init(kv_full + i, 1);
+            tc::mbar_init(kv_free + i, 1 + two);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             tc::mbar_init(s_full + i, 1);
             tc::mbar_init(p_full + i, 4);
         }
-        tc::mbar_init(o_full, 1);
+        tc::mbar_init(o_full, 1 + two);
         *abort = 0;
         tc::fence_mbar_init();
     }
@@ -115,60 +113,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             tc::mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * S::kTile);
             for (int w = 0; w <= two; ++w)
                 tc::load_tile<D>(sm + S::kQ + w * S::kTile, &f.q, h, t.first + w * kTileRows, q_full);
-            int it = 0;
-            for (; it < steps; ++it) {
-                const int st = it % S::kStages, use = it / S::kStages;
-                const int token = t.seq_start + (last - it) * kTileRows;
-                if (use && !tc::mbar_wait(k_free + st, (use - 1) & 1, abort, f.status, kErrEmpty, f.spin)) break;
-                tc::mbar_arrive_expect_tx(k_full + st, S::kTile);
-                tc::load_tile<D>(sm + S::kK + st * S::kTile, &f.k, hk, token, k_full + st);
-                if (use && !tc::mbar_wait(v_free + st, (use - 1) & 1, abort, f.status, kErrEmpty, f.spin)) {
-                    tc::mbar_drain(k_full + st, use & 1, f.status, kErrDrain);
-                    break;
-                }
-                tc::mbar_arrive_expect_tx(v_full + st, S::kTile);
-                tc::load_tile<D>(sm + S::kV + st * S::kTile, &f.v, hk, token, v_full + st);
+            int p = 0;
+            for (; p <= steps; ++p) {
+                const int st = p % S::kStages, use = p / S::kStages;
+                uint8_t *to = sm + S::kRing + st * 2 * S::kTile;
+                const int token = t.seq_start + (last - p) * kTileRows;
+                if (use && !tc::mbar_wait(kv_free + st, (use - 1) & 1, abort, f.status, kErrFree, f.spin)) break;
+                tc::mbar_arrive_expect_tx(kv_full + st, ((p < steps) + (p > 0)) * S::kTile);
+                if (p < steps) tc::load_tile<D>(to, &f.k, hk, token, kv_full + st);
+                if (p > 0) tc::load_tile<D>(to + S::kTile, &f.v, hk, token + kTileRows, kv_full + st);
             }
             // whatever the other warps do, the copies land before the memory is let go
             tc::mbar_drain(q_full, 0, f.status, kErrDrain);
-            for (int i = max(0, it - S::kStages); i < it; ++i) {
-                tc::mbar_drain(k_full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
-                tc::mbar_drain(v_full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
-            }
+            for (int i = max(0, p - S::kStages); i < p; ++i)
+                tc::mbar_drain(kv_full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
         }
-        if (warp == 8) {
+        // one warp issues for each query tile
+        const int w = warp == 8 ? 0 : warp == 10 && two ? 1 : -1;
+        if (w >= 0) {
             const uint32_t lead = lane == 0;
-            const uint32_t q = tc::smem_u32(sm + S::kQ), k = tc::smem_u32(sm + S::kK),
-                           v = tc::smem_u32(sm + S::kV);
+            const uint32_t q = tc::smem_u32(sm + S::kQ + w * S::kTile), ring = tc::smem_u32(sm + S::kRing);
+            const uint32_t s_acc = tmem + S::kTmemS + w * 128, o_acc = tmem + S::kTmemO + w * D;
+            const int begin = two && w == 0;
             auto wait = [&](uint64_t *bar, int n, int code) {
                 return __all_sync(0xffffffffu, tc::mbar_wait(bar, n & 1, abort, f.status, code, f.spin));
             };
             bool go = wait(q_full, 0, kErrQ);
-            // O_w += P_w(it) V(it)
-            auto pv = [&](int w, int begin, int it) {
-                const int st = it % S::kStages;
-                go = go && wait(v_full + st, it / S::kStages, kErrV) && wait(p_full + w, it - begin, kErrP);
-                if (!go) return;
-                tc::tc_fence_after_sync();
-                tc::mma_weights_rows<D, 32>(tmem + S::kTmemO + w * D, tmem + S::kTmemS + w * 128,
-                                            v + st * S::kTile, it > begin, lead);
-            };
-            for (int it = 0; it < steps && go; ++it) {
-                const int st = it % S::kStages;
-                go = wait(k_full + st, it / S::kStages, kErrK);
-                for (int w = 0; w <= two && go; ++w) {
-                    const int begin = two && w == 0;
-                    if (it < begin) continue;
-                    if (it > begin) pv(w, begin, it - 1);
-                    if (!go) break;
-                    tc::mma_rows_rows<D>(tmem + S::kTmemS + w * 128, q + w * S::kTile, k + st * S::kTile, lead);
-                    tc::commit(s_full + w, lead);
+            for (int it = 0; it <= steps && go; ++it) {
+                const uint32_t k = ring + it % S::kStages * 2 * S::kTile, v = k + S::kTile;
+                go = wait(kv_full + it % S::kStages, it / S::kStages, kErrKv);
+#pragma unroll
+                for (int h2 = 0; h2 < 2; ++h2) {
+                    if (go && it > begin) {  // O += P V of the same half of the step before
+                        go = wait(p_full + 2 * w + h2, it - 1 - begin, kErrP);
+                        if (!go) break;
+                        tc::tc_fence_after_sync();
+                        tc::mma_weights_half<D>(o_acc, s_acc + h2 * 64, v, h2, it - 1 > begin || h2 > 0, lead);
+                    }
+                    if (!go || it < begin) continue;
+                    // behind the last step the arrival alone is due: those products are done
+                    if (it < steps) tc::mma_rows_half<D>(s_acc + h2 * 64, q, k, h2, lead);
+                    tc::commit(s_full + 2 * w + h2, lead);
                 }
-                if (!go) break;
-                tc::commit(k_free + st, lead);
-                if (it > 0) tc::commit(v_free + (it - 1) % S::kStages, lead);
+                if (go && it < steps) tc::commit(kv_free + it % S::kStages, lead);
             }
-            for (int w = 0; w <= two && go; ++w) pv(w, two && w == 0, steps - 1);
             tc::commit(o_full, lead);
             tc::mbar_drain(o_full, 0, f.status, kErrDrain);
         }
@@ -183,34 +171,63 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             const float c = f.p.scale * 1.44269504088896340736f;
             float m = -INFINITY, l = 0.f;  // reference (unscaled score) and sum
             bool go = true;
-            for (int it = begin; it < steps; ++it) {
-                go = __all_sync(0xffffffffu,
-                                tc::mbar_wait(s_full + w, (it - begin) & 1, abort, f.status, kErrS, f.spin));
+            const int units = 2 * (steps - begin);  // halves of key tiles, the diagonal's first
+            for (int u = 0; u < units; ++u) {
+                const int half = u & 1;
+                const uint32_t here = ts + half * 64;
+                go = __all_sync(0xffffffffu, tc::mbar_wait(s_full + 2 * w + half, (u >> 1) & 1, abort, f.status,
+                                                           kErrS, f.spin));
                 if (!go) break;
                 tc::tc_fence_after_sync();
-                float s[128];
+                float s[64];
+                tc::tmem_start(here, s);
+                tc::tmem_start(here + 32, s + 32);
+                tc::tmem_ready(s);
+                tc::tmem_ready(s + 32);
+                if (u < 2) {  // the diagonal tile
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tc::tmem_start(ts + 32 * i, s + 32 * i);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tc::tmem_ready(s + 32 * i);
-                if (it == begin) {  // the diagonal tile
-#pragma unroll
-                    for (int i = 0; i < 128; ++i) s[i] = i <= in_tile ? s[i] : -INFINITY;
+                    for (int i = 0; i < 64; ++i) s[i] = i + half * 64 <= in_tile ? s[i] : -INFINITY;
                 }
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int i = 4; i < 124; i += 8) {
+                for (int i = 4; i < 60; i += 8) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) mx[j] = tc::max3(mx[j], s[i + j], s[i + j + 4]);
                 }
+                const float top = tc::max3(tc::max3(mx[0], s[60], s[61]), tc::max3(mx[1], s[62], s[63]),
+                                           fmaxf(mx[2], mx[3]));
+                if (u == 0) m = top;
+                // Formed with the reference that is there, next to the search for the
+                // maximum; once in a while done again.
+                for (;;) {
+                    const float ref = m == -INFINITY ? 0.f : m * c;
+                    const tc::f32x2 c2 = tc::pack2(c, c), r2 = tc::pack2(-ref, -ref);
+                    tc::f32x2 sum = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[124 + j]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                const bool grown = (top - m) * c > kRescale || m == -INFINITY;
-                if (it == begin) {
-                    m = top;
-                } else if (__any_sync(0xffffffffu, grown)) {
-                    // the products so far were complete before these scores were
+                    for (int i = 0; i < 64; i += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float a, b;
+                            tc::unpack2(tc::fma2(tc::pack2(s[i + j], s[i + j + 1]), c2, r2), a, b);
+                            a = tc::exp2_fast(a);
+                            b = tc::exp2_fast(b);
+                            sum = tc::add2(sum, tc::pack2(a, b));
+                            pk[j / 2] = tc::bf16x2(a, b);
+                        }
+                        tc::tmem_st16(here + i / 2, pk);
+                    }
+                    if (!__any_sync(0xffffffffu, (top - m) * c > kRescale || (m == -INFINITY && top > m))) {
+                        float sa, sb;
+                        tc::unpack2(sum, sa, sb);
+                        l += sa + sb;
+                        break;
+                    }
+                    // the next scores' arrival says that the products so far are complete
+                    go = __all_sync(0xffffffffu, tc::mbar_wait(s_full + 2 * w + (half ^ 1), ((u + 1) >> 1) & 1,
+                                                               abort, f.status, kErrS, f.spin));
+                    if (!go) break;
+                    tc::tc_fence_after_sync();
                     const float m_new = fmaxf(m, top);
                     const float keep = m_new == -INFINITY ? 1.f : tc::exp2_fast((m - m_new) * c);
                     m = m_new;
@@ -225,30 +242,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         tc::tmem_st16(to + i, y);
                     }
                 }
-                const float ref = m == -INFINITY ? 0.f : m * c;
-                const tc::f32x2 c2 = tc::pack2(c, c), r2 = tc::pack2(-ref, -ref);
-                tc::f32x2 sum = 0;
-#pragma unroll
-                for (int i = 0; i < 128; i += 32) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float a, b;
-                        tc::unpack2(tc::fma2(tc::pack2(s[i + j], s[i + j + 1]), c2, r2), a, b);
-                        a = tc::exp2_fast(a);
-                        b = tc::exp2_fast(b);
-                        sum = tc::add2(sum, tc::pack2(a, b));
-                        pk[j / 2] = tc::bf16x2(a, b);
-                    }
-                    tc::tmem_st16(ts + i / 2, pk);
-                }
-                float sa, sb;
-                tc::unpack2(sum, sa, sb);
-                l += sa + sb;
+                if (!go) break;
                 tc::tmem_st_wait();
                 tc::tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(p_full + w);
+                if (lane == 0) tc::mbar_arrive(p_full + 2 * w + half);
             }
             go = __all_sync(0xffffffffu, go && tc::mbar_wait(o_full, 0, abort, f.status, kErrO, f.spin));
             if (go && !*abort) {

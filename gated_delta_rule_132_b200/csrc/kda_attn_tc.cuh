@@ -132,15 +132,41 @@ __device__ __forceinline__ void mma_rows_rows(uint32_t acc, uint32_t x, uint32_t
     }
 }
 
-// acc[128 x D] (+)= W Y over 128 tokens: W [128 x 128] bf16 in TMEM, 32 columns for the
-// first 64 tokens and 32 more that begin kHalf columns on; Y a tile read along its tokens.
-template <int D, int kHalf>
+// acc[128 x 64] = X Y_h^T: half h of tile y's rows (64 of them).
+template <int D>
+__device__ __forceinline__ void mma_rows_half(uint32_t acc, uint32_t x, uint32_t y, int h,
+                                              uint32_t lead)
+{
+    const uint64_t a = smem_desc(x, 16, 1024), b = smem_desc(y + h * 64 * 128, 16, 1024);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = ((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4;
+        mma_ss(acc, a + off, b + off, idesc_bf16(128, 64, 0, 0), k > 0, lead);
+    }
+}
+
+// acc[128 x D] (+)= W Y_h over half h of tile y's tokens: W [128 x 64] bf16 in 32 columns.
+template <int D>
+__device__ __forceinline__ void mma_weights_half(uint32_t acc, uint32_t w, uint32_t y, int h,
+                                                 bool accumulate, uint32_t lead)
+{
+    const uint64_t b = smem_desc(y + h * 4 * 2048, kBlockBytes, 1024);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        mma_ts(acc, w + k * 8, b + ((k * 2048) >> 4), idesc_bf16(128, D, 0, 1), accumulate || k > 0,
+               lead);
+}
+
+// acc[128 x D] (+)= W Y over the tokens 16 kFrom .. 16 kTo of 128: W [128 x 128] bf16 in
+// TMEM, 32 columns for the first 64 tokens and 32 more that begin kHalf columns on; Y a
+// tile read along its tokens.
+template <int D, int kHalf, int kFrom = 0, int kTo = kTileRows / 16>
 __device__ __forceinline__ void mma_weights_rows(uint32_t acc, uint32_t w, uint32_t y,
                                                  bool accumulate, uint32_t lead)
 {
     const uint64_t b = smem_desc(y, kBlockBytes, 1024);
 #pragma unroll
-    for (int k = 0; k < kTileRows / 16; ++k)
+    for (int k = kFrom; k < kTo; ++k)
         mma_ts(acc, w + (k >> 2) * kHalf + (k & 3) * 8, b + ((k * 2048) >> 4),
                idesc_bf16(128, D, 0, 1), accumulate || k > 0, lead);
 }
@@ -272,7 +298,9 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
 
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
-    return fmaxf(fmaxf(a, b), c);
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 }  // namespace tc

@@ -114,15 +114,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         tc::mbar_init(q_full, 1);
         for (int i = 0; i < S::kStages; ++i) {
             tc::mbar_init(k_full + i, 1);
-            tc::mbar_init(k_free + i, 1);
+            tc::mbar_init(k_free + i, 1 + two);  // kPair: by both halves
             tc::mbar_init(v_full + i, 1);
-            tc::mbar_init(v_free + i, 1);
+            tc::mbar_init(v_free + i, 1 + two);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(s_full + i, 1);
             tc::mbar_init(p_full + i, 4);
         }
-        tc::mbar_init(o_full, 1);
+        tc::mbar_init(o_full, kPair ? 1 + two : 2);
         *abort = 0;
         for (int i = 0; i < 8; ++i) bad[i] = 0;
         tc::fence_mbar_init();
@@ -179,40 +179,34 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
                     tc::mbar_drain(full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
             }
         }
-        if (warp == 8) {
+        // one warp issues for each half
+        const int w = warp == 8 ? 0 : warp == 11 && (two || !kPair) ? 1 : -1;
+        if (w >= 0) {
             const uint32_t lead = lane == 0;
-            const uint32_t q = tc::smem_u32(sm + S::kQ), k = tc::smem_u32(sm + S::kK),
-                           v = tc::smem_u32(sm + S::kV);
+            const uint32_t q = tc::smem_u32(sm + S::kQ + (kPair ? w : 0) * S::kTile),
+                           k = tc::smem_u32(sm + S::kK), v = tc::smem_u32(sm + S::kV);
+            const uint32_t s_acc = tmem + S::kTmemS + w * 128, o_acc = tmem + S::kTmemO + w * D;
             constexpr int kEvery = kPair ? 1 : 2;  // steps between two of a half
             auto wait = [&](uint64_t *bar, int n, int code) {
                 return __all_sync(0xffffffffu, tc::mbar_wait(bar, n & 1, abort, f.status, code, f.spin));
             };
             bool go = wait(q_full, 0, kErrQ);
-            auto pv = [&](int w, int it) {
-                const int st = it % S::kStages, nth = it / kEvery;
-                go = go && wait(v_full + st, it / S::kStages, kErrV) && wait(p_full + w, nth, kErrP);
-                if (!go) return;
-                tc::tc_fence_after_sync();
-                tc::mma_weights_rows<D, 32>(tmem + S::kTmemO + w * D, tmem + S::kTmemS + w * 128,
-                                            v + st * S::kTile, nth > 0, lead);
-            };
-            for (int it = 0; it < steps && go; ++it) {
-                const int st = it % S::kStages;
-                go = wait(k_full + st, it / S::kStages, kErrK);
-                for (int w = 0; w < 2 && go; ++w) {
-                    if (!works(w, it)) continue;
-                    if (it >= kEvery) pv(w, it - kEvery);
+            int nth = 0;
+            for (int it = kPair ? 0 : w; go; it += kEvery, ++nth) {
+                const int st = it % S::kStages, last = it - kEvery, before = (last + S::kStages) % S::kStages;
+                if (it < steps) go = wait(k_full + st, it / S::kStages, kErrK);
+                if (nth > 0) {  // O += P V of the half's step before
+                    go = go && wait(v_full + before, last / S::kStages, kErrV) && wait(p_full + w, nth - 1, kErrP);
                     if (!go) break;
-                    tc::mma_rows_rows<D>(tmem + S::kTmemS + w * 128, q + (kPair ? w : 0) * S::kTile, k + st * S::kTile, lead);
-                    tc::commit(s_full + w, lead);
+                    tc::tc_fence_after_sync();
+                    tc::mma_weights_rows<D, 32>(o_acc, s_acc, v + before * S::kTile, nth > 1, lead);
                 }
-                if (!go) break;
+                if (!go || it >= steps) break;
+                tc::mma_rows_rows<D>(s_acc, q, k + st * S::kTile, lead);
+                tc::commit(s_full + w, lead);
                 tc::commit(k_free + st, lead);
-                if (it >= kEvery) tc::commit(v_free + (it - kEvery) % S::kStages, lead);
+                if (nth > 0) tc::commit(v_free + before, lead);
             }
-            for (int it = max(0, steps - kEvery); it < steps; ++it)
-                for (int w = 0; w < 2 && go; ++w)
-                    if (works(w, it)) pv(w, it);
             tc::commit(o_full, lead);
             tc::mbar_drain(o_full, 0, f.status, kErrDrain);
         }
