@@ -56,9 +56,10 @@ kda_status_t describe_attn(int B, int T, int Hq, int Hkv, int d, int n_seqs, boo
     p->B = B; p->T = T; p->Hq = Hq; p->Hkv = Hkv; p->d = d; p->dtype = dt;
     // any non-null value: only whether offsets are given matters before the call
     p->cu_seqlens = varlen ? reinterpret_cast<const int32_t *>(16) : nullptr;
-    // one CTA per tile and head in a one-dimensional grid, at least 64 tokens a tile;
-    // the row-wise kernels' grids are smaller than twice this
-    if ((kda::attn_tiles(*p, 64) + 1) * Hq * 8 > (long long)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    // one CTA per tile and head in a one-dimensional grid, at least 32 tokens a tile
+    if ((kda::attn_tiles(*p, 32) + 1) * Hq > (long long)INT32_MAX ||
+        p->tokens * Hq / 8 > (long long)INT32_MAX)  // and eight rows to a block at least
+        return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 

@@ -1,12 +1,14 @@
 // kda_attn_fp32.cu — causal prompt attention and its gradients in fp32 (CUDA cores),
 // and the choice between this path and the tensor-core path.
 //
-// Tiles of 64 tokens, 256 threads as 16 x 16. A product of two tiles over the channels
-// gives each thread 4 x 4 pairs (rows 4 ty + i, columns tx + 16 j), a product of a
-// 64 x 64 weight tile with a tile of rows 4 rows x D / 16 channels; both read shared
-// memory 16 bytes at a time, the first from swizzled rows. The FMA rate bounds the
-// kernels: per four channels a warp issues 64 FMAs (16 cycles of the SM) for 12 cycles
-// of shared memory reads.
+// A CTA of 128 threads (8 x 16) owns 32 tokens and walks over the 64-token tiles that
+// they meet. A product of the two tiles over the channels gives each thread 4 x 4 pairs
+// (own rows 4 ty + i, walked rows tx + 16 j), a product of a 32 x 64 weight tile with the
+// walked rows 4 rows x D / 16 channels; both read shared memory 16 bytes at a time, from
+// swizzled rows. The FMA rate bounds the kernels: per four channels a warp issues 64 FMAs
+// (16 cycles of the SM) for 12 cycles of shared memory reads. 32 own tokens rather than
+// 64 because calls in fp32 are short: B = 2, T = 777, 8 heads of 64 are 208 tiles of 64,
+// one wave whose longest CTA takes 84 us forward, and 400 of 32, which fill the SMs.
 //
 // The gradients follow the tensor-core path's split: one CTA per key tile for dK and
 // dV, one per query tile for dQ, every result written once. Rows that are not finite
@@ -17,8 +19,9 @@
 namespace kda {
 namespace {
 
-constexpr int kRows = 64;
-constexpr int kThreads = 256;
+constexpr int kRows = 32;  // own tokens
+constexpr int kWalk = 64;  // tokens of a walked tile
+constexpr int kThreads = 128;
 constexpr int kW = 68;  // row length of a weight tile
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -29,16 +32,16 @@ template <int D> __device__ __forceinline__ int unit_at(int r, int u)
     return r * D + (u ^ (r & 7)) * 4;
 }
 
-// Start the copies of 64 tokens of one head from `first` on; tokens from `end` on are
+// Start the copies of kCount tokens of one head from `first` on; tokens from `end` on are
 // filled with zeros.
-template <int D>
+template <int D, int kCount>
 __device__ __forceinline__ void load_tile(float *dst, const float *src, int heads, int h,
                                           int first, int end)
 {
     constexpr int kUnits = D / 4;
     const int u = threadIdx.x % kUnits;
 #pragma unroll
-    for (int r = threadIdx.x / kUnits; r < kRows; r += kThreads / kUnits) {
+    for (int r = threadIdx.x / kUnits; r < kCount; r += kThreads / kUnits) {
         const bool real = first + r < end;
         const float *from = src + ((size_t)(real ? first + r : first) * heads + h) * D + u * 4;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
@@ -92,23 +95,19 @@ template <int D> struct Cols {
     static __device__ __forceinline__ int channel(int e) { return ((threadIdx.x & 15) + 16 * e) * kVec; }
 };
 
-// acc[i] += sum over 64 tokens r of w(4 ty + i, r) * row r of y; w is read along its rows
-// (kT false) or its columns (true).
-template <int D, bool kT>
+// acc[i] += sum over 64 tokens r of w(4 ty + i, r) * row r of y.
+template <int D>
 __device__ __forceinline__ void add_weighted(const float *w, const float *y, float (&acc)[4][D / 16])
 {
     using C = Cols<D>;
     const int ty = threadIdx.x >> 4;
 #pragma unroll 2
-    for (int r = 0; r < kRows; r += 4) {
+    for (int r = 0; r < kWalk; r += 4) {
         float p[4][4];  // [i][token]
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 x = *reinterpret_cast<const float4 *>(kT ? w + (r + i) * kW + 4 * ty
-                                                                  : w + (4 * ty + i) * kW + r);
-            const float v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) (kT ? p[j][i] : p[i][j]) = v[j];
+            const float4 x = *reinterpret_cast<const float4 *>(w + (4 * ty + i) * kW + r);
+            p[i][0] = x.x; p[i][1] = x.y; p[i][2] = x.z; p[i][3] = x.w;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -166,7 +165,7 @@ __device__ __forceinline__ void store_rows(const float (&acc)[4][D / 16], const 
                 to[a] = v;
             }
         }
-        if (!(odd == 0.f)) atomicOr(bad + (r >> 5), 1u << (r & 31));
+        if (!(odd == 0.f)) atomicOr(bad, 1u << r);
     }
 }
 
@@ -175,7 +174,7 @@ template <typename F> __device__ __forceinline__ void redo_rows(const unsigned *
 {
     __syncthreads();
     for (int r = threadIdx.x >> 5; r < kRows; r += kThreads / 32)
-        if (bad[r >> 5] >> (r & 31) & 1) redo(r);
+        if (*bad >> r & 1) redo(r);
 }
 
 struct F32Params {
@@ -206,39 +205,45 @@ template <int D> __device__ __noinline__ void redo_dkv(const F32Params &f, int c
     attn_row_dkv<float, D>(f.p, col, end, hk, f.lse, f.delta, f.dO, f.gk, f.gv);
 }
 
+// The walked tiles of an own query tile: from the one with its last token down.
+__device__ __forceinline__ int last_walked(const AttnTile &t)
+{
+    return t.seq_start + (t.first - t.seq_start) / kWalk * kWalk;
+}
+
 // ---------------------------------------------------------------- forward
 template <int D>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(const __grid_constant__ F32Params f)
 {
     extern __shared__ __align__(16) float smem[];
-    __shared__ unsigned bad[2];
-    float *q = smem, *k = q + kRows * D, *v = k + kRows * D, *w = v + kRows * D;
+    __shared__ unsigned bad;
+    float *q = smem, *k = q + kRows * D, *v = k + kWalk * D, *w = v + kWalk * D;
     const AttnTile t = tile_of(f, blockIdx.x / f.p.Hq);
     if (t.first >= t.seq_end) return;
     const int h = blockIdx.x % f.p.Hq, hk = h / (f.p.Hq / f.p.Hkv);
     if (!f.tiles && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const float *gk = static_cast<const float *>(f.p.k), *gv = static_cast<const float *>(f.p.v);
-    if (threadIdx.x < 2) bad[threadIdx.x] = 0;
-    load_tile<D>(q, static_cast<const float *>(f.p.q), f.p.Hq, h, t.first, t.seq_end);
-    load_tile<D>(k, gk, f.p.Hkv, hk, t.first, t.seq_end);
+    if (threadIdx.x == 0) bad = 0;
+    const int last = last_walked(t);
+    load_tile<D, kRows>(q, static_cast<const float *>(f.p.q), f.p.Hq, h, t.first, t.seq_end);
+    load_tile<D, kWalk>(k, gk, f.p.Hkv, hk, last, t.seq_end);
     const float c = f.p.scale * kLog2e;
     float m[4], l[4] = {}, acc[4][D / 16] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i) m[i] = -INFINITY;
-    // key tiles from the diagonal down
-    for (int at = t.first; at >= t.seq_start; at -= kRows) {
-        load_tile<D>(v, gv, f.p.Hkv, hk, at, t.seq_end);
+    for (int at = last; at >= t.seq_start; at -= kWalk) {
+        load_tile<D, kWalk>(v, gv, f.p.Hkv, hk, at, t.seq_end);
         landed<1>();
         float x[4][4];
         dot_tiles<D>(q, k, x);
+        const int diag = t.first - at;  // keys up to row + diag are seen
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float top = m[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool see = at < t.first || tx + 16 * j <= 4 * ty + i;
-                x[i][j] = see ? x[i][j] * c : -INFINITY;
+                x[i][j] = tx + 16 * j <= 4 * ty + i + diag ? x[i][j] * c : -INFINITY;
                 top = fmaxf(top, x[i][j]);
             }
 #pragma unroll
@@ -256,8 +261,8 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const __grid_constant__ F
         }
         store_weights(w, x);
         landed<0>();  // the values, the weights, and k is free
-        if (at > t.seq_start) load_tile<D>(k, gk, f.p.Hkv, hk, at - kRows, t.seq_end);
-        add_weighted<D, false>(w, v, acc);
+        if (at > t.seq_start) load_tile<D, kWalk>(k, gk, f.p.Hkv, hk, at - kWalk, t.seq_end);
+        add_weighted<D>(w, v, acc);
         __syncthreads();
     }
     float by[4];
@@ -271,30 +276,16 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const __grid_constant__ F
             f.lse_out[(size_t)row * f.p.Hq + h] = m[i] * 0.693147180559945309417f + logf(l[i]);
     }
     store_rows<D>(acc, by, f.o + ((size_t)t.first * f.p.Hq + h) * D, (size_t)f.p.Hq * D,
-                  t.seq_end - t.first, bad);
-    redo_rows(bad, [&](int r) { redo_fwd<D>(f, t.first + r, t.seq_start, h); });
+                  t.seq_end - t.first, &bad);
+    redo_rows(&bad, [&](int r) { redo_fwd<D>(f, t.first + r, t.seq_start, h); });
 }
 
-// p = 2^(c s - lse2 of the row) where the pair is visible, from raw scores.
-__device__ __forceinline__ void weights_of(float (&x)[4][4], float c, const float *lse2, bool diag)
-{
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float z = lse2[4 * ty + i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool see = !diag || tx + 16 * j <= 4 * ty + i;
-            x[i][j] = see ? exp2f(fmaf(x[i][j], c, -z)) : 0.f;
-        }
-    }
-}
-
-// lse2 and D of 64 query rows; rows behind the sequence get weights of zero.
+// lse2 and D of kCount query rows; rows behind the sequence get weights of zero.
+template <int kCount>
 __device__ __forceinline__ void load_stats(const F32Params &f, float *lse2, float *del, int h,
                                            int first, int end)
 {
-    if (threadIdx.x < kRows) {
+    if (threadIdx.x < kCount) {
         const int r = first + threadIdx.x;
         const size_t at = (size_t)h * f.p.tokens + r;
         lse2[threadIdx.x] = r < end ? f.lse2[at] : INFINITY;
@@ -308,94 +299,105 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ F3
 {
     extern __shared__ __align__(16) float smem[];
     __shared__ float lse2[kRows], del[kRows];
-    __shared__ unsigned bad[2];
-    float *q = smem, *g = q + kRows * D, *k = g + kRows * D, *v = k + kRows * D, *w = v + kRows * D;
+    __shared__ unsigned bad;
+    float *q = smem, *g = q + kRows * D, *k = g + kRows * D, *v = k + kWalk * D, *w = v + kWalk * D;
     const AttnTile t = tile_of(f, blockIdx.x / f.p.Hq);
     if (t.first >= t.seq_end) return;
-    const int h = blockIdx.x % f.p.Hq, hk = h / (f.p.Hq / f.p.Hkv), ty = threadIdx.x >> 4;
-    if (threadIdx.x < 2) bad[threadIdx.x] = 0;
-    load_stats(f, lse2, del, h, t.first, t.seq_end);
-    load_tile<D>(q, static_cast<const float *>(f.p.q), f.p.Hq, h, t.first, t.seq_end);
-    load_tile<D>(g, f.dO, f.p.Hq, h, t.first, t.seq_end);
+    const int h = blockIdx.x % f.p.Hq, hk = h / (f.p.Hq / f.p.Hkv);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    if (threadIdx.x == 0) bad = 0;
+    load_stats<kRows>(f, lse2, del, h, t.first, t.seq_end);
+    load_tile<D, kRows>(q, static_cast<const float *>(f.p.q), f.p.Hq, h, t.first, t.seq_end);
+    load_tile<D, kRows>(g, f.dO, f.p.Hq, h, t.first, t.seq_end);
     const float c = f.p.scale * kLog2e;
     float acc[4][D / 16] = {};
-    for (int at = t.first; at >= t.seq_start; at -= kRows) {
-        load_tile<D>(k, static_cast<const float *>(f.p.k), f.p.Hkv, hk, at, t.seq_end);
-        load_tile<D>(v, static_cast<const float *>(f.p.v), f.p.Hkv, hk, at, t.seq_end);
+    for (int at = last_walked(t); at >= t.seq_start; at -= kWalk) {
+        load_tile<D, kWalk>(k, static_cast<const float *>(f.p.k), f.p.Hkv, hk, at, t.seq_end);
+        load_tile<D, kWalk>(v, static_cast<const float *>(f.p.v), f.p.Hkv, hk, at, t.seq_end);
         landed<1>();
         float x[4][4], y[4][4];
         dot_tiles<D>(q, k, x);
-        weights_of(x, c, lse2, at == t.first);
         landed<0>();
         dot_tiles<D>(g, v, y);
+        const int diag = t.first - at;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float dl = del[4 * ty + i];
+            const float z = lse2[4 * ty + i], dl = del[4 * ty + i];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[i][j] *= y[i][j] - dl;
+            for (int j = 0; j < 4; ++j)
+                x[i][j] = tx + 16 * j <= 4 * ty + i + diag
+                              ? exp2f(fmaf(x[i][j], c, -z)) * (y[i][j] - dl) : 0.f;
         }
         store_weights(w, x);
         __syncthreads();
-        add_weighted<D, false>(w, k, acc);
+        add_weighted<D>(w, k, acc);
         __syncthreads();
     }
     const float by[4] = {f.p.scale, f.p.scale, f.p.scale, f.p.scale};
     store_rows<D>(acc, by, f.gq + ((size_t)t.first * f.p.Hq + h) * D, (size_t)f.p.Hq * D,
-                  t.seq_end - t.first, bad);
-    redo_rows(bad, [&](int r) { redo_dq<D>(f, t.first + r, t.seq_start, h); });
+                  t.seq_end - t.first, &bad);
+    redo_rows(&bad, [&](int r) { redo_dq<D>(f, t.first + r, t.seq_start, h); });
 }
 
 // ---------------------------------------------------------------- dK and dV
+// Own rows are keys, walked rows queries.
 template <int D>
 __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ F32Params f)
 {
     extern __shared__ __align__(16) float smem[];
-    __shared__ float lse2[kRows], del[kRows];
-    __shared__ unsigned bad[2];
-    float *q = smem, *g = q + kRows * D, *k = g + kRows * D, *v = k + kRows * D;
-    float *w = v + kRows * D, *ws = w + kRows * kW;
+    __shared__ float lse2[kWalk], del[kWalk];
+    __shared__ unsigned bad;
+    float *k = smem, *v = k + kRows * D, *q = v + kRows * D, *g = q + kWalk * D, *w = g + kWalk * D;
     AttnTile t = tile_of(f, blockIdx.x / f.p.Hkv);
     if (t.first >= t.seq_end) return;
     if (!f.tiles && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
     // the list begins with a sequence's last tile; here the first one has most work
     const int count = (t.seq_end - t.seq_start + kRows - 1) / kRows;
     t.first = t.seq_start + (count - 1 - (t.first - t.seq_start) / kRows) * kRows;
-    const int hk = blockIdx.x % f.p.Hkv, G = f.p.Hq / f.p.Hkv, ty = threadIdx.x >> 4;
-    if (threadIdx.x < 2) bad[threadIdx.x] = 0;
-    load_tile<D>(k, static_cast<const float *>(f.p.k), f.p.Hkv, hk, t.first, t.seq_end);
-    load_tile<D>(v, static_cast<const float *>(f.p.v), f.p.Hkv, hk, t.first, t.seq_end);
+    const int hk = blockIdx.x % f.p.Hkv, G = f.p.Hq / f.p.Hkv;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    if (threadIdx.x == 0) bad = 0;
+    load_tile<D, kRows>(k, static_cast<const float *>(f.p.k), f.p.Hkv, hk, t.first, t.seq_end);
+    load_tile<D, kRows>(v, static_cast<const float *>(f.p.v), f.p.Hkv, hk, t.first, t.seq_end);
     const float c = f.p.scale * kLog2e;
     float ak[4][D / 16] = {}, av[4][D / 16] = {};
     for (int h = hk * G; h < (hk + 1) * G; ++h)
-        for (int at = t.first; at < t.seq_end; at += kRows) {
-            load_stats(f, lse2, del, h, at, t.seq_end);
-            load_tile<D>(q, static_cast<const float *>(f.p.q), f.p.Hq, h, at, t.seq_end);
-            load_tile<D>(g, f.dO, f.p.Hq, h, at, t.seq_end);
+        for (int at = t.first; at < t.seq_end; at += kWalk) {
+            load_stats<kWalk>(f, lse2, del, h, at, t.seq_end);
+            load_tile<D, kWalk>(q, static_cast<const float *>(f.p.q), f.p.Hq, h, at, t.seq_end);
+            load_tile<D, kWalk>(g, f.dO, f.p.Hq, h, at, t.seq_end);
             landed<1>();
             float x[4][4], y[4][4];
-            dot_tiles<D>(q, k, x);
-            weights_of(x, c, lse2, at == t.first);
+            dot_tiles<D>(k, q, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float z = lse2[tx + 16 * j];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i][j] = at > t.first || 4 * ty + i <= tx + 16 * j ? exp2f(fmaf(x[i][j], c, -z)) : 0.f;
+            }
             store_weights(w, x);
             landed<0>();
-            dot_tiles<D>(g, v, y);
+            add_weighted<D>(w, g, av);
+            dot_tiles<D>(v, g, y);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float dl = del[4 * ty + i];
+            for (int j = 0; j < 4; ++j) {
+                const float dl = del[tx + 16 * j];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[i][j] *= y[i][j] - dl;
+                for (int i = 0; i < 4; ++i) x[i][j] *= y[i][j] - dl;
             }
-            store_weights(ws, x);
-            add_weighted<D, true>(w, g, av);
             __syncthreads();
-            add_weighted<D, true>(ws, q, ak);
+            store_weights(w, x);
+            __syncthreads();
+            add_weighted<D>(w, q, ak);
             __syncthreads();
         }
     const size_t out = ((size_t)t.first * f.p.Hkv + hk) * D, stride = (size_t)f.p.Hkv * D;
     const float one[4] = {1.f, 1.f, 1.f, 1.f};
     const float by[4] = {f.p.scale, f.p.scale, f.p.scale, f.p.scale};
-    store_rows<D>(av, one, f.gv + out, stride, t.seq_end - t.first, bad);
-    store_rows<D>(ak, by, f.gk + out, stride, t.seq_end - t.first, bad);
-    redo_rows(bad, [&](int r) { redo_dkv<D>(f, t.first + r, t.seq_end, hk); });
+    store_rows<D>(av, one, f.gv + out, stride, t.seq_end - t.first, &bad);
+    store_rows<D>(ak, by, f.gk + out, stride, t.seq_end - t.first, &bad);
+    redo_rows(&bad, [&](int r) { redo_dkv<D>(f, t.first + r, t.seq_end, hk); });
 }
 
 template <typename K>
@@ -428,7 +430,7 @@ cudaError_t fwd(const AttnProblem &p, void *o, float *lse, void *workspace, cuda
     f.lse_out = lse;
     const cudaError_t e = prepare(p, false, workspace, f, st);
     if (e != cudaSuccess) return e;
-    return start(fwd_kernel<D>, f, attn_tiles(p, kRows) * p.Hq, (3 * kRows * D + kRows * kW) * 4, st);
+    return start(fwd_kernel<D>, f, attn_tiles(p, kRows) * p.Hq, ((kRows + 2 * kWalk) * D + kRows * kW) * 4, st);
 }
 
 template <int D>
@@ -449,9 +451,9 @@ cudaError_t bwd(const AttnProblem &p, const void *o, const float *lse, const voi
     if (e == cudaSuccess) e = launch_attn_delta(p, o, lse, dO, delta, lse2, st);
     const long long tiles = attn_tiles(p, kRows);
     if (e == cudaSuccess)
-        e = start(dkv_kernel<D>, f, tiles * p.Hkv, (4 * kRows * D + 2 * kRows * kW) * 4, st);
+        e = start(dkv_kernel<D>, f, tiles * p.Hkv, (2 * (kRows + kWalk) * D + kRows * kW) * 4, st);
     if (e == cudaSuccess)
-        e = start(dq_kernel<D>, f, tiles * p.Hq, (4 * kRows * D + kRows * kW) * 4, st);
+        e = start(dq_kernel<D>, f, tiles * p.Hq, (2 * (kRows + kWalk) * D + kRows * kW) * 4, st);
     return e;
 }
 

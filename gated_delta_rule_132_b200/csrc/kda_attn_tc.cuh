@@ -250,33 +250,6 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// 2^x for two numbers on the FMA pipe, to share the exponentials with the special-function
-// unit (16 a cycle and SM, the softmax's bound). x = n + r with n the nearest integer (x + 1.5 * 2^23
-// leaves n in the low mantissa bits) and |r| <= 1/2; 2^r by the polynomial of degree 4
-// with p(0) = 1 whose largest relative error is smallest (2.9e-6, fitted by Lawson's
-// iteration); n is added to the exponent. Below 2^-127 the result is 0; a NaN or an
-// infinity gives a number that is huge or NaN, so that it shows in the row's result.
-__device__ __forceinline__ void exp2_fma(f32x2 x, float &a, float &b)
-{
-    unpack2(x, a, b);
-    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(a));  // -127
-    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(b));
-    x = pack2(a, b);
-    const f32x2 big = pack2(12582912.f, 12582912.f);
-    const f32x2 n = add2(x, big);
-    const f32x2 r = fma2(add2(n, pack2(-12582912.f, -12582912.f)), pack2(-1.f, -1.f), x);
-    f32x2 p = fma2(pack2(0.009582855738699436f, 0.009582855738699436f), r,
-                   pack2(0.05590642988681793f, 0.05590642988681793f));
-    p = fma2(p, r, pack2(0.24024099111557007f, 0.24024099111557007f));
-    p = fma2(p, r, pack2(0.6931241750717163f, 0.6931241750717163f));
-    p = fma2(p, r, pack2(1.f, 1.f));
-    float na, nb;
-    unpack2(n, na, nb);
-    unpack2(p, a, b);
-    a = __int_as_float(__float_as_int(a) + (__float_as_int(na) << 23));
-    b = __int_as_float(__float_as_int(b) + (__float_as_int(nb) << 23));
-}
-
 // lo in the lower half: the operand's element order.
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 {
