@@ -77,6 +77,66 @@ cudaError_t launch_attn_tc_bwd(const AttnProblem &p, const void *o, const float 
 cudaError_t launch_attn_delta(const AttnProblem &p, const void *o, const float *lse,
                               const void *dO, float *delta, float *lse2, cudaStream_t st);
 
+// dK and dV of a key tile can be shared out over a cluster of CTAs, each with some of the
+// group's query heads; the partial sums are added in rank order through distributed
+// shared memory. That pays where the key tiles alone make too few CTAs (below `enough`):
+// one per SM on the tensor cores, whose CTAs take an SM each and some 10 us to begin and to
+// be joined (nine packed documents, 320 CTAs: 125 us, split in two 192 us), four per SM
+// in fp32 (B = 2, T = 777, 8/4 heads of 64, 200 CTAs: 180 us, split in two 106 us).
+inline int attn_head_split(const AttnProblem &p, int rows, int enough)
+{
+    const long long ctas = attn_tiles(p, rows) * p.Hkv;
+    int split = 1;
+    while (split < 4 && split * 2 <= p.Hq / p.Hkv && ctas * split < enough) split *= 2;
+    return split;
+}
+
+// A launch as clusters of `split` CTAs (1: none).
+template <typename K, typename P>
+cudaError_t launch_clusters(K kernel, const P &params, long long ctas, int threads, size_t smem,
+                            int split, cudaStream_t st)
+{
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(ctas * split));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, params);
+    note_launch();
+    return e;
+}
+
+__device__ __forceinline__ int cluster_rank()
+{
+    int r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// All threads of all CTAs of the cluster; orders their shared-memory accesses.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The float at this CTA's shared address `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ float peer_float(uint32_t addr, int rank)
+{
+    float v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+                 "ld.shared::cluster.f32 %0, [a];\n\t}" : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
+
 // A tree-attention call after host-side validation.
 struct TreeProblem {
     const void *q, *k_pages, *v_pages;

@@ -36,6 +36,7 @@ struct BwdParams {
     int *status;
     uint32_t spin;
     int starve;
+    int split;  // dK and dV: CTAs per key tile, see attn_head_split
 };
 
 // Shared memory: two tiles that stay (k, v or q, dO), and a ring of stages of the two
@@ -206,15 +207,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const Bars b(sm + S::kBars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int hk = blockIdx.x % f.p.Hkv, G = f.p.Hq / f.p.Hkv;
-    AttnTile t = attn_tile(f.tiles, blockIdx.x / f.p.Hkv, kTileRows, f.p.B, f.p.T);
-    if (t.first >= t.seq_end) return;
+    const int rank = f.split > 1 ? cluster_rank() : 0, unit = blockIdx.x / f.split;
+    const int hk = unit % f.p.Hkv, G = f.p.Hq / f.p.Hkv;
+    AttnTile t = attn_tile(f.tiles, unit / f.p.Hkv, kTileRows, f.p.B, f.p.T);
+    if (t.first >= t.seq_end) return;  // all of a cluster
     if (!f.tiles && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
     // the list begins with a sequence's last tile; here the first one has most work
     const int count = (t.seq_end - t.seq_start + kTileRows - 1) / kTileRows;
     const int tile = count - 1 - (t.first - t.seq_start) / kTileRows;
     t.first = t.seq_start + tile * kTileRows;
-    const int per_head = count - tile, steps = per_head * G;  // step = (head, query tile)
+    const int heads = (G - rank + f.split - 1) / f.split;     // this CTA's: rank, rank + split, ...
+    const int per_head = count - tile, steps = per_head * heads;  // step = (head, query tile)
 
     const uint32_t tmem = start_cta(b, 1 + 32, 2);
     constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 256 + D;
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
             int it = 0;
             for (; it < steps; ++it) {
                 const int st = it % S::kStages, use = it / S::kStages;
-                const int h = hk * G + it / per_head, token = t.first + it % per_head * kTileRows;
+                const int h = hk * G + rank + it / per_head * f.split, token = t.first + it % per_head * kTileRows;
                 bool go = !use || (tc::mbar_wait(b.free0 + st, (use - 1) & 1, b.abort, f.status, kErrFree, f.spin) &&
                                    tc::mbar_wait(b.free1 + st, (use - 1) & 1, b.abort, f.status, kErrFree, f.spin));
                 if (!__all_sync(0xffffffffu, go)) break;
@@ -355,16 +358,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         }
         go = __all_sync(0xffffffffu, go && tc::mbar_wait(b.acc, 0, b.abort, f.status, kErrAcc, f.spin));
         const int col = t.first + in_tile;
-        bool bad = false;
-        if (go && !*b.abort) {
-            tc::tc_fence_after_sync();
-            // the first four warps write dV, the others dK
-            const bool mine = col < t.seq_end;
-            __nv_bfloat16 *out = (half ? f.gk : f.gv) + ((size_t)col * f.p.Hkv + hk) * D;
-            bad = !store_sums<D>(tmem + lanes + (half ? kDk : kDv), half ? f.p.scale : 1.f,
-                                 mine ? out : nullptr) && mine;
+        const bool mine = col < t.seq_end;
+        bool bad = false, fine = go && !*b.abort;
+        // the first four warps write dV, the others dK
+        const uint32_t sums = tmem + lanes + (half ? kDk : kDv);
+        const float by = half ? f.p.scale : 1.f;
+        __nv_bfloat16 *out = (half ? f.gk : f.gv) + ((size_t)col * f.p.Hkv + hk) * D;
+        if (fine) tc::tc_fence_after_sync();
+        if (f.split == 1) {
+            if (fine) bad = !store_sums<D>(sums, by, mine ? out : nullptr) && mine;
+        } else {
+            // every CTA lays its sums out over its ring (all copies and products are done)
+            // and finishes its share of the channels, adding in rank order
+            float *own = reinterpret_cast<float *>(sm) + half * 128 * D + in_tile;
+            if (fine) {
+#pragma unroll
+                for (int i = 0; i < D; i += 32) {
+                    float x[32];
+                    tc::tmem_start(sums + i, x);
+                    tc::tmem_ready(x);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) own[(i + j) * 128] = x[j];
+                }
+            }
+            cluster_sync();
+            const int share = D / f.split;
+            const uint32_t from = tc::smem_u32(own);
+            float odd = 0.f;
+            for (int i = rank * share; i < (rank + 1) * share; i += 8) {
+                float x[8] = {};
+                for (int r = 0; r < f.split; ++r) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] += peer_float(from + (i + j) * 512, r);
+                }
+                uint32_t pk[4];
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    odd = fmaf(x[j], 0.f, fmaf(x[j + 1], 0.f, odd));
+                    pk[j / 2] = tc::bf16x2(x[j] * by, x[j + 1] * by);
+                }
+                if (mine && fine) *reinterpret_cast<uint4 *>(out + i) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+            bad = mine && fine && !(odd == 0.f);
+            cluster_sync();  // all reads and stores are made
         }
         redo_rows(b, bad, [&](int i) { redo_dkv<D>(f, t.first + i, t.seq_end, hk); });
+    }
+    if (warp >= 8 && f.split > 1) {
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
     }
     end_cta(tmem);
 }
@@ -593,12 +636,9 @@ cudaError_t launch(const AttnProblem &p, const void *o, const float *lse, const 
     if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)attn_tiles(p, kTileRows);
     constexpr uint32_t dkv_smem = BwdShape<D, true>::kBytes, dq_smem = BwdShape<D, false>::kBytes;
-    e = cudaFuncSetAttribute(attn_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             dkv_smem);
+    f.split = attn_head_split(p, kTileRows, 148);
+    e = launch_clusters(attn_dkv_kernel<D>, f, (long long)tiles * p.Hkv, kThreads, dkv_smem, f.split, st);
     if (e != cudaSuccess) return e;
-    attn_dkv_kernel<D><<<tiles * p.Hkv, kThreads, dkv_smem, st>>>(f);
-    note_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = cudaFuncSetAttribute(attn_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              dq_smem);
     if (e != cudaSuccess) return e;

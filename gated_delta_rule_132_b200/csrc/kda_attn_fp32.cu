@@ -183,6 +183,7 @@ struct F32Params {
     const float *lse, *lse2, *delta, *dO;
     float *o, *lse_out, *gq, *gk, *gv;
     int *status;  // of the workspace: nothing here can fail, the first CTA clears it
+    int split;    // dK and dV: CTAs per key tile, see attn_head_split
 };
 
 __device__ __forceinline__ AttnTile tile_of(const F32Params &f, int idx)
@@ -348,20 +349,21 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ F
     __shared__ float lse2[kWalk], del[kWalk];
     __shared__ unsigned bad;
     float *k = smem, *v = k + kRows * D, *q = v + kRows * D, *g = q + kWalk * D, *w = g + kWalk * D;
-    AttnTile t = tile_of(f, blockIdx.x / f.p.Hkv);
-    if (t.first >= t.seq_end) return;
+    const int rank = f.split > 1 ? cluster_rank() : 0, unit = blockIdx.x / f.split;
+    AttnTile t = tile_of(f, unit / f.p.Hkv);
+    if (t.first >= t.seq_end) return;  // all of a cluster
     if (!f.tiles && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
     // the list begins with a sequence's last tile; here the first one has most work
     const int count = (t.seq_end - t.seq_start + kRows - 1) / kRows;
     t.first = t.seq_start + (count - 1 - (t.first - t.seq_start) / kRows) * kRows;
-    const int hk = blockIdx.x % f.p.Hkv, G = f.p.Hq / f.p.Hkv;
+    const int hk = unit % f.p.Hkv, G = f.p.Hq / f.p.Hkv;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     if (threadIdx.x == 0) bad = 0;
     load_tile<D, kRows>(k, static_cast<const float *>(f.p.k), f.p.Hkv, hk, t.first, t.seq_end);
     load_tile<D, kRows>(v, static_cast<const float *>(f.p.v), f.p.Hkv, hk, t.first, t.seq_end);
     const float c = f.p.scale * kLog2e;
     float ak[4][D / 16] = {}, av[4][D / 16] = {};
-    for (int h = hk * G; h < (hk + 1) * G; ++h)
+    for (int h = hk * G + rank; h < (hk + 1) * G; h += f.split)
         for (int at = t.first; at < t.seq_end; at += kWalk) {
             load_stats<kWalk>(f, lse2, del, h, at, t.seq_end);
             load_tile<D, kWalk>(q, static_cast<const float *>(f.p.q), f.p.Hq, h, at, t.seq_end);
@@ -392,23 +394,38 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ F
             add_weighted<D>(w, q, ak);
             __syncthreads();
         }
+    if (f.split > 1) {  // the first CTA adds up the others' sums, kept thread by thread
+        if (rank) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e) {
+                    smem[(i * (D / 16) + e) * kThreads + threadIdx.x] = ak[i][e];
+                    smem[((4 + i) * (D / 16) + e) * kThreads + threadIdx.x] = av[i][e];
+                }
+            }
+        }
+        cluster_sync();
+        for (int r = 1; r < f.split && !rank; ++r) {
+            const uint32_t from = tc::smem_u32(smem + threadIdx.x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e) {
+                    ak[i][e] += peer_float(from + (i * (D / 16) + e) * kThreads * 4, r);
+                    av[i][e] += peer_float(from + ((4 + i) * (D / 16) + e) * kThreads * 4, r);
+                }
+            }
+        }
+        cluster_sync();
+        if (rank) return;
+    }
     const size_t out = ((size_t)t.first * f.p.Hkv + hk) * D, stride = (size_t)f.p.Hkv * D;
     const float one[4] = {1.f, 1.f, 1.f, 1.f};
     const float by[4] = {f.p.scale, f.p.scale, f.p.scale, f.p.scale};
     store_rows<D>(av, one, f.gv + out, stride, t.seq_end - t.first, &bad);
     store_rows<D>(ak, by, f.gk + out, stride, t.seq_end - t.first, &bad);
     redo_rows(&bad, [&](int r) { redo_dkv<D>(f, t.first + r, t.seq_end, hk); });
-}
-
-template <typename K>
-cudaError_t start(K kernel, const F32Params &f, long long ctas, int smem, cudaStream_t st)
-{
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)ctas, kThreads, smem, st>>>(f);
-    note_launch();
-    return cudaGetLastError();
 }
 
 // The tile list, or none for uniform sequences.
@@ -430,7 +447,8 @@ cudaError_t fwd(const AttnProblem &p, void *o, float *lse, void *workspace, cuda
     f.lse_out = lse;
     const cudaError_t e = prepare(p, false, workspace, f, st);
     if (e != cudaSuccess) return e;
-    return start(fwd_kernel<D>, f, attn_tiles(p, kRows) * p.Hq, ((kRows + 2 * kWalk) * D + kRows * kW) * 4, st);
+    return launch_clusters(fwd_kernel<D>, f, attn_tiles(p, kRows) * p.Hq, kThreads,
+                           ((kRows + 2 * kWalk) * D + kRows * kW) * 4, 1, st);
 }
 
 template <int D>
@@ -450,10 +468,10 @@ cudaError_t bwd(const AttnProblem &p, const void *o, const float *lse, const voi
     cudaError_t e = prepare(p, true, workspace, f, st);
     if (e == cudaSuccess) e = launch_attn_delta(p, o, lse, dO, delta, lse2, st);
     const long long tiles = attn_tiles(p, kRows);
-    if (e == cudaSuccess)
-        e = start(dkv_kernel<D>, f, tiles * p.Hkv, (2 * (kRows + kWalk) * D + kRows * kW) * 4, st);
-    if (e == cudaSuccess)
-        e = start(dq_kernel<D>, f, tiles * p.Hq, (2 * (kRows + kWalk) * D + kRows * kW) * 4, st);
+    const size_t smem = (2 * (kRows + kWalk) * D + kRows * kW) * 4;
+    f.split = attn_head_split(p, kRows, 148 * 4);
+    if (e == cudaSuccess) e = launch_clusters(dkv_kernel<D>, f, tiles * p.Hkv, kThreads, smem, f.split, st);
+    if (e == cudaSuccess) e = launch_clusters(dq_kernel<D>, f, tiles * p.Hq, kThreads, smem, 1, st);
     return e;
 }
 
