@@ -76,9 +76,9 @@ struct Bars {
     }
 };
 
-// full0_count: arrivals that fill a stage of the first ring; free1_count: that free one of
-// the second (the first is always freed by two).
-__device__ __forceinline__ uint32_t start_cta(const Bars &b, int full0_count, int free1_count)
+// full0_count: arrivals that fill a stage of the first ring; warps: that issue products
+// (the first ring's stages are freed by all of them).
+__device__ __forceinline__ uint32_t start_cta(const Bars &b, int full0_count, int warps)
 {
     const int warp = threadIdx.x >> 5;
     if (warp == 8) tc::tmem_alloc(b.tmem_slot, 512);
@@ -86,9 +86,9 @@ __device__ __forceinline__ uint32_t start_cta(const Bars &b, int full0_count, in
         tc::mbar_init(b.stay, 1);
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(b.full0 + i, full0_count);
-            tc::mbar_init(b.free0 + i, 2);
+            tc::mbar_init(b.free0 + i, warps);
             tc::mbar_init(b.full1 + i, 1);
-            tc::mbar_init(b.free1 + i, free1_count);
+            tc::mbar_init(b.free1 + i, 1);
         }
         tc::mbar_init(b.s_full, 1);
         tc::mbar_init(b.s_full + 1, 1);
@@ -97,7 +97,7 @@ __device__ __forceinline__ uint32_t start_cta(const Bars &b, int full0_count, in
         tc::mbar_init(b.dp_full, 1);
         tc::mbar_init(b.p_full, 8);
         tc::mbar_init(b.ds_full, 8);
-        tc::mbar_init(b.acc, 2);
+        tc::mbar_init(b.acc, warps);
         *b.abort = 0;
         for (int i = 0; i < 4; ++i) b.bad[i] = 0;
         tc::fence_mbar_init();
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     const int heads = (G - rank + f.split - 1) / f.split;     // this CTA's: rank, rank + split, ...
     const int per_head = count - tile, steps = per_head * heads;  // step = (head, query tile)
 
-    const uint32_t tmem = start_cta(b, 1 + 32, 2);
+    const uint32_t tmem = start_cta(b, 1 + 32, 1);
     constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 256 + D;
     const float *stats = reinterpret_cast<const float *>(sm + S::kStats);
 
@@ -263,37 +263,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
                 }
             }
         }
-        // warp 8 issues S and dV, warp 10 dP and dK: what a product reads in TMEM its warp's
-        // next one overwrites, in the order of issue
-        if (warp == 8 || warp == 10) {
-            const bool first = warp == 8;
+        // One warp issues: dV and the next S when P is there, dK and the next dP when dS is.
+        // What a product reads in TMEM a later one overwrites, in the order of issue. (A
+        // warp each for S, dV and for dP, dK: 5% slower, as their products hold each other up.)
+        if (warp == 8) {
             const uint32_t lead = lane == 0;
-            const uint32_t stay = tc::smem_u32(sm + S::kStay) + (first ? 0 : S::kTile);
+            const uint32_t k = tc::smem_u32(sm + S::kStay), v = k + S::kTile;
             const uint32_t q = tc::smem_u32(sm + S::kRing0), dO = tc::smem_u32(sm + S::kRing1);
-            const uint32_t rows = first ? q : dO, back = first ? dO : q;
-            const uint32_t pair = tmem + (first ? kS : kDp), acc = tmem + (first ? kDv : kDk);
-            uint64_t *rows_full = first ? b.full0 : b.full1, *back_full = first ? b.full1 : b.full0;
-            uint64_t *back_free = first ? b.free1 : b.free0, *rows_free = first ? b.free0 : b.free1;
-            uint64_t *done = first ? b.s_full : b.dp_full, *weights = first ? b.p_full : b.ds_full;
-            auto wait = [&](uint64_t *bar, int n, int code) {
-                return __all_sync(0xffffffffu, tc::mbar_wait(bar, n & 1, b.abort, f.status, code, f.spin));
+            auto wait = [&](uint64_t *x, int nx, uint64_t *y, int ny, int code) {
+                return tc::wait_both(x, nx, y, ny, b.abort, f.status, code, f.spin);
             };
-            bool go = wait(b.stay, 0, kErrStay);
-            for (int it = 0; it <= steps && go; ++it) {
-                const int st = it % S::kStages, before = (it + S::kStages - 1) % S::kStages;
-                if (it < steps) go = wait(rows_full + st, it / S::kStages, kErrA);
-                if (it > 0) {
-                    go = go && wait(back_full + before, (it - 1) / S::kStages, kErrB) &&
-                         wait(weights, it - 1, first ? kErrP : kErrDs);
-                    if (!go) break;
-                    tc::tc_fence_after_sync();
-                    tc::mma_weights_rows<D, 64>(acc, pair, back + before * S::kTile, it > 1, lead);
-                    tc::commit(back_free + before, lead);
+            bool go = wait(b.stay, 0, b.full0, 0, kErrStay);
+            if (go) {
+                tc::mma_rows_rows<D>(tmem + kS, k, q, lead);
+                tc::commit(b.s_full, lead);
+                go = wait(b.stay, 0, b.full1, 0, kErrB);
+            }
+            if (go) {
+                tc::mma_rows_rows<D>(tmem + kDp, v, dO, lead);
+                tc::commit(b.dp_full, lead);
+            }
+            for (int it = 0; it < steps && go; ++it) {
+                const int st = it % S::kStages;
+                const int next = min(it + 1, steps - 1), nst = next % S::kStages, use = next / S::kStages;
+                go = wait(b.p_full, it, b.full0 + nst, use, kErrP);
+                if (!go) break;
+                tc::tc_fence_after_sync();
+                tc::mma_weights_rows<D, 64>(tmem + kDv, tmem + kS, dO + st * S::kTile, it > 0, lead);
+                if (next > it) {
+                    tc::mma_rows_rows<D>(tmem + kS, k, q + nst * S::kTile, lead);
+                    tc::commit(b.s_full, lead);
                 }
-                if (!go || it == steps) break;
-                tc::mma_rows_rows<D>(pair, stay, rows + st * S::kTile, lead);
-                tc::commit(done, lead);
-                tc::commit(rows_free + st, lead);
+                tc::commit(b.free1 + st, lead);
+                go = wait(b.ds_full, it, b.full1 + nst, use, kErrDs);
+                if (!go) break;
+                tc::tc_fence_after_sync();
+                tc::mma_weights_rows<D, 64>(tmem + kDk, tmem + kDp, q + st * S::kTile, it > 0, lead);
+                if (next > it) {
+                    tc::mma_rows_rows<D>(tmem + kDp, v, dO + nst * S::kTile, lead);
+                    tc::commit(b.dp_full, lead);
+                }
+                tc::commit(b.free0 + st, lead);
             }
             tc::commit(b.acc, lead);
             tc::mbar_drain(b.acc, 0, f.status, kErrBwdDrain);
@@ -427,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     if (t.first >= t.seq_end) return;
     const int last = (t.first - t.seq_start) / kTileRows, steps = last + 1;  // key tiles, diagonal first
 
-    const uint32_t tmem = start_cta(b, 1, 1);
+    const uint32_t tmem = start_cta(b, 1, 2);
     constexpr uint32_t kS = 0, kDp = 256, kDq = 384;  // two score tiles in turn
 
     if (warp >= 8) {
@@ -470,7 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
             if (warp == 8) {
                 for (int it = 0; it < steps && go; ++it) {
                     const int st = it % S::kStages0;
-                    go = wait(b.full0 + st, it / S::kStages0, kErrA) && (it < 2 || wait(b.s_free + (it & 1), (it >> 1) - 1, kErrS));
+                    // before the third step only the keys are due
+                    go = tc::wait_both(b.full0 + st, it / S::kStages0, it < 2 ? b.stay : b.s_free + (it & 1),
+                                       it < 2 ? 0 : (it >> 1) - 1, b.abort, f.status, kErrA, f.spin);
                     if (!go) break;
                     tc::tc_fence_after_sync();
                     tc::mma_rows_rows<D>(tmem + kS + (it & 1) * 128, q, k + st * S::kTile, lead);
@@ -480,18 +492,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
             } else {
                 for (int it = 0; it <= steps && go; ++it) {
                     const int st = it % S::kStages, st0 = (it + S::kStages0 - 1) % S::kStages0;
-                    if (it < steps) go = wait(b.full1 + st, it / S::kStages, kErrB);
-                    if (it > 0) {
-                        go = go && wait(b.full0 + st0, (it - 1) / S::kStages0, kErrA) && wait(b.ds_full, it - 1, kErrDs);
-                        if (!go) break;
-                        tc::tc_fence_after_sync();
-                        tc::mma_weights_rows<D, 64>(tmem + kDq, tmem + kDp, k + st0 * S::kTile, it > 1, lead);
-                        tc::commit(b.free0 + st0, lead);
+                    const int due = min(it, steps - 1);  // values
+                    // dS says that the step's S was formed, so that its keys are there
+                    go = tc::wait_both(b.full1 + due % S::kStages, due / S::kStages, it ? b.ds_full : b.stay,
+                                       it ? it - 1 : 0, b.abort, f.status, kErrDs, f.spin);
+                    if (!go) break;
+                    tc::tc_fence_after_sync();
+                    if (it > 0) tc::mma_weights_rows<D, 64>(tmem + kDq, tmem + kDp, k + st0 * S::kTile, it > 1, lead);
+                    if (it < steps) {
+                        tc::mma_rows_rows<D>(tmem + kDp, dO, v + st * S::kTile, lead);
+                        tc::commit(b.dp_full, lead);
+                        tc::commit(b.free1 + st, lead);
                     }
-                    if (!go || it == steps) break;
-                    tc::mma_rows_rows<D>(tmem + kDp, dO, v + st * S::kTile, lead);
-                    tc::commit(b.dp_full, lead);
-                    tc::commit(b.free1 + st, lead);
+                    if (it > 0) tc::commit(b.free0 + st0, lead);
                 }
             }
             tc::commit(b.acc, lead);

@@ -141,11 +141,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             bool go = wait(q_full, 0, kErrQ);
             for (int it = 0; it <= steps && go; ++it) {
                 const uint32_t k = ring + it % S::kStages * 2 * S::kTile, v = k + S::kTile;
-                go = wait(kv_full + it % S::kStages, it / S::kStages, kErrKv);
+                const bool both = it > begin;  // and the first half's probabilities
+                go = tc::wait_both(kv_full + it % S::kStages, it / S::kStages, both ? p_full + 2 * w : q_full,
+                                   both ? it - 1 - begin : 0, abort, f.status, kErrKv, f.spin);
 #pragma unroll
                 for (int h2 = 0; h2 < 2; ++h2) {
                     if (go && it > begin) {  // O += P V of the same half of the step before
-                        go = wait(p_full + 2 * w + h2, it - 1 - begin, kErrP);
+                        if (h2) go = wait(p_full + 2 * w + 1, it - 1 - begin, kErrP);
                         if (!go) break;
                         tc::tc_fence_after_sync();
                         tc::mma_weights_half<D>(o_acc, s_acc + h2 * 64, v, h2, it - 1 > begin || h2 > 0, lead);

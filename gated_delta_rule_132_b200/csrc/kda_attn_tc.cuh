@@ -90,6 +90,15 @@ __device__ __forceinline__ void tma_load_4d(void *dst_smem, const void *tmap, in
 // in uniform registers. Issued from a single-lane branch, each instruction cost the
 // moves of its operands there.
 
+// Wait for two phases at once, by the whole warp: every other lane polls the other
+// barrier, since a poll costs some 150 cycles even of a phase that is complete.
+__device__ __forceinline__ bool wait_both(uint64_t *a, int na, uint64_t *b, int nb, volatile int *abort,
+                                          int *err, int code, uint32_t limit)
+{
+    const bool odd = threadIdx.x & 1;
+    return __all_sync(0xffffffffu, mbar_wait(odd ? b : a, (odd ? nb : na) & 1, abort, err, code, limit));
+}
+
 // D[tmem] (+)= A[smem desc] * B[smem desc], bf16 inputs, fp32 accumulate.
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                        uint32_t idesc, uint32_t accumulate, uint32_t lead)

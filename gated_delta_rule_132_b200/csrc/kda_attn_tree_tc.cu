@@ -193,11 +193,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             bool go = wait(q_full, 0, kErrQ);
             int nth = 0;
             for (int it = kPair ? 0 : w; go; it += kEvery, ++nth) {
-                const int st = it % S::kStages, last = it - kEvery, before = (last + S::kStages) % S::kStages;
-                if (it < steps) go = wait(k_full + st, it / S::kStages, kErrK);
-                if (nth > 0) {  // O += P V of the half's step before
-                    go = go && wait(v_full + before, last / S::kStages, kErrV) && wait(p_full + w, nth - 1, kErrP);
-                    if (!go) break;
+                const int st = it % S::kStages, before = (it - kEvery + S::kStages) % S::kStages;
+                // P says that the step's values are there: its rows have looked which keys are
+                go = tc::wait_both(it < steps ? k_full + st : q_full, it < steps ? it / S::kStages : 0,
+                                   nth > 0 ? p_full + w : q_full, nth > 0 ? nth - 1 : 0, abort, f.status, kErrP, f.spin);
+                if (go && nth > 0) {  // O += P V of the half's step before
                     tc::tc_fence_after_sync();
                     tc::mma_weights_rows<D, 32>(o_acc, s_acc, v + before * S::kTile, nth > 1, lead);
                 }
