@@ -1,7 +1,10 @@
 // kda_attn_fwd.cu — causal prompt attention on the tensor cores (bf16, d = 32, 64, 128).
 //
-// One CTA per (256 query tokens, query head): two query tiles of 128 rows that share
-// the key/value tiles, walked from the diagonal down to the sequence's first tile.
+// A work item is (256 query tokens, query head): two query tiles of 128 rows that share
+// the key/value tiles, walked from the diagonal down to the sequence's first tile. One
+// persistent CTA per SM takes items in order of falling work; its loads and products
+// run on into the next item while the rows of the last one are written. (With a CTA per
+// item, beginning and end cost 8 us of an SM, as much as five steps.)
 // Per tile pair S = Q K^T goes to TMEM, one thread per row turns it into
 // P = 2^(c s - c m) (c = scale log2 e, m the row's running reference) in registers,
 // writes P in bf16 over S, and O += P V reads it from there. Warps 0-3 own the rows of
@@ -35,6 +38,7 @@ struct FwdParams {
     __nv_bfloat16 *o;
     float *lse;
     int *status;
+    int items;
     uint32_t spin;
     int starve;
 };
@@ -58,6 +62,28 @@ __device__ __noinline__ void recompute_row(const FwdParams &f, int row, int star
     attn_row_fwd<__nv_bfloat16, D>(f.p, row, start, h, f.o, f.lse);
 }
 
+// An item: its query tiles, and the key tiles from the last one down: step it reads key
+// tile last - it; query tile w takes part from step begin(w) on.
+struct FwdItem {
+    int h, first, seq_start, seq_end, last, steps;
+    bool two;
+    __device__ __forceinline__ bool get(const FwdParams &f, int n)
+    {
+        const int idx = nth_item(n, f.items);
+        if (idx < 0) return false;
+        const AttnTile t = attn_tile(f.tiles, idx / f.p.Hq, kRows, f.p.B, f.p.T);
+        if (t.first >= t.seq_end) return false;  // the list's unused end
+        h = idx % f.p.Hq;
+        first = t.first; seq_start = t.seq_start; seq_end = t.seq_end;
+        two = first + kTileRows < seq_end;
+        last = (first - seq_start) / kTileRows + two;
+        steps = last + 1;
+        return true;
+    }
+    // an absent second tile never begins
+    __device__ __forceinline__ int begin(int w) const { return w ? (two ? 0 : steps + 1) : two; }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdParams f)
 {
@@ -66,38 +92,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     uint8_t *sm = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kBars);
-    uint64_t *q_full = bars;
-    uint64_t *kv_full = bars + 1, *kv_free = kv_full + S::kStages;
-    uint64_t *s_full = kv_free + S::kStages;  // [tile][half] scores are in TMEM
+    uint64_t *q_full = bars, *q_free = bars + 1, *done = bars + 2;
+    uint64_t *kv_full = bars + 3, *kv_free = kv_full + S::kStages;
+    uint64_t *s_full = kv_free + S::kStages;  // [tile][half] scores are in TMEM; once more behind an
+                                              // item's last step: the products of that half are done
     uint64_t *p_full = s_full + 4;            // [tile][half] probabilities are (one arrival per warp)
-    uint64_t *o_full = p_full + 4;            // all products are done
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_full + 1);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(p_full + 4);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x % f.p.Hq;
-    const AttnTile t = attn_tile(f.tiles, blockIdx.x / f.p.Hq, kRows, f.p.B, f.p.T);
-    if (t.first >= t.seq_end) return;  // the list's unused end
     if (!f.tiles && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
-
-    // query tiles, and the key tiles from the last one down: step it reads key tile
-    // last - it; tile w takes part from step begin[w] on
-    const bool two = t.first + kTileRows < t.seq_end;
-    const int diag0 = (t.first - t.seq_start) / kTileRows;
-    const int last = diag0 + two, steps = last + 1;
-
     if (warp == 8) tc::tmem_alloc(tmem_slot, 512);
     if (threadIdx.x == 0) {
         tc::mbar_init(q_full, 1);
+        tc::mbar_init(q_free, 2);
+        tc::mbar_init(done, 2);
         for (int i = 0; i < S::kStages; ++i) {
             tc::mbar_init(kv_full + i, 1);
-            tc::mbar_init(kv_free + i, 1 + two);
+            tc::mbar_init(kv_free + i, 2);
         }
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(s_full + i, 1);
             tc::mbar_init(p_full + i, 4);
         }
-        tc::mbar_init(o_full, 1 + two);
         *abort = 0;
         tc::fence_mbar_init();
     }
@@ -105,80 +122,96 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     __syncthreads();
     tc::tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    FwdItem t;
 
     if (warp >= 8) {
         tc::fewer_registers<kRegsOther>();
         if (warp == 9 && lane == 0 && !f.starve) {
-            const int hk = h / (f.p.Hq / f.p.Hkv);
-            tc::mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * S::kTile);
-            for (int w = 0; w <= two; ++w)
-                tc::load_tile<D>(sm + S::kQ + w * S::kTile, &f.q, h, t.first + w * kTileRows, q_full);
-            int p = 0;
-            for (; p <= steps; ++p) {
-                const int st = p % S::kStages, use = p / S::kStages;
-                uint8_t *to = sm + S::kRing + st * 2 * S::kTile;
-                const int token = t.seq_start + (last - p) * kTileRows;
-                if (use && !tc::mbar_wait(kv_free + st, (use - 1) & 1, abort, f.status, kErrFree, f.spin)) break;
-                tc::mbar_arrive_expect_tx(kv_full + st, ((p < steps) + (p > 0)) * S::kTile);
-                if (p < steps) tc::load_tile<D>(to, &f.k, hk, token, kv_full + st);
-                if (p > 0) tc::load_tile<D>(to + S::kTile, &f.v, hk, token + kTileRows, kv_full + st);
+            int g = 0, n = 0;  // stages filled, items begun
+            bool go = true;
+            for (; go && t.get(f, n); ++n) {
+                const int hk = t.h / (f.p.Hq / f.p.Hkv);
+                if (n && !tc::mbar_wait(q_free, (n - 1) & 1, abort, f.status, kErrFree, f.spin)) break;
+                tc::mbar_arrive_expect_tx(q_full, (t.two ? 2 : 1) * S::kTile);
+                for (int w = 0; w <= t.two; ++w)
+                    tc::load_tile<D>(sm + S::kQ + w * S::kTile, &f.q, t.h, t.first + w * kTileRows, q_full);
+                for (int p = 0; p <= t.steps; ++p, ++g) {
+                    const int st = g % S::kStages, use = g / S::kStages;
+                    uint8_t *to = sm + S::kRing + st * 2 * S::kTile;
+                    const int token = t.seq_start + (t.last - p) * kTileRows;
+                    go = !use || tc::mbar_wait(kv_free + st, (use - 1) & 1, abort, f.status, kErrFree, f.spin);
+                    if (!go) break;
+                    tc::mbar_arrive_expect_tx(kv_full + st, ((p < t.steps) + (p > 0)) * S::kTile);
+                    if (p < t.steps) tc::load_tile<D>(to, &f.k, hk, token, kv_full + st);
+                    if (p > 0) tc::load_tile<D>(to + S::kTile, &f.v, hk, token + kTileRows, kv_full + st);
+                }
             }
             // whatever the other warps do, the copies land before the memory is let go
-            tc::mbar_drain(q_full, 0, f.status, kErrDrain);
-            for (int i = max(0, p - S::kStages); i < p; ++i)
+            if (n) tc::mbar_drain(q_full, (n - 1) & 1, f.status, kErrDrain);
+            for (int i = max(0, g - S::kStages); i < g; ++i)
                 tc::mbar_drain(kv_full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
         }
         // one warp issues for each query tile
-        const int w = warp == 8 ? 0 : warp == 10 && two ? 1 : -1;
-        if (w >= 0) {
+        if (warp == 8 || warp == 10) {
+            const int w = warp == 10;
             const uint32_t lead = lane == 0;
             const uint32_t q = tc::smem_u32(sm + S::kQ + w * S::kTile), ring = tc::smem_u32(sm + S::kRing);
             const uint32_t s_acc = tmem + S::kTmemS + w * 128, o_acc = tmem + S::kTmemO + w * D;
-            const int begin = two && w == 0;
             auto wait = [&](uint64_t *bar, int n, int code) {
                 return __all_sync(0xffffffffu, tc::mbar_wait(bar, n & 1, abort, f.status, code, f.spin));
             };
-            bool go = wait(q_full, 0, kErrQ);
-            for (int it = 0; it <= steps && go; ++it) {
-                const uint32_t k = ring + it % S::kStages * 2 * S::kTile, v = k + S::kTile;
-                const bool both = it > begin;  // and the first half's probabilities
-                go = tc::wait_both(kv_full + it % S::kStages, it / S::kStages, both ? p_full + 2 * w : q_full,
-                                   both ? it - 1 - begin : 0, abort, f.status, kErrKv, f.spin);
+            int g = 0, weights = 0;  // stages read; phases of p_full waited for (either half)
+            bool go = true;
+            for (int n = 0; go && t.get(f, n); ++n) {
+                const int begin = t.begin(w), steps = t.steps;
+                go = wait(q_full, n, kErrQ);
+                for (int it = 0; it <= steps && go; ++it, ++g) {
+                    const uint32_t k = ring + g % S::kStages * 2 * S::kTile, v = k + S::kTile;
+                    const bool both = it > begin;  // and the first half's probabilities
+                    uint64_t *kv = kv_full + g % S::kStages;
+                    go = tc::wait_both(kv, g / S::kStages, both ? p_full + 2 * w : kv, both ? weights : g / S::kStages,
+                                       abort, f.status, kErrKv, f.spin);
 #pragma unroll
-                for (int h2 = 0; h2 < 2; ++h2) {
-                    if (go && it > begin) {  // O += P V of the same half of the step before
-                        if (h2) go = wait(p_full + 2 * w + 1, it - 1 - begin, kErrP);
-                        if (!go) break;
-                        tc::tc_fence_after_sync();
-                        tc::mma_weights_half<D>(o_acc, s_acc + h2 * 64, v, h2, it - 1 > begin || h2 > 0, lead);
+                    for (int h2 = 0; h2 < 2; ++h2) {
+                        if (go && both) {  // O += P V of the same half of the step before
+                            if (h2) go = wait(p_full + 2 * w + 1, weights, kErrP);
+                            if (!go) break;
+                            tc::tc_fence_after_sync();
+                            tc::mma_weights_half<D>(o_acc, s_acc + h2 * 64, v, h2, it - 1 > begin || h2 > 0, lead);
+                        }
+                        if (!go || it < begin) continue;
+                        // behind the last step the arrival alone is due: those products are done
+                        if (it < steps) tc::mma_rows_half<D>(s_acc + h2 * 64, q, k, h2, lead);
+                        tc::commit(s_full + 2 * w + h2, lead);
                     }
-                    if (!go || it < begin) continue;
-                    // behind the last step the arrival alone is due: those products are done
-                    if (it < steps) tc::mma_rows_half<D>(s_acc + h2 * 64, q, k, h2, lead);
-                    tc::commit(s_full + 2 * w + h2, lead);
+                    weights += both;
+                    if (!go) break;
+                    if (it == steps - 1) tc::commit(q_free, lead);
+                    tc::commit(kv_free + g % S::kStages, lead);
                 }
-                if (go && it < steps) tc::commit(kv_free + it % S::kStages, lead);
             }
-            tc::commit(o_full, lead);
-            tc::mbar_drain(o_full, 0, f.status, kErrDrain);
+            tc::commit(done, lead);
+            tc::mbar_drain(done, 0, f.status, kErrDrain);
         }
     } else {
         tc::more_registers<kRegsSoftmax>();
-        if (warp < (two ? 8 : 4)) {
-            const int w = warp >> 2, begin = two && w == 0;
-            const int in_tile = threadIdx.x & 127, row = t.first + w * kTileRows + in_tile;
-            const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's TMEM lanes (32 each, bits 16 up)
-            const uint32_t ts = tmem + lanes + S::kTmemS + w * 128;
-            const uint32_t to = tmem + lanes + S::kTmemO + w * D;
-            const float c = f.p.scale * 1.44269504088896340736f;
+        const int w = warp >> 2, in_tile = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's TMEM lanes (32 each, bits 16 up)
+        const uint32_t ts = tmem + lanes + S::kTmemS + w * 128;
+        const uint32_t to = tmem + lanes + S::kTmemO + w * D;
+        const float c = f.p.scale * 1.44269504088896340736f;
+        int base = 0;  // phases of s_full before this item (of either half)
+        bool go = true;
+        for (int n = 0; go && t.get(f, n); ++n) {
+            if (w && !t.two) continue;
+            const int row = t.first + w * kTileRows + in_tile;
             float m = -INFINITY, l = 0.f;  // reference (unscaled score) and sum
-            bool go = true;
-            const int units = 2 * (steps - begin);  // halves of key tiles, the diagonal's first
+            const int units = 2 * (t.steps - t.begin(w));  // halves of key tiles, the diagonal's first
             for (int u = 0; u < units; ++u) {
                 const int half = u & 1;
                 const uint32_t here = ts + half * 64;
-                go = __all_sync(0xffffffffu, tc::mbar_wait(s_full + 2 * w + half, (u >> 1) & 1, abort, f.status,
-                                                           kErrS, f.spin));
+                go = __all_sync(0xffffffffu, tc::mbar_wait(s_full + 2 * w + half, (base + (u >> 1)) & 1, abort,
+                                                           f.status, kErrS, f.spin));
                 if (!go) break;
                 tc::tc_fence_after_sync();
                 float s[64];
@@ -226,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         break;
                     }
                     // the next scores' arrival says that the products so far are complete
-                    go = __all_sync(0xffffffffu, tc::mbar_wait(s_full + 2 * w + (half ^ 1), ((u + 1) >> 1) & 1,
+                    go = __all_sync(0xffffffffu, tc::mbar_wait(s_full + 2 * w + (half ^ 1), (base + ((u + 1) >> 1)) & 1,
                                                                abort, f.status, kErrS, f.spin));
                     if (!go) break;
                     tc::tc_fence_after_sync();
@@ -250,41 +283,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(p_full + 2 * w + half);
             }
-            go = __all_sync(0xffffffffu, go && tc::mbar_wait(o_full, 0, abort, f.status, kErrO, f.spin));
-            if (go && !*abort) {
-                tc::tc_fence_after_sync();
-                const bool mine = row < t.seq_end;
-                const float inv = 1.f / l;
-                __nv_bfloat16 *out = f.o + ((size_t)row * f.p.Hq + h) * D;
-                float odd = 0.f;  // NaN if any value is not finite
+            // the arrivals behind the last step: all products are done
+            base += units / 2 + 1;
+            go = go && tc::wait_both(s_full + 2 * w, base - 1, s_full + 2 * w + 1, base - 1, abort, f.status, kErrO, f.spin);
+            if (!go || *abort) break;
+            tc::tc_fence_after_sync();
+            const bool mine = row < t.seq_end;
+            const float inv = 1.f / l;
+            __nv_bfloat16 *out = f.o + ((size_t)row * f.p.Hq + t.h) * D;
+            float odd = 0.f;  // NaN if any value is not finite
 #pragma unroll
-                for (int i = 0; i < D; i += 32) {
-                    float x[32];
-                    tc::tmem_start(to + i, x);
-                    tc::tmem_ready(x);
-                    uint32_t pk[16];
+            for (int i = 0; i < D; i += 32) {
+                float x[32];
+                tc::tmem_start(to + i, x);
+                tc::tmem_ready(x);
+                uint32_t pk[16];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        x[j] *= inv;
-                        x[j + 1] *= inv;
-                        odd = fmaf(x[j], 0.f, fmaf(x[j + 1], 0.f, odd));
-                        pk[j / 2] = tc::bf16x2(x[j], x[j + 1]);
-                    }
-                    if (mine) {
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4)
-                            *reinterpret_cast<uint4 *>(out + i + 2 * j) =
-                                make_uint4(pk[j], pk[j + 1], pk[j + 2], pk[j + 3]);
-                    }
+                for (int j = 0; j < 32; j += 2) {
+                    x[j] *= inv;
+                    x[j + 1] *= inv;
+                    odd = fmaf(x[j], 0.f, fmaf(x[j + 1], 0.f, odd));
+                    pk[j / 2] = tc::bf16x2(x[j], x[j + 1]);
                 }
-                if (mine && f.lse) f.lse[(size_t)row * f.p.Hq + h] = m * f.p.scale + logf(l);
-                __syncwarp();
-                unsigned bad = __ballot_sync(0xffffffffu, mine && !(odd == 0.f));
-                for (; bad; bad &= bad - 1)
-                    recompute_row<D>(f, row - lane + __ffs(bad) - 1, t.seq_start, h);
+                if (mine) {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<uint4 *>(out + i + 2 * j) =
+                            make_uint4(pk[j], pk[j + 1], pk[j + 2], pk[j + 3]);
+                }
             }
+            if (mine && f.lse) f.lse[(size_t)row * f.p.Hq + t.h] = m * f.p.scale + logf(l);
+            __syncwarp();
+            unsigned bad = __ballot_sync(0xffffffffu, mine && !(odd == 0.f));
+            for (; bad; bad &= bad - 1)
+                recompute_row<D>(f, row - lane + __ffs(bad) - 1, t.seq_start, t.h);
             tc::tc_fence_before_sync();
         }
+        tc::tc_fence_before_sync();
     }
     __syncthreads();
     if (warp == 8) {
@@ -303,6 +338,7 @@ cudaError_t launch(const AttnProblem &p, void *o, float *lse, void *workspace, c
     f.o = static_cast<__nv_bfloat16 *>(o);
     f.lse = lse;
     f.status = reinterpret_cast<int *>(ws);
+    f.items = (int)(attn_tiles(p, kRows) * p.Hq);
     const DebugKnobs dbg = debug_knobs();
     f.spin = dbg.wait_limit ? dbg.wait_limit : tc::kSpinLimit;
     f.starve = dbg.starve_carry;
@@ -319,7 +355,7 @@ cudaError_t launch(const AttnProblem &p, void *o, float *lse, void *workspace, c
     const cudaError_t e = cudaFuncSetAttribute(
         attn_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdShape<D>::kBytes);
     if (e != cudaSuccess) return e;
-    attn_fwd_kernel<D><<<(unsigned)(attn_tiles(p, kRows) * p.Hq), kThreads, FwdShape<D>::kBytes,
+    attn_fwd_kernel<D><<<(unsigned)(f.items < 148 ? f.items : 148), kThreads, FwdShape<D>::kBytes,
                          st>>>(f);
     note_launch();
     return cudaGetLastError();

@@ -41,6 +41,15 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnTile *list, int idx, int
     return AttnTile{b * T + t * rows, b * T, (b + 1) * T, 0};
 }
 
+// The n-th work item of a persistent CTA, -1 behind the last: every other round goes
+// through the CTAs backwards, so that with items in order of falling work the CTA with
+// the most work of one round gets the least of the next.
+__device__ __forceinline__ int nth_item(int n, int items)
+{
+    const long long at = (long long)n * gridDim.x + (n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    return at < items ? (int)at : -1;
+}
+
 #ifdef __CUDACC__
 namespace tc {
 
