@@ -16,8 +16,8 @@ struct AttnProblem {
 };
 
 // One tile of consecutive tokens of one sequence: the unit of work of the prompt
-// kernels, listed longest sequence first and, within a sequence, the last tile
-// (the one that sees most keys) first, so that the last CTAs to start are short.
+// kernels, listed by falling place in the sequence (see kda_attn_plan.cu), since later
+// tiles see more keys.
 struct __align__(16) AttnTile {
     int first;      // packed token of the tile's first row
     int seq_start;  // packed token range of its sequence

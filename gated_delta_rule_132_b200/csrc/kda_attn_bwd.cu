@@ -15,6 +15,8 @@
 //
 // Rows whose result is not finite are computed again from the visible pairs alone, as
 // in the forward (0 times what a masked place holds may be NaN).
+#include <algorithm>
+
 #include "kda_attn_rows.cuh"
 #include "kda_attn_tc.cuh"
 
@@ -37,6 +39,7 @@ struct BwdParams {
     uint32_t spin;
     int starve;
     int split;  // dK and dV: CTAs per key tile, see attn_head_split
+    int dkv_items, dq_items;
 };
 
 // Shared memory: two tiles that stay (k, v or q, dO), and a ring of stages of the two
@@ -50,7 +53,7 @@ struct BwdShape {
     static constexpr uint32_t kStay = 0, kRing0 = 2 * kTile, kRing1 = kRing0 + kStages0 * kTile;
     static constexpr uint32_t kStats = kRing1 + kStages * kTile;  // [stage][lse2, D][128]
     static constexpr uint32_t kBars = kStats + (kKeys ? kStages * 1024 : 0);
-    static constexpr uint32_t kBytes = kBars + 256 + 1024;
+    static constexpr uint32_t kBytes = kBars + 320 + 1024;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -58,15 +61,16 @@ enum : int { kErrStay = 111, kErrA, kErrB, kErrFree, kErrS, kErrDp, kErrP, kErrD
              kErrBwdDrain };
 
 struct Bars {
-    uint64_t *stay, *full0, *free0, *full1, *free1, *s_full, *s_free, *dp_full, *p_full, *ds_full, *acc;
+    uint64_t *stay, *stay_free, *done, *full0, *free0, *full1, *free1, *s_full, *s_free, *dp_full, *p_full, *ds_full, *acc;
     uint32_t *tmem_slot;
     volatile int *abort;
-    uint32_t *bad;  // [4] rows to compute again
+    uint32_t *bad;  // [2][5] rows to compute again, and whether to give up; of items in turn
     __device__ Bars(uint8_t *at)
     {
         constexpr int kMost = 4;  // stages
         stay = reinterpret_cast<uint64_t *>(at);
-        full0 = stay + 1; free0 = full0 + kMost;
+        stay_free = stay + 1; done = stay + 2;
+        full0 = stay + 3; free0 = full0 + kMost;
         full1 = free0 + kMost; free1 = full1 + kMost;
         s_full = free1 + kMost; s_free = s_full + 2; dp_full = s_free + 2; p_full = dp_full + 1;
         ds_full = p_full + 1; acc = ds_full + 1;
@@ -84,6 +88,8 @@ __device__ __forceinline__ uint32_t start_cta(const Bars &b, int full0_count, in
     if (warp == 8) tc::tmem_alloc(b.tmem_slot, 512);
     if (threadIdx.x == 0) {
         tc::mbar_init(b.stay, 1);
+        tc::mbar_init(b.stay_free, warps);
+        tc::mbar_init(b.done, warps);
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(b.full0 + i, full0_count);
             tc::mbar_init(b.free0 + i, warps);
@@ -97,9 +103,9 @@ __device__ __forceinline__ uint32_t start_cta(const Bars &b, int full0_count, in
         tc::mbar_init(b.dp_full, 1);
         tc::mbar_init(b.p_full, 8);
         tc::mbar_init(b.ds_full, 8);
-        tc::mbar_init(b.acc, warps);
+        tc::mbar_init(b.acc, 1);
         *b.abort = 0;
-        for (int i = 0; i < 4; ++i) b.bad[i] = 0;
+        for (int i = 0; i < 10; ++i) b.bad[i] = 0;
         tc::fence_mbar_init();
     }
     tc::tc_fence_before_sync();
@@ -169,20 +175,28 @@ __device__ __forceinline__ bool store_sums(uint32_t taddr, float by, __nv_bfloat
     return odd == 0.f;
 }
 
-// The rows that a thread of their own flagged, one warp each, after all stores. All eight
-// warps come here, also where the CTA has given up.
+// The rows of the n-th item that a thread of their own flagged, one warp each, after all
+// stores. All eight warps come here for every item; returns, to all of them alike,
+// whether none has given up.
 template <typename F>
-__device__ __forceinline__ void redo_rows(const Bars &b, bool mine_bad, F redo)
+__device__ __forceinline__ bool redo_rows(const Bars &b, int n, bool fine, bool mine_bad, F redo)
 {
     const int warp = threadIdx.x >> 5;  // 0..7, two warps per 32 rows
+    volatile uint32_t *now = b.bad + (n & 1) * 5, *next = b.bad + (~n & 1) * 5;
     const unsigned bad = __ballot_sync(0xffffffffu, mine_bad);
-    if ((threadIdx.x & 31) == 0 && bad) atomicOr(b.bad + (warp & 3), bad);
+    if ((threadIdx.x & 31) == 0) {
+        if (bad) atomicOr(const_cast<uint32_t *>(now) + (warp & 3), bad);
+        if (!fine) now[4] = 1;
+        if (warp < 4) next[warp] = 0;  // read last before this barrier, written next behind it
+    }
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    unsigned todo = *const_cast<volatile uint32_t *>(b.bad + (warp & 3));
+    const bool stop = now[4];
+    unsigned todo = now[warp & 3];
     for (; todo; todo &= todo - 1) {
         const int i = __ffs(todo) - 1;
         if ((i & 1) == (warp >> 2)) redo((warp & 3) * 32 + i);
     }
+    return !stop;
 }
 
 template <int D>
@@ -198,6 +212,35 @@ __device__ __noinline__ void redo_dq(const BwdParams &f, int row, int start, int
 }
 
 // ---------------------------------------------------------------- dK and dV
+// An item: a key tile and its kv head; its steps are (query head, query tile). Persistent
+// CTAs take items in order of falling work, a cluster that shares one out takes one.
+struct KeyItem {
+    int hk, first, seq_end, per_head, steps;
+    __device__ __forceinline__ bool get(const BwdParams &f, int n, int rank)
+    {
+        const int idx = f.split == 1 ? nth_item(n, f.dkv_items) : n ? -1 : blockIdx.x / f.split;
+        if (idx < 0) return false;
+        const AttnTile t = attn_tile(f.tiles, idx / f.p.Hkv, kTileRows, f.p.B, f.p.T);
+        if (t.first >= t.seq_end) return false;  // the list's unused end
+        hk = idx % f.p.Hkv;
+        seq_end = t.seq_end;
+        // the list begins with a sequence's last tile; here the first one has most work
+        const int count = (t.seq_end - t.seq_start + kTileRows - 1) / kTileRows;
+        const int tile = count - 1 - (t.first - t.seq_start) / kTileRows;
+        first = t.seq_start + tile * kTileRows;
+        const int G = f.p.Hq / f.p.Hkv, heads = (G - rank + f.split - 1) / f.split;
+        per_head = count - tile;
+        steps = per_head * heads;
+        return true;
+    }
+    // query head and first token of a step; the heads of a cluster's CTAs: rank, rank + split, ...
+    __device__ __forceinline__ int head(const BwdParams &f, int it, int rank) const
+    {
+        return hk * (f.p.Hq / f.p.Hkv) + rank + it / per_head * f.split;
+    }
+    __device__ __forceinline__ int token(int it) const { return first + it % per_head * kTileRows; }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_constant__ BwdParams f)
 {
@@ -207,17 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const Bars b(sm + S::kBars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = f.split > 1 ? cluster_rank() : 0, unit = blockIdx.x / f.split;
-    const int hk = unit % f.p.Hkv, G = f.p.Hq / f.p.Hkv;
-    AttnTile t = attn_tile(f.tiles, unit / f.p.Hkv, kTileRows, f.p.B, f.p.T);
-    if (t.first >= t.seq_end) return;  // all of a cluster
+    const int rank = f.split > 1 ? cluster_rank() : 0;
     if (!f.tiles && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
-    // the list begins with a sequence's last tile; here the first one has most work
-    const int count = (t.seq_end - t.seq_start + kTileRows - 1) / kTileRows;
-    const int tile = count - 1 - (t.first - t.seq_start) / kTileRows;
-    t.first = t.seq_start + tile * kTileRows;
-    const int heads = (G - rank + f.split - 1) / f.split;     // this CTA's: rank, rank + split, ...
-    const int per_head = count - tile, steps = per_head * heads;  // step = (head, query tile)
+    KeyItem t;
+    if (f.split > 1 && !t.get(f, 0, rank)) return;  // all of a cluster
 
     const uint32_t tmem = start_cta(b, 1 + 32, 1);
     constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 256 + D;
@@ -226,38 +262,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     if (warp >= 8) {
         tc::fewer_registers<kRegsOther>();
         if (warp == 9 && !f.starve) {
-            if (lane == 0) {
-                tc::mbar_arrive_expect_tx(b.stay, 2 * S::kTile);
-                tc::load_tile<D>(sm + S::kStay, &f.k, hk, t.first, b.stay);
-                tc::load_tile<D>(sm + S::kStay + S::kTile, &f.v, hk, t.first, b.stay);
-            }
-            int it = 0;
-            for (; it < steps; ++it) {
-                const int st = it % S::kStages, use = it / S::kStages;
-                const int h = hk * G + rank + it / per_head * f.split, token = t.first + it % per_head * kTileRows;
-                bool go = !use || (tc::mbar_wait(b.free0 + st, (use - 1) & 1, b.abort, f.status, kErrFree, f.spin) &&
-                                   tc::mbar_wait(b.free1 + st, (use - 1) & 1, b.abort, f.status, kErrFree, f.spin));
-                if (!__all_sync(0xffffffffu, go)) break;
-                float *to = reinterpret_cast<float *>(sm + S::kStats) + st * 256;
-                const size_t base = (size_t)h * f.p.tokens;
-#pragma unroll
-                for (int i = lane; i < kTileRows; i += 32) {
-                    const size_t at = base + min(token + i, (int)f.p.tokens - 1);
-                    tc::cp_async4(to + i, f.lse2 + at);
-                    tc::cp_async4(to + 128 + i, f.delta + at);
-                }
-                tc::cp_async_arrive(b.full0 + st);
+            int g = 0, n = 0;  // stages filled, items begun
+            bool go = true;
+            for (; go && t.get(f, n, rank); ++n) {
+                if (n && !__all_sync(0xffffffffu, tc::mbar_wait(b.stay_free, (n - 1) & 1, b.abort, f.status, kErrFree, f.spin)))
+                    break;
                 if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(b.full0 + st, S::kTile);
-                    tc::load_tile<D>(sm + S::kRing0 + st * S::kTile, &f.q, h, token, b.full0 + st);
-                    tc::mbar_arrive_expect_tx(b.full1 + st, S::kTile);
-                    tc::load_tile<D>(sm + S::kRing1 + st * S::kTile, &f.dO, h, token, b.full1 + st);
+                    tc::mbar_arrive_expect_tx(b.stay, 2 * S::kTile);
+                    tc::load_tile<D>(sm + S::kStay, &f.k, t.hk, t.first, b.stay);
+                    tc::load_tile<D>(sm + S::kStay + S::kTile, &f.v, t.hk, t.first, b.stay);
                 }
-                __syncwarp();
+                for (int it = 0; it < t.steps; ++it, ++g) {
+                    const int st = g % S::kStages, use = g / S::kStages;
+                    const int h = t.head(f, it, rank), token = t.token(it);
+                    go = !use || tc::wait_both(b.free0 + st, use - 1, b.free1 + st, use - 1, b.abort, f.status, kErrFree, f.spin);
+                    if (!go) break;
+                    float *to = reinterpret_cast<float *>(sm + S::kStats) + st * 256;
+                    const size_t base = (size_t)h * f.p.tokens;
+#pragma unroll
+                    for (int i = lane; i < kTileRows; i += 32) {
+                        const size_t at = base + min(token + i, (int)f.p.tokens - 1);
+                        tc::cp_async4(to + i, f.lse2 + at);
+                        tc::cp_async4(to + 128 + i, f.delta + at);
+                    }
+                    tc::cp_async_arrive(b.full0 + st);
+                    if (lane == 0) {
+                        tc::mbar_arrive_expect_tx(b.full0 + st, S::kTile);
+                        tc::load_tile<D>(sm + S::kRing0 + st * S::kTile, &f.q, h, token, b.full0 + st);
+                        tc::mbar_arrive_expect_tx(b.full1 + st, S::kTile);
+                        tc::load_tile<D>(sm + S::kRing1 + st * S::kTile, &f.dO, h, token, b.full1 + st);
+                    }
+                    __syncwarp();
+                }
             }
             if (lane == 0) {  // whatever the other warps do, the copies land before the memory is let go
-                tc::mbar_drain(b.stay, 0, f.status, kErrBwdDrain);
-                for (int i = max(0, it - S::kStages); i < it; ++i) {
+                if (n) tc::mbar_drain(b.stay, (n - 1) & 1, f.status, kErrBwdDrain);
+                for (int i = max(0, g - S::kStages); i < g; ++i) {
                     tc::mbar_drain(b.full0 + i % S::kStages, (i / S::kStages) & 1, f.status, kErrBwdDrain);
                     tc::mbar_drain(b.full1 + i % S::kStages, (i / S::kStages) & 1, f.status, kErrBwdDrain);
                 }
@@ -273,40 +313,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
             auto wait = [&](uint64_t *x, int nx, uint64_t *y, int ny, int code) {
                 return tc::wait_both(x, nx, y, ny, b.abort, f.status, code, f.spin);
             };
-            bool go = wait(b.stay, 0, b.full0, 0, kErrStay);
-            if (go) {
-                tc::mma_rows_rows<D>(tmem + kS, k, q, lead);
+            int g = 0;  // steps of all items
+            bool go = true;
+            for (int n = 0; go && t.get(f, n, rank); ++n) {
+                const int end = g + t.steps;
+                const int st0 = g % S::kStages, use0 = g / S::kStages;
+                go = wait(b.stay, n, b.full0 + st0, use0, kErrStay);
+                if (!go) break;
+                tc::mma_rows_rows<D>(tmem + kS, k, q + st0 * S::kTile, lead);
                 tc::commit(b.s_full, lead);
-                go = wait(b.stay, 0, b.full1, 0, kErrB);
-            }
-            if (go) {
-                tc::mma_rows_rows<D>(tmem + kDp, v, dO, lead);
+                go = wait(b.full1 + st0, use0, b.full1 + st0, use0, kErrB);
+                if (!go) break;
+                tc::mma_rows_rows<D>(tmem + kDp, v, dO + st0 * S::kTile, lead);
                 tc::commit(b.dp_full, lead);
-            }
-            for (int it = 0; it < steps && go; ++it) {
-                const int st = it % S::kStages;
-                const int next = min(it + 1, steps - 1), nst = next % S::kStages, use = next / S::kStages;
-                go = wait(b.p_full, it, b.full0 + nst, use, kErrP);
-                if (!go) break;
-                tc::tc_fence_after_sync();
-                tc::mma_weights_rows<D, 64>(tmem + kDv, tmem + kS, dO + st * S::kTile, it > 0, lead);
-                if (next > it) {
-                    tc::mma_rows_rows<D>(tmem + kS, k, q + nst * S::kTile, lead);
-                    tc::commit(b.s_full, lead);
+                if (t.steps == 1) tc::commit(b.stay_free, lead);
+                for (bool first = true; g < end; ++g, first = false) {
+                    const int st = g % S::kStages, nst = (g + 1) % S::kStages, use = (g + 1) / S::kStages;
+                    const bool more = g + 1 < end;
+                    go = more ? wait(b.p_full, g, b.full0 + nst, use, kErrP) : wait(b.p_full, g, b.p_full, g, kErrP);
+                    if (!go) break;
+                    tc::tc_fence_after_sync();
+                    tc::mma_weights_rows<D, 64>(tmem + kDv, tmem + kS, dO + st * S::kTile, !first, lead);
+                    if (more) {
+                        tc::mma_rows_rows<D>(tmem + kS, k, q + nst * S::kTile, lead);
+                        tc::commit(b.s_full, lead);
+                    }
+                    tc::commit(b.free1 + st, lead);
+                    go = more ? wait(b.ds_full, g, b.full1 + nst, use, kErrDs) : wait(b.ds_full, g, b.ds_full, g, kErrDs);
+                    if (!go) break;
+                    tc::tc_fence_after_sync();
+                    tc::mma_weights_rows<D, 64>(tmem + kDk, tmem + kDp, q + st * S::kTile, !first, lead);
+                    if (more) {
+                        tc::mma_rows_rows<D>(tmem + kDp, v, dO + nst * S::kTile, lead);
+                        tc::commit(b.dp_full, lead);
+                        if (g + 2 == end) tc::commit(b.stay_free, lead);
+                    }
+                    tc::commit(b.free0 + st, lead);
                 }
-                tc::commit(b.free1 + st, lead);
-                go = wait(b.ds_full, it, b.full1 + nst, use, kErrDs);
-                if (!go) break;
-                tc::tc_fence_after_sync();
-                tc::mma_weights_rows<D, 64>(tmem + kDk, tmem + kDp, q + st * S::kTile, it > 0, lead);
-                if (next > it) {
-                    tc::mma_rows_rows<D>(tmem + kDp, v, dO + nst * S::kTile, lead);
-                    tc::commit(b.dp_full, lead);
-                }
-                tc::commit(b.free0 + st, lead);
+                if (go) tc::commit(b.acc, lead);
             }
-            tc::commit(b.acc, lead);
-            tc::mbar_drain(b.acc, 0, f.status, kErrBwdDrain);
+            tc::commit(b.done, lead);
+            tc::mbar_drain(b.done, 0, f.status, kErrBwdDrain);
         }
     } else {
         tc::more_registers<kRegsCompute>();
@@ -316,12 +363,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         const float c = f.p.scale * kLog2e;
         const tc::f32x2 c2 = tc::pack2(c, c);
         bool go = true;
-        for (int it = 0; it < steps; ++it) {
-            const int st = it % S::kStages, i0 = it % per_head;
+        int g = 0;  // steps of all items
+        for (int n = 0; t.get(f, n, rank); ++n) {
+        for (int it = 0; it < t.steps && go; ++it, ++g) {
+            const int st = g % S::kStages, i0 = it % t.per_head;
             const float *lse2 = stats + st * 256 + half * 64, *del = lse2 + 128;
             go = __all_sync(0xffffffffu,
-                            tc::mbar_wait(b.s_full, it & 1, b.abort, f.status, kErrS, f.spin) &&
-                            tc::mbar_wait(b.full0 + st, (it / S::kStages) & 1, b.abort, f.status, kErrA, f.spin));
+                            tc::mbar_wait(b.s_full, g & 1, b.abort, f.status, kErrS, f.spin) &&
+                            tc::mbar_wait(b.full0 + st, (g / S::kStages) & 1, b.abort, f.status, kErrA, f.spin));
             if (!go) break;
             tc::tc_fence_after_sync();
             float x[64];
@@ -346,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
             }
             store_weights(ts, x);
             weights_done(b.p_full);
-            go = __all_sync(0xffffffffu, tc::mbar_wait(b.dp_full, it & 1, b.abort, f.status, kErrDp, f.spin));
+            go = __all_sync(0xffffffffu, tc::mbar_wait(b.dp_full, g & 1, b.abort, f.status, kErrDp, f.spin));
             if (!go) break;
             tc::tc_fence_after_sync();
             float y[64];
@@ -366,14 +415,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
             store_weights(td, x);
             weights_done(b.ds_full);
         }
-        go = __all_sync(0xffffffffu, go && tc::mbar_wait(b.acc, 0, b.abort, f.status, kErrAcc, f.spin));
+        go = __all_sync(0xffffffffu, go && tc::mbar_wait(b.acc, n & 1, b.abort, f.status, kErrAcc, f.spin));
         const int col = t.first + in_tile;
         const bool mine = col < t.seq_end;
-        bool bad = false, fine = go && !*b.abort;
+        const bool fine = __all_sync(0xffffffffu, go && !*b.abort);
+        bool bad = false;
         // the first four warps write dV, the others dK
         const uint32_t sums = tmem + lanes + (half ? kDk : kDv);
         const float by = half ? f.p.scale : 1.f;
-        __nv_bfloat16 *out = (half ? f.gk : f.gv) + ((size_t)col * f.p.Hkv + hk) * D;
+        __nv_bfloat16 *out = (half ? f.gk : f.gv) + ((size_t)col * f.p.Hkv + t.hk) * D;
         if (fine) tc::tc_fence_after_sync();
         if (f.split == 1) {
             if (fine) bad = !store_sums<D>(sums, by, mine ? out : nullptr) && mine;
@@ -412,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
             bad = mine && fine && !(odd == 0.f);
             cluster_sync();  // all reads and stores are made
         }
-        redo_rows(b, bad, [&](int i) { redo_dkv<D>(f, t.first + i, t.seq_end, hk); });
+        if (!redo_rows(b, n, fine, bad, [&](int i) { redo_dkv<D>(f, t.first + i, t.seq_end, t.hk); })) break;
+        }
     }
     if (warp >= 8 && f.split > 1) {
         __syncwarp();
@@ -423,6 +474,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------- dQ
+// An item: a query tile and its head; its steps are the key tiles, the diagonal's first.
+struct QueryItem {
+    int h, first, seq_start, seq_end, last, steps;
+    __device__ __forceinline__ bool get(const BwdParams &f, int n)
+    {
+        const int idx = nth_item(n, f.dq_items);
+        if (idx < 0) return false;
+        const AttnTile t = attn_tile(f.tiles, idx / f.p.Hq, kTileRows, f.p.B, f.p.T);
+        if (t.first >= t.seq_end) return false;  // the list's unused end
+        h = idx % f.p.Hq;
+        first = t.first; seq_start = t.seq_start; seq_end = t.seq_end;
+        last = (first - seq_start) / kTileRows;
+        steps = last + 1;
+        return true;
+    }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_constant__ BwdParams f)
 {
@@ -432,10 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const Bars b(sm + S::kBars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x % f.p.Hq;
-    const AttnTile t = attn_tile(f.tiles, blockIdx.x / f.p.Hq, kTileRows, f.p.B, f.p.T);
-    if (t.first >= t.seq_end) return;
-    const int last = (t.first - t.seq_start) / kTileRows, steps = last + 1;  // key tiles, diagonal first
+    QueryItem t;
 
     const uint32_t tmem = start_cta(b, 1, 2);
     constexpr uint32_t kS = 0, kDp = 256, kDq = 384;  // two score tiles in turn
@@ -443,29 +508,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     if (warp >= 8) {
         tc::fewer_registers<kRegsOther>();
         if (warp == 9 && lane == 0 && !f.starve) {
-            const int hk = h / (f.p.Hq / f.p.Hkv);
-            tc::mbar_arrive_expect_tx(b.stay, 2 * S::kTile);
-            tc::load_tile<D>(sm + S::kStay, &f.q, h, t.first, b.stay);
-            tc::load_tile<D>(sm + S::kStay + S::kTile, &f.dO, h, t.first, b.stay);
-            int it = 0;
-            for (; it < steps; ++it) {
-                const int st0 = it % S::kStages0, use0 = it / S::kStages0;
-                const int st = it % S::kStages, use = it / S::kStages;
-                const int token = t.seq_start + (last - it) * kTileRows;
-                if (use0 && !tc::mbar_wait(b.free0 + st0, (use0 - 1) & 1, b.abort, f.status, kErrFree, f.spin)) break;
-                tc::mbar_arrive_expect_tx(b.full0 + st0, S::kTile);
-                tc::load_tile<D>(sm + S::kRing0 + st0 * S::kTile, &f.k, hk, token, b.full0 + st0);
-                if (use && !tc::mbar_wait(b.free1 + st, (use - 1) & 1, b.abort, f.status, kErrFree, f.spin)) {
-                    tc::mbar_drain(b.full0 + st0, use0 & 1, f.status, kErrBwdDrain);
-                    break;
+            int g0 = 0, g = 0, n = 0;  // stages filled in either ring, items begun
+            bool go = true;
+            for (; go && t.get(f, n); ++n) {
+                const int hk = t.h / (f.p.Hq / f.p.Hkv);
+                if (n && !tc::mbar_wait(b.stay_free, (n - 1) & 1, b.abort, f.status, kErrFree, f.spin)) break;
+                tc::mbar_arrive_expect_tx(b.stay, 2 * S::kTile);
+                tc::load_tile<D>(sm + S::kStay, &f.q, t.h, t.first, b.stay);
+                tc::load_tile<D>(sm + S::kStay + S::kTile, &f.dO, t.h, t.first, b.stay);
+                for (int it = 0; it < t.steps; ++it) {
+                    const int st0 = g0 % S::kStages0, use0 = g0 / S::kStages0;
+                    const int st = g % S::kStages, use = g / S::kStages;
+                    const int token = t.seq_start + (t.last - it) * kTileRows;
+                    go = !use0 || tc::mbar_wait(b.free0 + st0, (use0 - 1) & 1, b.abort, f.status, kErrFree, f.spin);
+                    if (!go) break;
+                    tc::mbar_arrive_expect_tx(b.full0 + st0, S::kTile);
+                    tc::load_tile<D>(sm + S::kRing0 + st0 * S::kTile, &f.k, hk, token, b.full0 + st0);
+                    ++g0;
+                    go = !use || tc::mbar_wait(b.free1 + st, (use - 1) & 1, b.abort, f.status, kErrFree, f.spin);
+                    if (!go) break;
+                    tc::mbar_arrive_expect_tx(b.full1 + st, S::kTile);
+                    tc::load_tile<D>(sm + S::kRing1 + st * S::kTile, &f.v, hk, token, b.full1 + st);
+                    ++g;
                 }
-                tc::mbar_arrive_expect_tx(b.full1 + st, S::kTile);
-                tc::load_tile<D>(sm + S::kRing1 + st * S::kTile, &f.v, hk, token, b.full1 + st);
             }
-            tc::mbar_drain(b.stay, 0, f.status, kErrBwdDrain);
-            for (int i = max(0, it - S::kStages0); i < it; ++i)
+            // whatever the other warps do, the copies land before the memory is let go
+            if (n) tc::mbar_drain(b.stay, (n - 1) & 1, f.status, kErrBwdDrain);
+            for (int i = max(0, g0 - S::kStages0); i < g0; ++i)
                 tc::mbar_drain(b.full0 + i % S::kStages0, (i / S::kStages0) & 1, f.status, kErrBwdDrain);
-            for (int i = max(0, it - S::kStages); i < it; ++i)
+            for (int i = max(0, g - S::kStages); i < g; ++i)
                 tc::mbar_drain(b.full1 + i % S::kStages, (i / S::kStages) & 1, f.status, kErrBwdDrain);
         }
         // warp 8 issues S, two steps ahead, warp 10 dP and dQ
@@ -473,67 +544,84 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
             const uint32_t lead = lane == 0;
             const uint32_t q = tc::smem_u32(sm + S::kStay), dO = q + S::kTile;
             const uint32_t k = tc::smem_u32(sm + S::kRing0), v = tc::smem_u32(sm + S::kRing1);
-            auto wait = [&](uint64_t *bar, int n, int code) {
-                return __all_sync(0xffffffffu, tc::mbar_wait(bar, n & 1, b.abort, f.status, code, f.spin));
+            auto wait = [&](uint64_t *x, int nx, uint64_t *y, int ny, int code) {
+                return tc::wait_both(x, nx, y, ny, b.abort, f.status, code, f.spin);
             };
-            bool go = wait(b.stay, 0, kErrStay);
-            if (warp == 8) {
-                for (int it = 0; it < steps && go; ++it) {
-                    const int st = it % S::kStages0;
-                    // before the third step only the keys are due
-                    go = tc::wait_both(b.full0 + st, it / S::kStages0, it < 2 ? b.stay : b.s_free + (it & 1),
-                                       it < 2 ? 0 : (it >> 1) - 1, b.abort, f.status, kErrA, f.spin);
-                    if (!go) break;
-                    tc::tc_fence_after_sync();
-                    tc::mma_rows_rows<D>(tmem + kS + (it & 1) * 128, q, k + st * S::kTile, lead);
-                    tc::commit(b.s_full + (it & 1), lead);
-                    tc::commit(b.free0 + st, lead);
-                }
-            } else {
-                for (int it = 0; it <= steps && go; ++it) {
-                    const int st = it % S::kStages, st0 = (it + S::kStages0 - 1) % S::kStages0;
-                    const int due = min(it, steps - 1);  // values
-                    // dS says that the step's S was formed, so that its keys are there
-                    go = tc::wait_both(b.full1 + due % S::kStages, due / S::kStages, it ? b.ds_full : b.stay,
-                                       it ? it - 1 : 0, b.abort, f.status, kErrDs, f.spin);
-                    if (!go) break;
-                    tc::tc_fence_after_sync();
-                    if (it > 0) tc::mma_weights_rows<D, 64>(tmem + kDq, tmem + kDp, k + st0 * S::kTile, it > 1, lead);
-                    if (it < steps) {
-                        tc::mma_rows_rows<D>(tmem + kDp, dO, v + st * S::kTile, lead);
-                        tc::commit(b.dp_full, lead);
-                        tc::commit(b.free1 + st, lead);
+            int g = 0;  // steps of all items
+            bool go = true;
+            for (int n = 0; go && t.get(f, n); ++n) {
+                const int begin = g, end = g + t.steps;
+                go = wait(b.stay, n, b.stay, n, kErrStay);
+                if (warp == 8) {
+                    for (; g < end && go; ++g) {
+                        uint64_t *keys = b.full0 + g % S::kStages0;
+                        const int use = g / S::kStages0;
+                        // its buffer was read (the first two steps have none to wait for)
+                        go = g < 2 ? wait(keys, use, keys, use, kErrA)
+                                   : wait(keys, use, b.s_free + (g & 1), (g >> 1) - 1, kErrA);
+                        if (!go) break;
+                        tc::tc_fence_after_sync();
+                        tc::mma_rows_rows<D>(tmem + kS + (g & 1) * 128, q, k + g % S::kStages0 * S::kTile, lead);
+                        tc::commit(b.s_full + (g & 1), lead);
+                        tc::commit(b.free0 + g % S::kStages0, lead);
+                        if (g + 1 == end) tc::commit(b.stay_free, lead);
                     }
-                    if (it > 0) tc::commit(b.free0 + st0, lead);
+                } else {
+                    for (; g <= end && go; ++g) {  // dQ of step g - 1 and dP of step g
+                        uint64_t *values = b.full1 + g % S::kStages;
+                        const int use = g / S::kStages;
+                        const bool dp = g < end, dq = g > begin;
+                        // dS says that the step's S was formed, so that its keys are there
+                        go = !dq   ? wait(values, use, values, use, kErrB)
+                             : !dp ? wait(b.ds_full, g - 1, b.ds_full, g - 1, kErrDs)
+                                   : wait(values, use, b.ds_full, g - 1, kErrDs);
+                        if (!go) break;
+                        tc::tc_fence_after_sync();
+                        const int st0 = (g + S::kStages0 - 1) % S::kStages0;
+                        if (dq) tc::mma_weights_rows<D, 64>(tmem + kDq, tmem + kDp, k + st0 * S::kTile, g - 1 > begin, lead);
+                        if (dp) {
+                            tc::mma_rows_rows<D>(tmem + kDp, dO, v + g % S::kStages * S::kTile, lead);
+                            tc::commit(b.dp_full, lead);
+                            tc::commit(b.free1 + g % S::kStages, lead);
+                            if (g + 1 == end) tc::commit(b.stay_free, lead);
+                        }
+                        if (dq) tc::commit(b.free0 + st0, lead);
+                    }
+                    g = end;  // the next item's first dP comes with no dQ
+                    if (go) tc::commit(b.acc, lead);
                 }
             }
-            tc::commit(b.acc, lead);
-            tc::mbar_drain(b.acc, 0, f.status, kErrBwdDrain);
+            tc::commit(b.done, lead);
+            tc::mbar_drain(b.done, 0, f.status, kErrBwdDrain);
         }
     } else {
         tc::more_registers<kRegsCompute>();
-        const int half = warp >> 2, in_tile = threadIdx.x & 127, row = t.first + in_tile;
-        const bool mine = row < t.seq_end;
+        const int half = warp >> 2, in_tile = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t ts = tmem + lanes + kS + half * 64, td = tmem + lanes + kDp + half * 64;
         const float c = f.p.scale * kLog2e;
-        const size_t at = (size_t)h * f.p.tokens + min(row, (int)f.p.tokens - 1);
-        const float z = f.lse2[at], del = f.delta[at];
-        const tc::f32x2 c2 = tc::pack2(c, c), z2 = tc::pack2(-z, -z), d2 = tc::pack2(-del, -del);
+        const tc::f32x2 c2 = tc::pack2(c, c);
         bool go = true;
-        for (int it = 0; it < steps; ++it) {
-            go = __all_sync(0xffffffffu, tc::mbar_wait(b.s_full + (it & 1), (it >> 1) & 1, b.abort, f.status,
+        int g = 0;  // steps of all items
+        for (int n = 0; t.get(f, n); ++n) {
+        const int row = t.first + in_tile;
+        const bool mine = row < t.seq_end;
+        const size_t at = (size_t)t.h * f.p.tokens + min(row, (int)f.p.tokens - 1);
+        const float z = f.lse2[at], del = f.delta[at];
+        const tc::f32x2 z2 = tc::pack2(-z, -z), d2 = tc::pack2(-del, -del);
+        for (int it = 0; it < t.steps && go; ++it, ++g) {
+            go = __all_sync(0xffffffffu, tc::mbar_wait(b.s_full + (g & 1), (g >> 1) & 1, b.abort, f.status,
                                                        kErrS, f.spin));
             if (!go) break;
             tc::tc_fence_after_sync();
             float x[64];
-            tc::tmem_start(ts + (it & 1) * 128, x);
-            tc::tmem_start(ts + (it & 1) * 128 + 32, x + 32);
+            tc::tmem_start(ts + (g & 1) * 128, x);
+            tc::tmem_start(ts + (g & 1) * 128 + 32, x + 32);
             tc::tmem_ready(x);
             tc::tmem_ready(x + 32);
             tc::tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(b.s_free + (it & 1));
+            if (lane == 0) tc::mbar_arrive(b.s_free + (g & 1));
 #pragma unroll
             for (int j = 0; j < 64; j += 2) {
                 tc::unpack2(tc::fma2(tc::pack2(x[j], x[j + 1]), c2, z2), x[j], x[j + 1]);
@@ -544,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
 #pragma unroll
                 for (int j = 0; j < 64; ++j) x[j] = j + half * 64 <= in_tile ? x[j] : 0.f;
             }
-            go = __all_sync(0xffffffffu, tc::mbar_wait(b.dp_full, it & 1, b.abort, f.status, kErrDp, f.spin));
+            go = __all_sync(0xffffffffu, tc::mbar_wait(b.dp_full, g & 1, b.abort, f.status, kErrDp, f.spin));
             if (!go) break;
             tc::tc_fence_after_sync();
             float y[64];
@@ -559,18 +647,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
             store_weights(td, x);
             weights_done(b.ds_full);
         }
-        go = __all_sync(0xffffffffu, go && tc::mbar_wait(b.acc, 0, b.abort, f.status, kErrAcc, f.spin));
+        go = __all_sync(0xffffffffu, go && tc::mbar_wait(b.acc, n & 1, b.abort, f.status, kErrAcc, f.spin));
+        const bool fine = __all_sync(0xffffffffu, go && !*b.abort);
         bool bad = false;
-        if (go && !*b.abort) {
+        if (fine) {
             tc::tc_fence_after_sync();
             // each half of the warps writes half of the row's channels
-            __nv_bfloat16 *out = f.gq + ((size_t)row * f.p.Hq + h) * D;
+            __nv_bfloat16 *out = f.gq + ((size_t)row * f.p.Hq + t.h) * D;
             constexpr int kPart = D == 32 ? 32 : D / 2;
             if (D > 32 || half == 0)
                 bad = !store_sums<kPart>(tmem + lanes + kDq + half * kPart, f.p.scale,
                                          mine ? out + half * kPart : nullptr) && mine;
         }
-        redo_rows(b, bad, [&](int i) { redo_dq<D>(f, t.first + i, t.seq_start, h); });
+        if (!redo_rows(b, n, fine, bad, [&](int i) { redo_dq<D>(f, t.first + i, t.seq_start, t.h); })) break;
+        }
     }
     end_cta(tmem);
 }
@@ -647,15 +737,18 @@ cudaError_t launch(const AttnProblem &p, const void *o, const float *lse, const 
     }
     e = launch_attn_delta(p, o, lse, dO, delta, delta + (size_t)p.tokens * p.Hq, st);
     if (e != cudaSuccess) return e;
-    const unsigned tiles = (unsigned)attn_tiles(p, kTileRows);
+    const long long tiles = attn_tiles(p, kTileRows);
     constexpr uint32_t dkv_smem = BwdShape<D, true>::kBytes, dq_smem = BwdShape<D, false>::kBytes;
     f.split = attn_head_split(p, kTileRows, 148);
-    e = launch_clusters(attn_dkv_kernel<D>, f, (long long)tiles * p.Hkv, kThreads, dkv_smem, f.split, st);
+    f.dkv_items = (int)(tiles * p.Hkv);
+    f.dq_items = (int)(tiles * p.Hq);
+    e = launch_clusters(attn_dkv_kernel<D>, f, f.split > 1 ? f.dkv_items : std::min(f.dkv_items, 148), kThreads,
+                        dkv_smem, f.split, st);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(attn_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              dq_smem);
     if (e != cudaSuccess) return e;
-    attn_dq_kernel<D><<<tiles * p.Hq, kThreads, dq_smem, st>>>(f);
+    attn_dq_kernel<D><<<std::min(f.dq_items, 148), kThreads, dq_smem, st>>>(f);
     note_launch();
     return cudaGetLastError();
 }

@@ -1,11 +1,13 @@
 // kda_attn_plan.cu — the tile list of the prompt-attention kernels.
 //
 // cu_seqlens lives in device memory, so it is sanitised here as the prefill's plan
-// does it: offsets clamped to [0, tokens] and made non-decreasing. Sequences are
-// ranked by decreasing length (up to kRankMax of them, the ranking is quadratic;
-// beyond that they keep their order) and their tiles listed last tile first: a
-// tile's work grows with its place in the sequence, so the CTAs that start last
-// are short ones.
+// does it: offsets clamped to [0, tokens] and made non-decreasing.
+//
+// A tile's work grows with its place in its sequence, and persistent CTAs take the list's
+// entries in turn: so it is sorted by falling place. Sequences are ranked by decreasing
+// length first; those that have a tile at place t are then the first ones, and an entry's
+// position is the number of tiles at later places plus its sequence's rank. The ranking
+// is quadratic: beyond kRankMax sequences they keep their order, last tile first in each.
 #include "kda_attn.cuh"
 
 namespace kda {
@@ -48,7 +50,7 @@ attn_plan_kernel(const int32_t *__restrict__ cu, int N, int T, int tokens, int r
 {
     __shared__ int s_warp[32];
     __shared__ int s_carry;
-    __shared__ int s_len[kRankMax];
+    __shared__ int s_len[kRankMax], s_tiles[kRankMax];
     const int tid = threadIdx.x;
     if (tid == 0) *status = 0;
     // sanitised starts
@@ -63,8 +65,8 @@ attn_plan_kernel(const int32_t *__restrict__ cu, int N, int T, int tokens, int r
         if (tid == kThreads - 1) s_carry = x;
         __syncthreads();
     }
-    // longest first, ties by index
     if (N <= kRankMax) {
+        // longest first, ties by index
         for (int n = tid; n < N; n += kThreads) s_len[n] = starts[n + 1] - starts[n];
         __syncthreads();
         for (int n = tid; n < N; n += kThreads) {
@@ -72,10 +74,34 @@ attn_plan_kernel(const int32_t *__restrict__ cu, int N, int T, int tokens, int r
             int rank = 0;
             for (int m = 0; m < N; ++m) rank += s_len[m] > ln || (s_len[m] == ln && m < n);
             order[rank] = n;
+            s_tiles[rank] = (ln + rows - 1) / rows;
         }
-    } else {
-        for (int n = tid; n < N; n += kThreads) order[n] = n;
+        __syncthreads();
+        const int lane = tid & 31;
+        if (tid == 0) s_carry = 0;
+        __syncthreads();
+        for (int t = tid >> 5; t < s_tiles[0]; t += kThreads / 32) {
+            int later = 0, here = 0;
+            for (int r = lane; r < N && s_tiles[r] > t; r += 32) {
+                later += s_tiles[r] - t - 1;
+                ++here;
+            }
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) {
+                later += __shfl_xor_sync(0xffffffffu, later, d);
+                here += __shfl_xor_sync(0xffffffffu, here, d);
+            }
+            for (int r = lane; r < here; r += 32) {
+                const int n = order[r], a = starts[n];
+                tiles[later + r] = AttnTile{a + t * rows, a, starts[n + 1], 0};
+            }
+            if (lane == 0) atomicAdd(&s_carry, here);
+        }
+        __syncthreads();
+        for (int t = s_carry + tid; t < max_tiles; t += kThreads) tiles[t] = AttnTile{0, 0, 0, 0};
+        return;
     }
+    for (int n = tid; n < N; n += kThreads) order[n] = n;
     __syncthreads();
     // first tile of each rank
     if (tid == 0) s_carry = 0;
