@@ -91,31 +91,47 @@ inline int attn_head_split(const AttnProblem &p, int rows, int enough)
     return split;
 }
 
-// A launch as clusters of `split` CTAs (1: none).
+// A launch as clusters of `split` CTAs (1: none). `early`: its CTAs may start while those of
+// the kernel before it, which allows it, still run; it waits for that kernel's end itself.
 template <typename K, typename P>
-cudaError_t launch_clusters(K kernel, const P &params, long long ctas, int threads, size_t smem,
-                            int split, cudaStream_t st)
+cudaError_t launch_kernel(K kernel, const P &params, long long ctas, int threads, size_t smem,
+                          int split, bool early, cudaStream_t st)
 {
+    if (ctas * split > INT32_MAX) return cudaErrorInvalidValue;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(
             kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)split;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2] = {};
+    int attrs = 0;
+    if (split > 1) {
+        attr[attrs].id = cudaLaunchAttributeClusterDimension;
+        attr[attrs].val.clusterDim.x = (unsigned)split;
+        attr[attrs].val.clusterDim.y = attr[attrs].val.clusterDim.z = 1;
+        ++attrs;
+    }
+    if (early) {
+        attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[attrs].val.programmaticStreamSerializationAllowed = 1;
+        ++attrs;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(ctas * split));
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = split > 1 ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = (unsigned)attrs;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, params);
     note_launch();
     return e;
 }
+
+// The kernel launched early behind this one may start; this kernel waits for the end of
+// the one before it and sees what that wrote.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ int cluster_rank()
 {

@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = f.split > 1 ? cluster_rank() : 0;
     if (!f.tiles && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
+    let_next_start();
     KeyItem t;
     if (f.split > 1 && !t.get(f, 0, rank)) return;  // all of a cluster
 
@@ -475,6 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
 
 // ---------------------------------------------------------------- dQ
 // An item: a query tile and its head; its steps are the key tiles, the diagonal's first.
+// Launched early behind dK and dV, of which it needs nothing: its CTAs, two for each SM
+// to fill in where there is room, start as the SMs run out of key tiles, and only must
+// not end before those do.
 struct QueryItem {
     int h, first, seq_start, seq_end, last, steps;
     __device__ __forceinline__ bool get(const BwdParams &f, int n)
@@ -662,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         if (!redo_rows(b, n, fine, bad, [&](int i) { redo_dq<D>(f, t.first + i, t.seq_start, t.h); })) break;
         }
     }
+    wait_for_previous();
     end_cta(tmem);
 }
 
@@ -742,15 +747,10 @@ cudaError_t launch(const AttnProblem &p, const void *o, const float *lse, const 
     f.split = attn_head_split(p, kTileRows, 148);
     f.dkv_items = (int)(tiles * p.Hkv);
     f.dq_items = (int)(tiles * p.Hq);
-    e = launch_clusters(attn_dkv_kernel<D>, f, f.split > 1 ? f.dkv_items : std::min(f.dkv_items, 148), kThreads,
-                        dkv_smem, f.split, st);
+    e = launch_kernel(attn_dkv_kernel<D>, f, f.split > 1 ? f.dkv_items : std::min(f.dkv_items, 148), kThreads,
+                      dkv_smem, f.split, false, st);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(attn_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             dq_smem);
-    if (e != cudaSuccess) return e;
-    attn_dq_kernel<D><<<std::min(f.dq_items, 148), kThreads, dq_smem, st>>>(f);
-    note_launch();
-    return cudaGetLastError();
+    return launch_kernel(attn_dq_kernel<D>, f, std::min(f.dq_items, 148 * 2), kThreads, dq_smem, 1, true, st);
 }
 
 }  // namespace

@@ -295,6 +295,8 @@ __device__ __forceinline__ void load_stats(const F32Params &f, float *lse2, floa
 }
 
 // ---------------------------------------------------------------- dQ
+// Launched early behind dK and dV, of which it needs nothing: it fills the SMs that have
+// run out of them, and only must not end before they do.
 template <int D>
 __global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ F32Params f)
 {
@@ -338,6 +340,7 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ F3
     store_rows<D>(acc, by, f.gq + ((size_t)t.first * f.p.Hq + h) * D, (size_t)f.p.Hq * D,
                   t.seq_end - t.first, &bad);
     redo_rows(&bad, [&](int r) { redo_dq<D>(f, t.first + r, t.seq_start, h); });
+    wait_for_previous();
 }
 
 // ---------------------------------------------------------------- dK and dV
@@ -350,6 +353,7 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ F
     __shared__ unsigned bad;
     float *k = smem, *v = k + kRows * D, *q = v + kRows * D, *g = q + kWalk * D, *w = g + kWalk * D;
     const int rank = f.split > 1 ? cluster_rank() : 0, unit = blockIdx.x / f.split;
+    let_next_start();
     AttnTile t = tile_of(f, unit / f.p.Hkv);
     if (t.first >= t.seq_end) return;  // all of a cluster
     if (!f.tiles && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
@@ -447,8 +451,8 @@ cudaError_t fwd(const AttnProblem &p, void *o, float *lse, void *workspace, cuda
     f.lse_out = lse;
     const cudaError_t e = prepare(p, false, workspace, f, st);
     if (e != cudaSuccess) return e;
-    return launch_clusters(fwd_kernel<D>, f, attn_tiles(p, kRows) * p.Hq, kThreads,
-                           ((kRows + 2 * kWalk) * D + kRows * kW) * 4, 1, st);
+    return launch_kernel(fwd_kernel<D>, f, attn_tiles(p, kRows) * p.Hq, kThreads,
+                         ((kRows + 2 * kWalk) * D + kRows * kW) * 4, 1, false, st);
 }
 
 template <int D>
@@ -470,8 +474,8 @@ cudaError_t bwd(const AttnProblem &p, const void *o, const float *lse, const voi
     const long long tiles = attn_tiles(p, kRows);
     const size_t smem = (2 * (kRows + kWalk) * D + kRows * kW) * 4;
     f.split = attn_head_split(p, kRows, 148 * 4);
-    if (e == cudaSuccess) e = launch_clusters(dkv_kernel<D>, f, tiles * p.Hkv, kThreads, smem, f.split, st);
-    if (e == cudaSuccess) e = launch_clusters(dq_kernel<D>, f, tiles * p.Hq, kThreads, smem, 1, st);
+    if (e == cudaSuccess) e = launch_kernel(dkv_kernel<D>, f, tiles * p.Hkv, kThreads, smem, f.split, false, st);
+    if (e == cudaSuccess) e = launch_kernel(dq_kernel<D>, f, tiles * p.Hq, kThreads, smem, 1, true, st);
     return e;
 }
 
