@@ -51,7 +51,7 @@ def _lib():
 @functools.lru_cache(maxsize=4096)
 def _size(fn, *args):
     """Workspace bytes: a function of the sizes alone."""
-    return max(int(getattr(_lib(), fn)(*args)), 16)
+    return max(int(_function(fn)(*args)), 16)
 
 
 def _dt(t):
@@ -91,9 +91,14 @@ def _on(device, stream):
     return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
+@functools.lru_cache(maxsize=None)
+def _function(fn):
+    return getattr(_lib(), fn)
+
+
 def _call(fn, device, *args):
     """C call ``fn`` on the device's current stream."""
-    st = getattr(_lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    st = _function(fn)(*args, torch._C._cuda_getCurrentRawStream(device.index))
     if st != 0:
         raise KdaError(fn, st)
 
@@ -109,10 +114,11 @@ def _bytes(t):
     return t.numel() * t.element_size()
 
 
-def _out(t, name, shape, dtype, device):
+def _out(t, name, like, dtype, shape):
+    """The caller's output tensor, checked, or a new one on the device of ``like``."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check(t, name, dtype, shape, device)
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
+    _check(t, name, dtype, shape, like.device)
     return t
 
 
@@ -145,8 +151,8 @@ def kda_attn_fwd(q, k, v, cu_seqlens=None, scale=None, o=None, lse=None, workspa
     sizes, n, dt, scale = _prompt(q, k, v, cu_seqlens, scale)
     dev = q.device
     with _on(dev, stream):
-        o = _out(o, "o", q.shape, q.dtype, dev)
-        lse = _out(lse, "lse", q.shape[:3], torch.float32, dev)
+        o = _out(o, "o", q, q.dtype, q.shape)
+        lse = _out(lse, "lse", q, torch.float32, q.shape[:3])
         ws = _ws(workspace, _size("kda_attn_fwd_workspace_size", *sizes, n, dt), dev)
         _call("kda_attn_fwd", dev, _p(q), _p(k), _p(v), dt, _p(cu_seqlens), n, *sizes, scale,
               _p(o), _p(lse), _p(ws), _bytes(ws))
@@ -227,8 +233,8 @@ def kda_attn_tree(q, k_pages, v_pages, block_table, ctx_lens, parents=None, scal
         _ints(parents, "parents", (N, R), dev)
     scale = d ** -0.5 if scale is None else float(scale)
     with _on(dev, stream):
-        o = _out(o, "o", q.shape, q.dtype, dev)
-        lse = _out(lse, "lse", q.shape[:3], torch.float32, dev)
+        o = _out(o, "o", q, q.dtype, q.shape)
+        lse = _out(lse, "lse", q, torch.float32, q.shape[:3])
         ws = _ws(workspace, _size("kda_attn_tree_workspace_size", N, R, Hq, Hkv, d, M, page, dt),
                  dev)
         _call("kda_attn_tree", dev, _p(q), _p(k_pages), _p(v_pages), dt, _p(block_table),
@@ -248,8 +254,7 @@ def kda_cache_fork(refs, block_table, lens, parents, stream=None):
     _ints(lens, "lens", (N,), dev)
     _ints(parents, "parents", (n_out,), dev)
     with _on(dev, stream):
-        table = torch.empty((n_out, M), dtype=torch.int32, device=dev)
-        out = torch.empty(n_out, dtype=torch.int32, device=dev)
+        table, out = lens.new_empty((n_out, M)), lens.new_empty(n_out)
         _call("kda_cache_fork", dev, _p(refs), _p(block_table), _p(lens), _p(parents), N, n_out,
               M, refs.numel(), _p(table), _p(out))
     return table, out
@@ -267,8 +272,7 @@ def kda_cache_reserve(refs, block_table, lens, add, page_size, workspace=None, s
     _ints(lens, "lens", (N,), dev)
     _ints(add, "add", (N,), dev)
     with _on(dev, stream):
-        copies = torch.empty((N, 2), dtype=torch.int32, device=dev)
-        status = torch.empty(1, dtype=torch.int32, device=dev)
+        copies, status = lens.new_empty((N, 2)), lens.new_empty(1)
         ws = _ws(workspace, _size("kda_cache_reserve_workspace_size", N, M, P), dev)
         _call("kda_cache_reserve", dev, _p(refs), _p(block_table), _p(lens), _p(add), N, M, P,
               int(page_size), _p(copies), _p(status), _p(ws), _bytes(ws))
@@ -323,7 +327,7 @@ def kda_cache_compact(k_pages, v_pages, block_table, ctx_lens, path, stream=None
     _ints(path, "path", (N, R), dev)
     _ints(ctx_lens, "ctx_lens", (N,), dev)
     with _on(dev, stream):
-        out = torch.empty(N, dtype=torch.int32, device=dev)
+        out = path.new_empty(N)
         _call("kda_cache_compact", dev, _p(k_pages), _p(v_pages), dt, _p(block_table),
               _p(ctx_lens), _p(path), N, R, Hkv, d, P, M, page, _p(out))
     return out
