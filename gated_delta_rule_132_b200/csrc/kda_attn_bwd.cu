@@ -13,8 +13,8 @@
 // where the gradient products read them as their TMEM operand. scale is applied to
 // the finished sums.
 //
-// Rows whose result is not finite are computed again from the visible pairs alone, as
-// in the forward (0 times what a masked place holds may be NaN).
+// Rows whose result is not finite are computed again from the visible pairs alone, at the
+// CTA's end, as in the forward (0 times what a masked place holds may be NaN).
 #include <algorithm>
 
 #include "kda_attn_rows.cuh"
@@ -64,7 +64,7 @@ struct Bars {
     uint64_t *stay, *stay_free, *done, *full0, *free0, *full1, *free1, *s_full, *s_free, *dp_full, *p_full, *ds_full, *acc;
     uint32_t *tmem_slot;
     volatile int *abort;
-    uint32_t *bad;  // [2][5] rows to compute again, and whether to give up; of items in turn
+    volatile uint32_t *odd_rows;  // whether a row is not finite
     __device__ Bars(uint8_t *at)
     {
         constexpr int kMost = 4;  // stages
@@ -76,7 +76,7 @@ struct Bars {
         ds_full = p_full + 1; acc = ds_full + 1;
         tmem_slot = reinterpret_cast<uint32_t *>(acc + 1);
         abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-        bad = tmem_slot + 2;
+        odd_rows = tmem_slot + 2;
     }
 };
 
@@ -105,7 +105,7 @@ __device__ __forceinline__ uint32_t start_cta(const Bars &b, int full0_count, in
         tc::mbar_init(b.ds_full, 8);
         tc::mbar_init(b.acc, 1);
         *b.abort = 0;
-        for (int i = 0; i < 10; ++i) b.bad[i] = 0;
+        *b.odd_rows = 0;
         tc::fence_mbar_init();
     }
     tc::tc_fence_before_sync();
@@ -175,28 +175,13 @@ __device__ __forceinline__ bool store_sums(uint32_t taddr, float by, __nv_bfloat
     return odd == 0.f;
 }
 
-// The rows of the n-th item that a thread of their own flagged, one warp each, after all
-// stores. All eight warps come here for every item; returns, to all of them alike,
-// whether none has given up.
-template <typename F>
-__device__ __forceinline__ bool redo_rows(const Bars &b, int n, bool fine, bool mine_bad, F redo)
+// Behind all items: whether any of the CTA's eight warps had a row that is not finite, and
+// none has given up.
+__device__ __forceinline__ bool any_odd_rows(const Bars &b, bool odd)
 {
-    const int warp = threadIdx.x >> 5;  // 0..7, two warps per 32 rows
-    volatile uint32_t *now = b.bad + (n & 1) * 5, *next = b.bad + (~n & 1) * 5;
-    const unsigned bad = __ballot_sync(0xffffffffu, mine_bad);
-    if ((threadIdx.x & 31) == 0) {
-        if (bad) atomicOr(const_cast<uint32_t *>(now) + (warp & 3), bad);
-        if (!fine) now[4] = 1;
-        if (warp < 4) next[warp] = 0;  // read last before this barrier, written next behind it
-    }
+    if (odd) *b.odd_rows = 1;
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    const bool stop = now[4];
-    unsigned todo = now[warp & 3];
-    for (; todo; todo &= todo - 1) {
-        const int i = __ffs(todo) - 1;
-        if ((i & 1) == (warp >> 2)) redo((warp & 3) * 32 + i);
-    }
-    return !stop;
+    return *b.odd_rows && !*b.abort;
 }
 
 template <int D>
@@ -363,108 +348,116 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         const uint32_t ts = tmem + lanes + kS + half * 64, td = tmem + lanes + kDp + half * 64;
         const float c = f.p.scale * kLog2e;
         const tc::f32x2 c2 = tc::pack2(c, c);
-        bool go = true;
+        bool go = true, odd_rows = false;
         int g = 0;  // steps of all items
         for (int n = 0; t.get(f, n, rank); ++n) {
-        for (int it = 0; it < t.steps && go; ++it, ++g) {
-            const int st = g % S::kStages, i0 = it % t.per_head;
-            const float *lse2 = stats + st * 256 + half * 64, *del = lse2 + 128;
-            go = __all_sync(0xffffffffu,
-                            tc::mbar_wait(b.s_full, g & 1, b.abort, f.status, kErrS, f.spin) &&
-                            tc::mbar_wait(b.full0 + st, (g / S::kStages) & 1, b.abort, f.status, kErrA, f.spin));
-            if (!go) break;
-            tc::tc_fence_after_sync();
-            float x[64];
-            tc::tmem_start(ts, x);
-            tc::tmem_start(ts + 32, x + 32);
-            tc::tmem_ready(x);
-            tc::tmem_ready(x + 32);
+            for (int it = 0; it < t.steps && go; ++it, ++g) {
+                const int st = g % S::kStages, i0 = it % t.per_head;
+                const float *lse2 = stats + st * 256 + half * 64, *del = lse2 + 128;
+                go = __all_sync(0xffffffffu,
+                                tc::mbar_wait(b.s_full, g & 1, b.abort, f.status, kErrS, f.spin) &&
+                                tc::mbar_wait(b.full0 + st, (g / S::kStages) & 1, b.abort, f.status, kErrA, f.spin));
+                if (!go) break;
+                tc::tc_fence_after_sync();
+                float x[64];
+                tc::tmem_start(ts, x);
+                tc::tmem_start(ts + 32, x + 32);
+                tc::tmem_ready(x);
+                tc::tmem_ready(x + 32);
 #pragma unroll
-            for (int j = 0; j < 64; j += 4) {
-                const float4 z = *reinterpret_cast<const float4 *>(lse2 + j);
-                tc::unpack2(tc::fma2(tc::pack2(x[j], x[j + 1]), c2, tc::pack2(-z.x, -z.y)), x[j], x[j + 1]);
-                tc::unpack2(tc::fma2(tc::pack2(x[j + 2], x[j + 3]), c2, tc::pack2(-z.z, -z.w)), x[j + 2], x[j + 3]);
+                for (int j = 0; j < 64; j += 4) {
+                    const float4 z = *reinterpret_cast<const float4 *>(lse2 + j);
+                    tc::unpack2(tc::fma2(tc::pack2(x[j], x[j + 1]), c2, tc::pack2(-z.x, -z.y)), x[j], x[j + 1]);
+                    tc::unpack2(tc::fma2(tc::pack2(x[j + 2], x[j + 3]), c2, tc::pack2(-z.z, -z.w)), x[j + 2], x[j + 3]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[j + e] = tc::exp2_fast(x[j + e]);
-            }
-            // queries before the key, or behind the sequence
-            const int behind = t.seq_end - (t.first + i0 * kTileRows) - half * 64;
-            const int before = i0 == 0 ? in_tile - half * 64 : 0;
-            if (i0 == 0 || behind < 64) {
-#pragma unroll
-                for (int j = 0; j < 64; ++j) x[j] = j >= before && j < behind ? x[j] : 0.f;
-            }
-            store_weights(ts, x);
-            weights_done(b.p_full);
-            go = __all_sync(0xffffffffu, tc::mbar_wait(b.dp_full, g & 1, b.abort, f.status, kErrDp, f.spin));
-            if (!go) break;
-            tc::tc_fence_after_sync();
-            float y[64];
-            tc::tmem_start(td, y);
-            tc::tmem_start(td + 32, y + 32);
-            tc::tmem_ready(y);
-            tc::tmem_ready(y + 32);
-#pragma unroll
-            for (int j = 0; j < 64; j += 4) {
-                const float4 z = *reinterpret_cast<const float4 *>(del + j);
-                tc::unpack2(tc::mul2(tc::pack2(x[j], x[j + 1]),
-                                     tc::add2(tc::pack2(y[j], y[j + 1]), tc::pack2(-z.x, -z.y))), x[j], x[j + 1]);
-                tc::unpack2(tc::mul2(tc::pack2(x[j + 2], x[j + 3]),
-                                     tc::add2(tc::pack2(y[j + 2], y[j + 3]), tc::pack2(-z.z, -z.w))),
-                            x[j + 2], x[j + 3]);
-            }
-            store_weights(td, x);
-            weights_done(b.ds_full);
-        }
-        go = __all_sync(0xffffffffu, go && tc::mbar_wait(b.acc, n & 1, b.abort, f.status, kErrAcc, f.spin));
-        const int col = t.first + in_tile;
-        const bool mine = col < t.seq_end;
-        const bool fine = __all_sync(0xffffffffu, go && !*b.abort);
-        bool bad = false;
-        // the first four warps write dV, the others dK
-        const uint32_t sums = tmem + lanes + (half ? kDk : kDv);
-        const float by = half ? f.p.scale : 1.f;
-        __nv_bfloat16 *out = (half ? f.gk : f.gv) + ((size_t)col * f.p.Hkv + t.hk) * D;
-        if (fine) tc::tc_fence_after_sync();
-        if (f.split == 1) {
-            if (fine) bad = !store_sums<D>(sums, by, mine ? out : nullptr) && mine;
-        } else {
-            // every CTA lays its sums out over its ring (all copies and products are done)
-            // and finishes its share of the channels, adding in rank order
-            float *own = reinterpret_cast<float *>(sm) + half * 128 * D + in_tile;
-            if (fine) {
-#pragma unroll
-                for (int i = 0; i < D; i += 32) {
-                    float x[32];
-                    tc::tmem_start(sums + i, x);
-                    tc::tmem_ready(x);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) own[(i + j) * 128] = x[j];
+                    for (int e = 0; e < 4; ++e) x[j + e] = tc::exp2_fast(x[j + e]);
                 }
-            }
-            cluster_sync();
-            const int share = D / f.split;
-            const uint32_t from = tc::smem_u32(own);
-            float odd = 0.f;
-            for (int i = rank * share; i < (rank + 1) * share; i += 8) {
-                float x[8] = {};
-                for (int r = 0; r < f.split; ++r) {
+                // queries before the key, or behind the sequence
+                const int behind = t.seq_end - (t.first + i0 * kTileRows) - half * 64;
+                const int before = i0 == 0 ? in_tile - half * 64 : 0;
+                if (i0 == 0 || behind < 64) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] += peer_float(from + (i + j) * 512, r);
+                    for (int j = 0; j < 64; ++j) x[j] = j >= before && j < behind ? x[j] : 0.f;
                 }
-                uint32_t pk[4];
+                store_weights(ts, x);
+                weights_done(b.p_full);
+                go = __all_sync(0xffffffffu, tc::mbar_wait(b.dp_full, g & 1, b.abort, f.status, kErrDp, f.spin));
+                if (!go) break;
+                tc::tc_fence_after_sync();
+                float y[64];
+                tc::tmem_start(td, y);
+                tc::tmem_start(td + 32, y + 32);
+                tc::tmem_ready(y);
+                tc::tmem_ready(y + 32);
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    odd = fmaf(x[j], 0.f, fmaf(x[j + 1], 0.f, odd));
-                    pk[j / 2] = tc::bf16x2(x[j] * by, x[j + 1] * by);
+                for (int j = 0; j < 64; j += 4) {
+                    const float4 z = *reinterpret_cast<const float4 *>(del + j);
+                    tc::unpack2(tc::mul2(tc::pack2(x[j], x[j + 1]),
+                                         tc::add2(tc::pack2(y[j], y[j + 1]), tc::pack2(-z.x, -z.y))), x[j], x[j + 1]);
+                    tc::unpack2(tc::mul2(tc::pack2(x[j + 2], x[j + 3]),
+                                         tc::add2(tc::pack2(y[j + 2], y[j + 3]), tc::pack2(-z.z, -z.w))),
+                                x[j + 2], x[j + 3]);
                 }
-                if (mine && fine) *reinterpret_cast<uint4 *>(out + i) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                store_weights(td, x);
+                weights_done(b.ds_full);
             }
-            bad = mine && fine && !(odd == 0.f);
-            cluster_sync();  // all reads and stores are made
+            go = __all_sync(0xffffffffu, go && tc::mbar_wait(b.acc, n & 1, b.abort, f.status, kErrAcc, f.spin));
+            const int col = t.first + in_tile;
+            const bool mine = col < t.seq_end;
+            const bool fine = __all_sync(0xffffffffu, go && !*b.abort);
+            bool bad = false;
+            // the first four warps write dV, the others dK
+            const uint32_t sums = tmem + lanes + (half ? kDk : kDv);
+            const float by = half ? f.p.scale : 1.f;
+            __nv_bfloat16 *out = (half ? f.gk : f.gv) + ((size_t)col * f.p.Hkv + t.hk) * D;
+            if (fine) tc::tc_fence_after_sync();
+            if (f.split == 1) {
+                if (fine) bad = !store_sums<D>(sums, by, mine ? out : nullptr) && mine;
+            } else {
+                // every CTA lays its sums out over its ring (all copies and products are done)
+                // and finishes its share of the channels, adding in rank order
+                float *own = reinterpret_cast<float *>(sm) + half * 128 * D + in_tile;
+                if (fine) {
+#pragma unroll
+                    for (int i = 0; i < D; i += 32) {
+                        float x[32];
+                        tc::tmem_start(sums + i, x);
+                        tc::tmem_ready(x);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) own[(i + j) * 128] = x[j];
+                    }
+                }
+                cluster_sync();
+                const int share = D / f.split;
+                const uint32_t from = tc::smem_u32(own);
+                float odd = 0.f;
+                for (int i = rank * share; i < (rank + 1) * share; i += 8) {
+                    float x[8] = {};
+                    for (int r = 0; r < f.split; ++r) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] += peer_float(from + (i + j) * 512, r);
+                    }
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        odd = fmaf(x[j], 0.f, fmaf(x[j + 1], 0.f, odd));
+                        pk[j / 2] = tc::bf16x2(x[j] * by, x[j + 1] * by);
+                    }
+                    if (mine && fine) *reinterpret_cast<uint4 *>(out + i) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+                bad = mine && fine && !(odd == 0.f);
+                cluster_sync();  // all reads and stores are made
+            }
+            odd_rows |= bad;
+            if (!fine) break;
         }
-        if (!redo_rows(b, n, fine, bad, [&](int i) { redo_dkv<D>(f, t.first + i, t.seq_end, t.hk); })) break;
-        }
+        if (any_odd_rows(b, odd_rows))
+            for (int n = 0; t.get(f, n, rank); ++n)
+                for (int col = t.first + warp; col < min(t.first + kTileRows, t.seq_end); col += 8) {
+                    const size_t at = ((size_t)col * f.p.Hkv + t.hk) * D;
+                    if (!row_finite<__nv_bfloat16, D>(f.gk + at) || !row_finite<__nv_bfloat16, D>(f.gv + at))
+                        redo_dkv<D>(f, col, t.seq_end, t.hk);
+                }
     }
     if (warp >= 8 && f.split > 1) {
         __syncwarp();
@@ -605,66 +598,72 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         const uint32_t ts = tmem + lanes + kS + half * 64, td = tmem + lanes + kDp + half * 64;
         const float c = f.p.scale * kLog2e;
         const tc::f32x2 c2 = tc::pack2(c, c);
-        bool go = true;
+        bool go = true, odd_rows = false;
         int g = 0;  // steps of all items
         for (int n = 0; t.get(f, n); ++n) {
-        const int row = t.first + in_tile;
-        const bool mine = row < t.seq_end;
-        const size_t at = (size_t)t.h * f.p.tokens + min(row, (int)f.p.tokens - 1);
-        const float z = f.lse2[at], del = f.delta[at];
-        const tc::f32x2 z2 = tc::pack2(-z, -z), d2 = tc::pack2(-del, -del);
-        for (int it = 0; it < t.steps && go; ++it, ++g) {
-            go = __all_sync(0xffffffffu, tc::mbar_wait(b.s_full + (g & 1), (g >> 1) & 1, b.abort, f.status,
-                                                       kErrS, f.spin));
-            if (!go) break;
-            tc::tc_fence_after_sync();
-            float x[64];
-            tc::tmem_start(ts + (g & 1) * 128, x);
-            tc::tmem_start(ts + (g & 1) * 128 + 32, x + 32);
-            tc::tmem_ready(x);
-            tc::tmem_ready(x + 32);
-            tc::tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(b.s_free + (g & 1));
+            const int row = t.first + in_tile;
+            const bool mine = row < t.seq_end;
+            const size_t at = (size_t)t.h * f.p.tokens + min(row, (int)f.p.tokens - 1);
+            const float z = f.lse2[at], del = f.delta[at];
+            const tc::f32x2 z2 = tc::pack2(-z, -z), d2 = tc::pack2(-del, -del);
+            for (int it = 0; it < t.steps && go; ++it, ++g) {
+                go = __all_sync(0xffffffffu, tc::mbar_wait(b.s_full + (g & 1), (g >> 1) & 1, b.abort, f.status,
+                                                           kErrS, f.spin));
+                if (!go) break;
+                tc::tc_fence_after_sync();
+                float x[64];
+                tc::tmem_start(ts + (g & 1) * 128, x);
+                tc::tmem_start(ts + (g & 1) * 128 + 32, x + 32);
+                tc::tmem_ready(x);
+                tc::tmem_ready(x + 32);
+                tc::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(b.s_free + (g & 1));
 #pragma unroll
-            for (int j = 0; j < 64; j += 2) {
-                tc::unpack2(tc::fma2(tc::pack2(x[j], x[j + 1]), c2, z2), x[j], x[j + 1]);
-                x[j] = tc::exp2_fast(x[j]);
-                x[j + 1] = tc::exp2_fast(x[j + 1]);
+                for (int j = 0; j < 64; j += 2) {
+                    tc::unpack2(tc::fma2(tc::pack2(x[j], x[j + 1]), c2, z2), x[j], x[j + 1]);
+                    x[j] = tc::exp2_fast(x[j]);
+                    x[j + 1] = tc::exp2_fast(x[j + 1]);
+                }
+                if (it == 0) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) x[j] = j + half * 64 <= in_tile ? x[j] : 0.f;
+                }
+                go = __all_sync(0xffffffffu, tc::mbar_wait(b.dp_full, g & 1, b.abort, f.status, kErrDp, f.spin));
+                if (!go) break;
+                tc::tc_fence_after_sync();
+                float y[64];
+                tc::tmem_start(td, y);
+                tc::tmem_start(td + 32, y + 32);
+                tc::tmem_ready(y);
+                tc::tmem_ready(y + 32);
+#pragma unroll
+                for (int j = 0; j < 64; j += 2)
+                    tc::unpack2(tc::mul2(tc::pack2(x[j], x[j + 1]), tc::add2(tc::pack2(y[j], y[j + 1]), d2)),
+                                x[j], x[j + 1]);
+                store_weights(td, x);
+                weights_done(b.ds_full);
             }
-            if (it == 0) {
-#pragma unroll
-                for (int j = 0; j < 64; ++j) x[j] = j + half * 64 <= in_tile ? x[j] : 0.f;
+            go = __all_sync(0xffffffffu, go && tc::mbar_wait(b.acc, n & 1, b.abort, f.status, kErrAcc, f.spin));
+            const bool fine = __all_sync(0xffffffffu, go && !*b.abort);
+            bool bad = false;
+            if (fine) {
+                tc::tc_fence_after_sync();
+                // each half of the warps writes half of the row's channels
+                __nv_bfloat16 *out = f.gq + ((size_t)row * f.p.Hq + t.h) * D;
+                constexpr int kPart = D == 32 ? 32 : D / 2;
+                if (D > 32 || half == 0)
+                    bad = !store_sums<kPart>(tmem + lanes + kDq + half * kPart, f.p.scale,
+                                             mine ? out + half * kPart : nullptr) && mine;
             }
-            go = __all_sync(0xffffffffu, tc::mbar_wait(b.dp_full, g & 1, b.abort, f.status, kErrDp, f.spin));
-            if (!go) break;
-            tc::tc_fence_after_sync();
-            float y[64];
-            tc::tmem_start(td, y);
-            tc::tmem_start(td + 32, y + 32);
-            tc::tmem_ready(y);
-            tc::tmem_ready(y + 32);
-#pragma unroll
-            for (int j = 0; j < 64; j += 2)
-                tc::unpack2(tc::mul2(tc::pack2(x[j], x[j + 1]), tc::add2(tc::pack2(y[j], y[j + 1]), d2)),
-                            x[j], x[j + 1]);
-            store_weights(td, x);
-            weights_done(b.ds_full);
+            odd_rows |= bad;
+            if (!fine) break;
         }
-        go = __all_sync(0xffffffffu, go && tc::mbar_wait(b.acc, n & 1, b.abort, f.status, kErrAcc, f.spin));
-        const bool fine = __all_sync(0xffffffffu, go && !*b.abort);
-        bool bad = false;
-        if (fine) {
-            tc::tc_fence_after_sync();
-            // each half of the warps writes half of the row's channels
-            __nv_bfloat16 *out = f.gq + ((size_t)row * f.p.Hq + t.h) * D;
-            constexpr int kPart = D == 32 ? 32 : D / 2;
-            if (D > 32 || half == 0)
-                bad = !store_sums<kPart>(tmem + lanes + kDq + half * kPart, f.p.scale,
-                                         mine ? out + half * kPart : nullptr) && mine;
-        }
-        if (!redo_rows(b, n, fine, bad, [&](int i) { redo_dq<D>(f, t.first + i, t.seq_start, t.h); })) break;
-        }
+        if (any_odd_rows(b, odd_rows))
+            for (int n = 0; t.get(f, n); ++n)
+                for (int row = t.first + warp; row < min(t.first + kTileRows, t.seq_end); row += 8)
+                    if (!row_finite<__nv_bfloat16, D>(f.gq + ((size_t)row * f.p.Hq + t.h) * D))
+                        redo_dq<D>(f, row, t.seq_start, t.h);
     }
     wait_for_previous();
     end_cta(tmem);

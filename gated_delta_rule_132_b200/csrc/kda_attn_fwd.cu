@@ -17,7 +17,8 @@
 //
 // A masked probability is 0, but 0 times an infinity or NaN in a later token's (or
 // another sequence's) value row is NaN. Rows with a result that is not finite are
-// therefore computed again from the visible keys alone.
+// therefore computed again from the visible keys alone, once the CTA is through with its
+// items: until then other warps wait for the ones that would do it.
 #include "kda_attn_rows.cuh"
 #include "kda_attn_tc.cuh"
 
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const uint32_t to = tmem + lanes + S::kTmemO + w * D;
         const float c = f.p.scale * 1.44269504088896340736f;
         int base = 0;  // phases of s_full before this item (of either half)
-        bool go = true;
+        bool go = true, odd_rows = false;
         for (int n = 0; go && t.get(f, n); ++n) {
             if (w && !t.two) continue;
             const int row = t.first + w * kTileRows + in_tile;
@@ -313,13 +314,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 }
             }
             if (mine && f.lse) f.lse[(size_t)row * f.p.Hq + t.h] = m * f.p.scale + logf(l);
-            __syncwarp();
-            unsigned bad = __ballot_sync(0xffffffffu, mine && !(odd == 0.f));
-            for (; bad; bad &= bad - 1)
-                recompute_row<D>(f, row - lane + __ffs(bad) - 1, t.seq_start, t.h);
+            odd_rows |= __any_sync(0xffffffffu, mine && !(odd == 0.f));
             tc::tc_fence_before_sync();
         }
         tc::tc_fence_before_sync();
+        __syncwarp();
+        for (int n = 0; odd_rows && go && t.get(f, n); ++n) {
+            const int begin = t.first + warp * 32, end = min(begin + 32, t.seq_end);
+            for (int row = begin; row < end; ++row)
+                if (!row_finite<__nv_bfloat16, D>(f.o + ((size_t)row * f.p.Hq + t.h) * D))
+                    recompute_row<D>(f, row, t.seq_start, t.h);
+        }
     }
     __syncthreads();
     if (warp == 8) {

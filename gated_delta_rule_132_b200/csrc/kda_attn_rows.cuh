@@ -44,6 +44,16 @@ __device__ __forceinline__ float row_dot(const float (&a)[V], const float (&b)[V
     return warp_sum(s);
 }
 
+// Whether a row holds nothing but finite numbers, by the whole warp.
+template <typename T, int D> __device__ __forceinline__ bool row_finite(const T *row)
+{
+    float x[D / 32], odd = 0.f;
+    load_row<T, D>(row, x);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) odd = fmaf(x[i], 0.f, odd);  // NaN if x is not
+    return __all_sync(0xffffffffu, odd == 0.f);
+}
+
 // Running softmax of one query row: m the maximum of the scaled scores so far, l
 // the sum of e^(s - m), acc the same sum over the values.
 template <int V>

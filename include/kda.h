@@ -105,9 +105,9 @@ kda_status_t kda_chunk_fwd_status(const void *workspace, size_t workspace_bytes,
  * Debugging aid for the failure path (process-wide; not needed in normal use):
  * `polls` replaces the poll limit of every bounded wait in the tensor-core
  * kernels launched afterwards (0 restores the default of 2^20 polls), and a
- * nonzero `starve_carry` makes the sequential kernel's copy producer issue no
- * copies, so that its first wait on a chunk record runs out while nothing
- * asynchronous is in flight. The kernels then return early and the status word
+ * nonzero `starve_carry` makes the sequential kernel's copy producer (and the
+ * tensor-core attention kernels' loading warps) issue no copies, so that the
+ * first wait on a copy runs out while nothing asynchronous is in flight. The kernels then return early and the status word
  * reports the failure. Always returns KDA_OK.
  */
 kda_status_t kda_debug_set_wait_limit(unsigned int polls, int starve_carry);

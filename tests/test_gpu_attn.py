@@ -84,6 +84,44 @@ def test_many_sequences_keep_their_order(d):
     R.close(lse[0], rl, tl)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("count,longest", [(300, 200), (60, 700), (2100, 9)])
+def test_many_packed(count, longest, dtype):
+    """More tiles than CTAs, of all sizes: every one is worked on once, in either order."""
+    g = torch.Generator().manual_seed(count)
+    lens = torch.randint(0, longest + 1, (count,), generator=g).tolist()
+    q, k, v, dO = inputs(27, sum(lens), 3, 1, 64, DT[dtype])
+    check(q, k, v, dO, spans_of(lens), cu_of(lens))
+
+
+def test_starved_kernels_report_their_wait():
+    """A loading warp that copies nothing: the waits run out, the status word says so, and the
+    next call on the workspace is clean. Nothing is in flight meanwhile."""
+    from gated_delta_rule_132_b200 import kda
+    attn = api()
+    for Hq, Hkv, T in ((2, 1, 300), (4, 1, 100)):  # a key tile's CTA alone, and a cluster
+        q, k, v, dO = inputs(28, T, Hq, Hkv, 128, torch.bfloat16)
+        want = attn.kda_attn_fwd(q, k, v)
+        grads = attn.kda_attn_bwd(q, k, v, *want, dO)
+        for cu in (None, cu_of([T // 3, T - T // 3])):
+            ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+            calls = (lambda: attn.kda_attn_fwd(q, k, v, cu_seqlens=cu, workspace=ws),
+                     lambda: attn.kda_attn_bwd(q, k, v, *want, dO, cu_seqlens=cu, workspace=ws))
+            for call in calls:
+                try:
+                    kda.kda_debug_set_wait_limit(20000, starve_carry=True)
+                    call()
+                    status, code = attn.kda_attn_status(ws)
+                finally:
+                    kda.kda_debug_set_wait_limit(0, starve_carry=False)
+                assert status == 6 and code != 0
+                call()
+                assert attn.kda_attn_status(ws) == (0, 0)
+        assert torch.equal(attn.kda_attn_fwd(q, k, v)[0], want[0])
+        again = attn.kda_attn_bwd(q, k, v, *want, dO)
+        assert all(torch.equal(again[n], grads[n]) for n in grads)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_long_sharp(d):
     """A longer sequence with large scores, whose row maximum moves late, and a scale of one."""

@@ -220,6 +220,25 @@ def test_offsets_past_32_bits():
     check((q, kp, vp, ids, torch.tensor([170], dtype=torch.int32, device="cuda")), None)
 
 
+@pytest.mark.parametrize("n_draft", [1, 20, 40])
+def test_starved_kernels_report_their_wait(n_draft):
+    from gated_delta_rule_132_b200 import kda
+    attn = api()
+    x = cache(24, [300, 5], n_draft, 16, 8, 2, 128, torch.bfloat16)
+    want = attn.kda_attn_tree(*x)
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    try:
+        kda.kda_debug_set_wait_limit(20000, starve_carry=True)
+        attn.kda_attn_tree(*x, workspace=ws)
+        status, code = attn.kda_attn_status(ws)
+    finally:
+        kda.kda_debug_set_wait_limit(0, starve_carry=False)
+    assert status == 6 and code != 0
+    again = attn.kda_attn_tree(*x, workspace=ws)
+    assert attn.kda_attn_status(ws) == (0, 0)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
 def test_refusals():
     attn = api()
     from gated_delta_rule_132_b200.kda import KdaError
