@@ -99,6 +99,10 @@ __device__ __forceinline__ void tma_load_4d(void *dst_smem, const void *tmap, in
 // in uniform registers. Issued from a single-lane branch, each instruction cost the
 // moves of its operands there.
 
+// A barrier's phase is told by its parity only: whoever waits on a barrier has to see every
+// phase of it, or be sure that it is at most one ahead. (With rings whose stages alternate
+// between two consumers, the number of stages is even for that.)
+//
 // Wait for two phases at once, by the whole warp: every other lane polls the other
 // barrier, since a poll costs some 150 cycles even of a phase that is complete.
 __device__ __forceinline__ bool wait_both(uint64_t *a, int na, uint64_t *b, int nb, volatile int *abort,
@@ -106,6 +110,15 @@ __device__ __forceinline__ bool wait_both(uint64_t *a, int na, uint64_t *b, int 
 {
     const bool odd = threadIdx.x & 1;
     return __all_sync(0xffffffffu, mbar_wait(odd ? b : a, (odd ? nb : na) & 1, abort, err, code, limit));
+}
+
+// The same for three.
+__device__ __forceinline__ bool wait_three(uint64_t *a, int na, uint64_t *b, int nb, uint64_t *c, int nc,
+                                           volatile int *abort, int *err, int code, uint32_t limit)
+{
+    const int which = (threadIdx.x & 31) % 3;
+    return __all_sync(0xffffffffu, mbar_wait(which == 0 ? a : which == 1 ? b : c,
+                                             (which == 0 ? na : which == 1 ? nb : nc) & 1, abort, err, code, limit));
 }
 
 // D[tmem] (+)= A[smem desc] * B[smem desc], bf16 inputs, fp32 accumulate.

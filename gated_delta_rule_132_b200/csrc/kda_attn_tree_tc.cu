@@ -26,16 +26,19 @@ enum : int { kErrQ = 131, kErrK, kErrV, kErrFree, kErrS, kErrP, kErrO, kErrDrain
 template <int D, bool kPair>
 struct TcShape {
     static constexpr int kMaskThreads = 256;
-    static constexpr int kStages = D < 128 ? 4 : kPair ? 2 : 3;
+    // Without kPair a stage is to serve the same half always: even numbers of them.
+    static constexpr int kStagesK = D < 128 || !kPair ? 4 : 2, kStagesV = D < 128 ? 4 : 2;
     static constexpr uint32_t kTile = TileShape<D>::kBytes;
-    static constexpr uint32_t kQ = 0, kK = (kPair ? 2 : 1) * kTile, kV = kK + kStages * kTile;
-    static constexpr uint32_t kSeen = kV + kStages * kTile;   // 64 x 8 bytes
+    static constexpr uint32_t kQ = 0, kK = (kPair ? 2 : 1) * kTile, kV = kK + kStagesK * kTile;
+    static constexpr uint32_t kSeen = kV + kStagesV * kTile;  // 64 x 8 bytes
     static constexpr uint32_t kParents = kSeen + 512;         // 64 x 4
     static constexpr uint32_t kMl = kParents;                 // then float2 [128] of the odd tiles
     static constexpr uint32_t kBad = kMl + 1024;              // rows to compute again, 8 words
-    static constexpr uint32_t kThere = kBad + 32;             // [stage] 16 bytes
-    static constexpr uint32_t kBars = kThere + 64;
-    static constexpr uint32_t kBytes = kBars + (6 + 4 * kStages) * 8 + 8 + 1024;
+    // [step % 8] 16 bytes: which keys are there. Written with the keys' load, read when their
+    // scores are; by then the loads are at most six steps on.
+    static constexpr uint32_t kThere = kBad + 32;
+    static constexpr uint32_t kBars = kThere + 128;
+    static constexpr uint32_t kBytes = kBars + (6 + 2 * kStagesK + 2 * kStagesV) * 8 + 8 + 1024;
     static_assert(kThere % 16 == 0, "alignment");
     static constexpr uint32_t kTmemS = 0, kTmemO = 256;
     static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -90,12 +93,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     uint8_t *sm = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *q_full = reinterpret_cast<uint64_t *>(sm + S::kBars);
-    uint64_t *k_full = q_full + 1, *k_free = k_full + S::kStages;
-    uint64_t *v_full = k_free + S::kStages, *v_free = v_full + S::kStages;
-    uint64_t *s_full = v_free + S::kStages, *p_full = s_full + 2, *o_full = p_full + 2;
+    uint64_t *k_full = q_full + 1, *k_free = k_full + S::kStagesK;
+    uint64_t *v_full = k_free + S::kStagesK, *v_free = v_full + S::kStagesV;
+    uint64_t *s_full = v_free + S::kStagesV, *p_full = s_full + 2, *o_full = p_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_full + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    // keys of a stage that are there, 128 bits each (written with the values)
     uint32_t *there_of = reinterpret_cast<uint32_t *>(sm + S::kThere);
     uint32_t *bad = reinterpret_cast<uint32_t *>(sm + S::kBad);
 
@@ -112,9 +114,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     if (warp == 8) tc::tmem_alloc(tmem_slot, 512);
     if (threadIdx.x == 0) {
         tc::mbar_init(q_full, 1);
-        for (int i = 0; i < S::kStages; ++i) {
+        for (int i = 0; i < S::kStagesK; ++i) {
             tc::mbar_init(k_full + i, 1);
             tc::mbar_init(k_free + i, 1 + two);  // kPair: by both halves
+        }
+        for (int i = 0; i < S::kStagesV; ++i) {
             tc::mbar_init(v_full + i, 1);
             tc::mbar_init(v_free + i, 1 + two);
         }
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 
     if (warp >= 8) {
         tc::fewer_registers<kRegsOther>();
-        // one warp loads the keys (and q), one the values and which keys are there
+        // one warp loads the keys, with which of them are there, and q; one the values
         if ((warp == 9 || warp == 10) && !f.starve) {
             const bool keys = warp == 9, by_page = f.p.page_shift >= 3;
             if (keys && lane == 0) {
@@ -151,21 +155,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             uint64_t *full = keys ? k_full : v_full, *free = keys ? k_free : v_free;
             uint8_t *ring = sm + (keys ? S::kK : S::kV);
             const CUtensorMap *map = keys ? &f.k : &f.v;
+            const int stages = keys ? S::kStagesK : S::kStagesV;
             int it = 0, page = by_page && steps ? boxes.page(f, s, s.first) : 0;
             for (; it < steps; ++it) {
-                const int st = it % S::kStages, use = it / S::kStages, pos = s.first + it * kTileRows;
+                const int st = it % stages, use = it / stages, pos = s.first + it * kTileRows;
                 const int next = by_page ? boxes.page(f, s, pos + kTileRows) : 0;
                 const bool go = !use || tc::mbar_wait(free + st, (use - 1) & 1, abort, f.status, kErrFree, f.spin);
                 if (!__all_sync(0xffffffffu, go)) break;
                 const int row = by_page ? boxes.row(f, s, pos, page) : 0;
-                if (!keys) {
+                if (keys) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t there =
                             by_page ? boxes.there(f, s, pos, row, e)
                                     : __ballot_sync(0xffffffffu, pos + 32 * e + lane < s.last &&
                                                                      key_at(f.p, s.table, pos + 32 * e + lane, s.hk) >= 0);
-                        if (lane == 0) there_of[st * 4 + e] = there;
+                        if (lane == 0) there_of[it % 8 * 4 + e] = there;
                     }
                 }
                 if (by_page) load_boxes<D>(boxes, row, map, ring + st * S::kTile, full + st);
@@ -175,8 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             // whatever the other warps do, the copies land before the memory is let go
             if (lane == 0) {
                 if (keys) tc::mbar_drain(q_full, 0, f.status, kErrDrain);
-                for (int i = max(0, it - S::kStages); i < it; ++i)
-                    tc::mbar_drain(full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
+                for (int i = max(0, it - stages); i < it; ++i)
+                    tc::mbar_drain(full + i % stages, (i / stages) & 1, f.status, kErrDrain);
             }
         }
         // one warp issues for each half
@@ -193,19 +198,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             bool go = wait(q_full, 0, kErrQ);
             int nth = 0;
             for (int it = kPair ? 0 : w; go; it += kEvery, ++nth) {
-                const int st = it % S::kStages, before = (it - kEvery + S::kStages) % S::kStages;
-                // P says that the step's values are there: its rows have looked which keys are
-                go = tc::wait_both(it < steps ? k_full + st : q_full, it < steps ? it / S::kStages : 0,
-                                   nth > 0 ? p_full + w : q_full, nth > 0 ? nth - 1 : 0, abort, f.status, kErrP, f.spin);
-                if (go && nth > 0) {  // O += P V of the half's step before
-                    tc::tc_fence_after_sync();
-                    tc::mma_weights_rows<D, 32>(o_acc, s_acc, v + before * S::kTile, nth > 1, lead);
-                }
-                if (!go || it >= steps) break;
+                const int st = it % S::kStagesK, last = it - kEvery;
+                const int before = (last + S::kStagesV) % S::kStagesV;
+                const bool qk = it < steps, pv = nth > 0;  // S of this step, O += P V of the half's last
+                go = tc::wait_three(qk ? k_full + st : q_full, qk ? it / S::kStagesK : 0,
+                                    pv ? v_full + before : q_full, pv ? last / S::kStagesV : 0,
+                                    pv ? p_full + w : q_full, pv ? nth - 1 : 0, abort, f.status, kErrP, f.spin);
+                if (!go) break;
+                tc::tc_fence_after_sync();
+                if (pv) tc::mma_weights_rows<D, 32>(o_acc, s_acc, v + before * S::kTile, nth > 1, lead);
+                if (!qk) break;
                 tc::mma_rows_rows<D>(s_acc, q, k + st * S::kTile, lead);
                 tc::commit(s_full + w, lead);
                 tc::commit(k_free + st, lead);
-                if (nth > 0) tc::commit(v_free + before, lead);
+                if (pv) tc::commit(v_free + before, lead);
             }
             tc::commit(o_full, lead);
             tc::mbar_drain(o_full, 0, f.status, kErrDrain);
@@ -227,10 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         int nth = 0;
         for (int it = 0; it < steps; ++it) {
             if (!works(w, it)) continue;
-            const int st = it % S::kStages;
-            go = __all_sync(0xffffffffu,
-                            tc::mbar_wait(v_full + st, (it / S::kStages) & 1, abort, f.status, kErrV, f.spin) &&
-                            tc::mbar_wait(s_full + w, nth & 1, abort, f.status, kErrS, f.spin));
+            go = __all_sync(0xffffffffu, tc::mbar_wait(s_full + w, nth & 1, abort, f.status, kErrS, f.spin));
             if (!go) break;
             tc::tc_fence_after_sync();
             const int pos = s.first + it * kTileRows;
@@ -239,10 +242,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             for (int j = 0; j < 4; ++j) tc::tmem_start(ts + 32 * j, x + 32 * j);
 #pragma unroll
             for (int j = 0; j < 4; ++j) tc::tmem_ready(x + 32 * j);
-            const uint4 there = *reinterpret_cast<const uint4 *>(there_of + st * 4);
+            const uint4 there = *reinterpret_cast<const uint4 *>(there_of + it % 8 * 4);
             const uint32_t real[4] = {there.x, there.y, there.z, there.w};
             if ((real[0] & real[1] & real[2] & real[3]) != ~0u || pos + kTileRows > s.ctx) {
                 // what is behind the sequence in its last page is not to meet a weight of 0
+                const int st = it % S::kStagesV;
+                go = __all_sync(0xffffffffu, tc::mbar_wait(v_full + st, (it / S::kStagesV) & 1, abort, f.status,
+                                                           kErrV, f.spin));
+                if (!go) break;
                 if (!(real[in_tile >> 5] >> (in_tile & 31) & 1)) {
 #pragma unroll
                     for (int b = 0; b < TileShape<D>::kBlocks; ++b) {
