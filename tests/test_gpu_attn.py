@@ -225,6 +225,23 @@ def test_runs_are_bit_equal(dtype):
         assert all(torch.equal(g1[n], g2[n]) for n in g1)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_calls_one_after_another_agree(d):
+    """Many calls without a pause in between, on two sets of inputs in turn."""
+    attn, lens = api(), [900, 33, 1700, 128, 257]
+    cu = cu_of(lens)
+    sets = [inputs(s, sum(lens), 8, 2, d, torch.bfloat16) for s in (29, 30)]
+
+    def run(x):
+        o, lse = attn.kda_attn_fwd(*x[:3], cu_seqlens=cu)
+        return [o, lse, *attn.kda_attn_bwd(*x[:3], o, lse, x[3], cu_seqlens=cu).values()]
+
+    want = [run(x) for x in sets]
+    for _ in range(20):
+        for i, got in enumerate([run(sets[i % 2]) for i in range(10)]):
+            assert all(torch.equal(a, b) for a, b in zip(got, want[i % 2]))
+
+
 def test_no_lse_and_given_buffers():
     from gated_delta_rule_132_b200 import kda
     import ctypes

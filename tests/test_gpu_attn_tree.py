@@ -184,6 +184,17 @@ def test_runs_are_bit_equal_and_independent_of_the_batch():
         assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
 
 
+@pytest.mark.parametrize("n_draft", [1, 9, 24, 50])
+def test_calls_one_after_another_agree(n_draft):
+    """Many calls without a pause in between, on two sets of inputs in turn."""
+    sets = [cache(s, [9000, 130, 4000], n_draft, 64, 8, 2, 128, torch.bfloat16) for s in (25, 26)]
+    want = [check(x, None) for x in sets]
+    for _ in range(30):
+        got = [api().kda_attn_tree(*sets[i % 2]) for i in range(10)]
+        for i, (o, lse) in enumerate(got):
+            assert torch.equal(o, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
+
+
 def test_stream_and_graphs():
     attn = api()
     sets = [cache(s, [500, 40], 3, 16, 4, 2, 64, torch.bfloat16) for s in (15, 16)]
