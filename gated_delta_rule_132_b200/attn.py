@@ -29,6 +29,7 @@ _CALLS = {
     "kda_cache_compact": [_vp, _vp, _i] + [_vp] * 3 + [_i] * 7 + [_vp, _vp],
     "kda_cache_copy_pages": [_vp, _vp, _i, _vp] + [_i] * 5 + [_vp],
 }
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, by device index
 _DTYPES = {torch.float32: KDA_DTYPE_F32, torch.bfloat16: KDA_DTYPE_BF16}
 _ready = False
 
@@ -67,8 +68,8 @@ def _p(t):
 
 def _check(t, name, dtype, shape, device):
     """A contiguous CUDA tensor of this type, shape (None: any) and device."""
-    if t.dtype is dtype and (shape is None or t.shape == shape) and t.device == device \
-            and t.is_cuda and t.is_contiguous():
+    if (t.dtype is dtype and (shape is None or t.shape == shape) and t.is_cuda
+            and t.is_contiguous() and t.device == device):
         return
     _need(t, name, dtype, shape)
     raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -80,15 +81,16 @@ def _stream_of(device, stream):
         yield
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _on(device, stream):
-    """The context in which ``device`` and ``stream`` are the current ones (nothing where
-    they are): what a call allocates belongs to the stream that its work runs on."""
+def _on(device, stream, body, *args):
+    """``body(*args)`` with ``device`` and ``stream`` as the current ones: what a call allocates
+    belongs to the stream that its work runs on."""
     if stream is not None and stream != torch.cuda.current_stream(device):
-        return _stream_of(device, stream)
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        with _stream_of(device, stream):
+            return body(*args)
+    if device.index == torch.cuda.current_device():
+        return body(*args)
+    with torch.cuda.device(device):
+        return body(*args)
 
 
 @functools.lru_cache(maxsize=None)
@@ -98,20 +100,18 @@ def _function(fn):
 
 def _call(fn, device, *args):
     """C call ``fn`` on the device's current stream."""
-    st = _function(fn)(*args, torch._C._cuda_getCurrentRawStream(device.index))
-    if st != 0:
+    st = _function(fn)(*args, _raw_stream(device.index))
+    if st:
         raise KdaError(fn, st)
 
 
-def _ws(workspace, need, device):
+def _ws(workspace, like, fn, *sizes):
+    """The caller's workspace, checked, or a new one: the tensor and its bytes."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    _check(workspace, "workspace", workspace.dtype, None, device)
-    return workspace
-
-
-def _bytes(t):
-    return t.numel() * t.element_size()
+        need = _size(fn, *sizes)
+        return like.new_empty(need, dtype=torch.uint8), need
+    _check(workspace, "workspace", workspace.dtype, None, like.device)
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _out(t, name, like, dtype, shape):
@@ -149,13 +149,15 @@ def kda_attn_fwd(q, k, v, cu_seqlens=None, scale=None, o=None, lse=None, workspa
     logarithm of each row's sum). Tokens outside every sequence are not written.
     """
     sizes, n, dt, scale = _prompt(q, k, v, cu_seqlens, scale)
-    dev = q.device
-    with _on(dev, stream):
-        o = _out(o, "o", q, q.dtype, q.shape)
-        lse = _out(lse, "lse", q, torch.float32, q.shape[:3])
-        ws = _ws(workspace, _size("kda_attn_fwd_workspace_size", *sizes, n, dt), dev)
-        _call("kda_attn_fwd", dev, _p(q), _p(k), _p(v), dt, _p(cu_seqlens), n, *sizes, scale,
-              _p(o), _p(lse), _p(ws), _bytes(ws))
+    return _on(q.device, stream, _fwd, q, k, v, cu_seqlens, sizes, n, dt, scale, o, lse, workspace)
+
+
+def _fwd(q, k, v, cu_seqlens, sizes, n, dt, scale, o, lse, workspace):
+    o = _out(o, "o", q, q.dtype, q.shape)
+    lse = _out(lse, "lse", q, torch.float32, sizes[:3])
+    ws, size = _ws(workspace, q, "kda_attn_fwd_workspace_size", *sizes, n, dt)
+    _call("kda_attn_fwd", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, _p(cu_seqlens), n,
+          *sizes, scale, o.data_ptr(), lse.data_ptr(), ws.data_ptr(), size)
     return o, lse
 
 
@@ -167,11 +169,15 @@ def kda_attn_bwd(q, k, v, o, lse, dO, cu_seqlens=None, scale=None, workspace=Non
     _check(o, "o", q.dtype, q.shape, dev)
     _check(dO, "dO", q.dtype, q.shape, dev)
     _check(lse, "lse", torch.float32, q.shape[:3], dev)
-    with _on(dev, stream):
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        ws = _ws(workspace, _size("kda_attn_bwd_workspace_size", *sizes, n, dt), dev)
-        _call("kda_attn_bwd", dev, _p(q), _p(k), _p(v), _p(o), _p(lse), _p(dO), dt,
-              _p(cu_seqlens), n, *sizes, scale, _p(dq), _p(dk), _p(dv), _p(ws), _bytes(ws))
+    return _on(dev, stream, _bwd, q, k, v, o, lse, dO, cu_seqlens, sizes, n, dt, scale, workspace)
+
+
+def _bwd(q, k, v, o, lse, dO, cu_seqlens, sizes, n, dt, scale, workspace):
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ws, size = _ws(workspace, q, "kda_attn_bwd_workspace_size", *sizes, n, dt)
+    _call("kda_attn_bwd", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+          lse.data_ptr(), dO.data_ptr(), dt, _p(cu_seqlens), n, *sizes, scale, dq.data_ptr(),
+          dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), size)
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
@@ -180,8 +186,8 @@ def kda_attn_status(workspace, stream=None):
     for the stream): (0, 0), or (6, code of the first bounded wait that ran out)."""
     code = _i(0)
     s = torch.cuda.current_stream(workspace.device) if stream is None else stream
-    st = _lib().kda_attn_status(_p(workspace), _bytes(workspace), ctypes.byref(code),
-                                ctypes.c_void_p(s.cuda_stream))
+    st = _lib().kda_attn_status(_p(workspace), workspace.numel() * workspace.element_size(),
+                                ctypes.byref(code), ctypes.c_void_p(s.cuda_stream))
     if st not in (0, 6):
         raise KdaError("kda_attn_status", st)
     return st, code.value
@@ -232,14 +238,18 @@ def kda_attn_tree(q, k_pages, v_pages, block_table, ctx_lens, parents=None, scal
     if parents is not None:
         _ints(parents, "parents", (N, R), dev)
     scale = d ** -0.5 if scale is None else float(scale)
-    with _on(dev, stream):
-        o = _out(o, "o", q, q.dtype, q.shape)
-        lse = _out(lse, "lse", q, torch.float32, q.shape[:3])
-        ws = _ws(workspace, _size("kda_attn_tree_workspace_size", N, R, Hq, Hkv, d, M, page, dt),
-                 dev)
-        _call("kda_attn_tree", dev, _p(q), _p(k_pages), _p(v_pages), dt, _p(block_table),
-              _p(ctx_lens), _p(parents), N, R, Hq, Hkv, d, P, M, page, scale, _p(o), _p(lse),
-              _p(ws), _bytes(ws))
+    return _on(dev, stream, _tree, q, k_pages, v_pages, block_table, ctx_lens, parents,
+               (N, R, Hq, Hkv, d), P, (M, page), dt, scale, o, lse, workspace)
+
+
+def _tree(q, k_pages, v_pages, block_table, ctx_lens, parents, sizes, P, table, dt, scale, o, lse,
+          workspace):
+    o = _out(o, "o", q, q.dtype, q.shape)
+    lse = _out(lse, "lse", q, torch.float32, sizes[:3])
+    ws, size = _ws(workspace, q, "kda_attn_tree_workspace_size", *sizes, *table, dt)
+    _call("kda_attn_tree", q.device, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), dt,
+          block_table.data_ptr(), ctx_lens.data_ptr(), _p(parents), *sizes, P, *table, scale,
+          o.data_ptr(), lse.data_ptr(), ws.data_ptr(), size)
     return o, lse
 
 
@@ -253,11 +263,14 @@ def kda_cache_fork(refs, block_table, lens, parents, stream=None):
     _ints(refs, "refs", None, dev)
     _ints(lens, "lens", (N,), dev)
     _ints(parents, "parents", (n_out,), dev)
-    with _on(dev, stream):
+
+    def body():
         table, out = lens.new_empty((n_out, M)), lens.new_empty(n_out)
-        _call("kda_cache_fork", dev, _p(refs), _p(block_table), _p(lens), _p(parents), N, n_out,
-              M, refs.numel(), _p(table), _p(out))
-    return table, out
+        _call("kda_cache_fork", dev, refs.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+              parents.data_ptr(), N, n_out, M, refs.numel(), table.data_ptr(), out.data_ptr())
+        return table, out
+
+    return _on(dev, stream, body)
 
 
 def kda_cache_reserve(refs, block_table, lens, add, page_size, workspace=None, stream=None):
@@ -271,12 +284,16 @@ def kda_cache_reserve(refs, block_table, lens, add, page_size, workspace=None, s
     _ints(refs, "refs", None, dev)
     _ints(lens, "lens", (N,), dev)
     _ints(add, "add", (N,), dev)
-    with _on(dev, stream):
+
+    def body():
         copies, status = lens.new_empty((N, 2)), lens.new_empty(1)
-        ws = _ws(workspace, _size("kda_cache_reserve_workspace_size", N, M, P), dev)
-        _call("kda_cache_reserve", dev, _p(refs), _p(block_table), _p(lens), _p(add), N, M, P,
-              int(page_size), _p(copies), _p(status), _p(ws), _bytes(ws))
-    return copies, status
+        ws, size = _ws(workspace, lens, "kda_cache_reserve_workspace_size", N, M, P)
+        _call("kda_cache_reserve", dev, refs.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+              add.data_ptr(), N, M, P, int(page_size), copies.data_ptr(), status.data_ptr(),
+              ws.data_ptr(), size)
+        return copies, status
+
+    return _on(dev, stream, body)
 
 
 def kda_cache_release(refs, block_table, lens, new_lens, page_size, stream=None):
@@ -287,9 +304,8 @@ def kda_cache_release(refs, block_table, lens, new_lens, page_size, stream=None)
     _ints(refs, "refs", None, dev)
     _ints(lens, "lens", (N,), dev)
     _ints(new_lens, "new_lens", (N,), dev)
-    with _on(dev, stream):
-        _call("kda_cache_release", dev, _p(refs), _p(block_table), _p(lens), _p(new_lens), N, M,
-              refs.numel(), int(page_size))
+    _on(dev, stream, _call, "kda_cache_release", dev, refs.data_ptr(), block_table.data_ptr(),
+        lens.data_ptr(), new_lens.data_ptr(), N, M, refs.numel(), int(page_size))
 
 
 def kda_cache_append(k_pages, v_pages, block_table, start, k_new, v_new, cu_seqlens=None,
@@ -309,9 +325,9 @@ def kda_cache_append(k_pages, v_pages, block_table, start, k_new, v_new, cu_seql
     if N != (n_seqs if cu_seqlens is not None else B):
         raise ValueError(f"block_table has {N} rows for {n_seqs or B} sequences")
     _ints(start, "start", (N,), dev)
-    with _on(dev, stream):
-        _call("kda_cache_append", dev, _p(k_pages), _p(v_pages), dt, _p(block_table), _p(start),
-              _p(k_new), _p(v_new), _p(cu_seqlens), n_seqs, B, T, Hkv, d, P, M, page)
+    _on(dev, stream, _call, "kda_cache_append", dev, k_pages.data_ptr(), v_pages.data_ptr(), dt,
+        block_table.data_ptr(), start.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+        _p(cu_seqlens), n_seqs, B, T, Hkv, d, P, M, page)
 
 
 def kda_cache_compact(k_pages, v_pages, block_table, ctx_lens, path, stream=None):
@@ -326,11 +342,15 @@ def kda_cache_compact(k_pages, v_pages, block_table, ctx_lens, path, stream=None
     R = path.shape[1]
     _ints(path, "path", (N, R), dev)
     _ints(ctx_lens, "ctx_lens", (N,), dev)
-    with _on(dev, stream):
+
+    def body():
         out = path.new_empty(N)
-        _call("kda_cache_compact", dev, _p(k_pages), _p(v_pages), dt, _p(block_table),
-              _p(ctx_lens), _p(path), N, R, Hkv, d, P, M, page, _p(out))
-    return out
+        _call("kda_cache_compact", dev, k_pages.data_ptr(), v_pages.data_ptr(), dt,
+              block_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(), N, R, Hkv, d, P, M,
+              page, out.data_ptr())
+        return out
+
+    return _on(dev, stream, body)
 
 
 def kda_cache_copy_pages(k_pages, v_pages, copies, stream=None):
@@ -340,6 +360,5 @@ def kda_cache_copy_pages(k_pages, v_pages, copies, stream=None):
     (P, Hkv, page, d), dt = _pool(k_pages, v_pages)
     C = copies.shape[0]
     _ints(copies, "copies", (C, 2), dev)
-    with _on(dev, stream):
-        _call("kda_cache_copy_pages", dev, _p(k_pages), _p(v_pages), dt, _p(copies), C, Hkv, d,
-              P, page)
+    _on(dev, stream, _call, "kda_cache_copy_pages", dev, k_pages.data_ptr(), v_pages.data_ptr(), dt,
+        copies.data_ptr(), C, Hkv, d, P, page)
