@@ -66,7 +66,7 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, const void *o, const float *ls
                             cudaStream_t st);
 
 // The tensor-core path (bf16).
-int attn_tc_fwd_rows();
+int attn_tc_fwd_rows(const AttnProblem &p);
 int attn_tc_bwd_rows();
 cudaError_t launch_attn_tc_fwd(const AttnProblem &p, void *o, float *lse, void *workspace,
                                cudaStream_t st);

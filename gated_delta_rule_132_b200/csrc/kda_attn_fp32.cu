@@ -483,7 +483,7 @@ cudaError_t bwd(const AttnProblem &p, const void *o, const float *lse, const voi
 
 int attn_fwd_rows(const AttnProblem &p)
 {
-    return p.dtype == KDA_DTYPE_BF16 ? attn_tc_fwd_rows() : kRows;
+    return p.dtype == KDA_DTYPE_BF16 ? attn_tc_fwd_rows(p) : kRows;
 }
 
 int attn_bwd_rows(const AttnProblem &p)

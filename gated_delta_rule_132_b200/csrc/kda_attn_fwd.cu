@@ -1,7 +1,10 @@
 // kda_attn_fwd.cu — causal prompt attention on the tensor cores (bf16, d = 32, 64, 128).
 //
-// A work item is (256 query tokens, query head): two query tiles of 128 rows that share
-// the key/value tiles, walked from the diagonal down to the sequence's first tile. One
+// A work item is two query tiles of 128 rows that share the key/value tiles, walked from
+// the diagonal down to the sequence's first tile: 128 tokens of two heads of one key/value
+// head where those come in pairs, else 256 tokens of one head, whose first tile sits out
+// a step and whose second is absent from every other sequence's end (24 packed prompts
+// of up to 700 tokens, 16 heads: HEADS_US against TOKENS_US us). One
 // persistent CTA per SM takes items in order of falling work; its loads and products
 // run on into the next item while the rows of the last one are written. (With a CTA per
 // item, beginning and end cost 8 us of an SM, as much as five steps.)
@@ -25,7 +28,6 @@
 namespace kda {
 namespace {
 
-constexpr int kRows = 2 * kTileRows;
 constexpr int kThreads = 384;  // two softmax warpgroups; MMA, load and two idle warps
 // 384 threads start with 168 registers; the softmax keeps a row of 128 scores.
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
@@ -39,7 +41,7 @@ struct FwdParams {
     __nv_bfloat16 *o;
     float *lse;
     int *status;
-    int items;
+    int items, heads;  // heads: of an item, 1 or 2
     uint32_t spin;
     int starve;
 };
@@ -63,26 +65,33 @@ __device__ __noinline__ void recompute_row(const FwdParams &f, int row, int star
     attn_row_fwd<__nv_bfloat16, D>(f.p, row, start, h, f.o, f.lse);
 }
 
+__host__ __device__ constexpr int fwd_rows(int heads) { return 2 * kTileRows / heads; }
+
 // An item: its query tiles, and the key tiles from the last one down: step it reads key
 // tile last - it; query tile w takes part from step begin(w) on.
 struct FwdItem {
     int h, first, seq_start, seq_end, last, steps;
-    bool two;
+    int next_h, next_row;  // from the first tile to the second
+    bool two, late;        // there is a second tile; the first one sits out a step
     __device__ __forceinline__ bool get(const FwdParams &f, int n)
     {
         const int idx = nth_item(n, f.items);
         if (idx < 0) return false;
-        const AttnTile t = attn_tile(f.tiles, idx / f.p.Hq, kRows, f.p.B, f.p.T);
+        const int per_tile = f.p.Hq / f.heads;
+        const AttnTile t = attn_tile(f.tiles, idx / per_tile, fwd_rows(f.heads), f.p.B, f.p.T);
         if (t.first >= t.seq_end) return false;  // the list's unused end
-        h = idx % f.p.Hq;
+        h = idx % per_tile * f.heads;
         first = t.first; seq_start = t.seq_start; seq_end = t.seq_end;
-        two = first + kTileRows < seq_end;
-        last = (first - seq_start) / kTileRows + two;
+        next_h = f.heads - 1;
+        next_row = f.heads == 1 ? kTileRows : 0;
+        two = first + next_row < seq_end;
+        late = two && next_row;
+        last = (first - seq_start) / kTileRows + late;
         steps = last + 1;
         return true;
     }
     // an absent second tile never begins
-    __device__ __forceinline__ int begin(int w) const { return w ? (two ? 0 : steps + 1) : two; }
+    __device__ __forceinline__ int begin(int w) const { return w ? (two ? 0 : steps + 1) : late; }
 };
 
 template <int D>
@@ -124,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     tc::tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     FwdItem t;
+    if (f.tiles) wait_for_previous();  // the list
 
     if (warp >= 8) {
         tc::fewer_registers<kRegsOther>();
@@ -135,7 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 if (n && !tc::mbar_wait(q_free, (n - 1) & 1, abort, f.status, kErrFree, f.spin)) break;
                 tc::mbar_arrive_expect_tx(q_full, (t.two ? 2 : 1) * S::kTile);
                 for (int w = 0; w <= t.two; ++w)
-                    tc::load_tile<D>(sm + S::kQ + w * S::kTile, &f.q, t.h, t.first + w * kTileRows, q_full);
+                    tc::load_tile<D>(sm + S::kQ + w * S::kTile, &f.q, t.h + w * t.next_h,
+                                     t.first + w * t.next_row, q_full);
                 for (int p = 0; p <= t.steps; ++p, ++g) {
                     const int st = g % S::kStages, use = g / S::kStages;
                     uint8_t *to = sm + S::kRing + st * 2 * S::kTile;
@@ -205,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         bool go = true, odd_rows = false;
         for (int n = 0; go && t.get(f, n); ++n) {
             if (w && !t.two) continue;
-            const int row = t.first + w * kTileRows + in_tile;
+            const int row = t.first + w * t.next_row + in_tile, h = t.h + w * t.next_h;
             float m = -INFINITY, l = 0.f;  // reference (unscaled score) and sum
             const int units = 2 * (t.steps - t.begin(w));  // halves of key tiles, the diagonal's first
             for (int u = 0; u < units; ++u) {
@@ -291,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             tc::tc_fence_after_sync();
             const bool mine = row < t.seq_end;
             const float inv = 1.f / l;
-            __nv_bfloat16 *out = f.o + ((size_t)row * f.p.Hq + t.h) * D;
+            __nv_bfloat16 *out = f.o + ((size_t)row * f.p.Hq + h) * D;
             float odd = 0.f;  // NaN if any value is not finite
 #pragma unroll
             for (int i = 0; i < D; i += 32) {
@@ -313,17 +324,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                             make_uint4(pk[j], pk[j + 1], pk[j + 2], pk[j + 3]);
                 }
             }
-            if (mine && f.lse) f.lse[(size_t)row * f.p.Hq + t.h] = m * f.p.scale + logf(l);
+            if (mine && f.lse) f.lse[(size_t)row * f.p.Hq + h] = m * f.p.scale + logf(l);
             odd_rows |= __any_sync(0xffffffffu, mine && !(odd == 0.f));
             tc::tc_fence_before_sync();
         }
         tc::tc_fence_before_sync();
         __syncwarp();
         for (int n = 0; odd_rows && go && t.get(f, n); ++n) {
-            const int begin = t.first + warp * 32, end = min(begin + 32, t.seq_end);
+            const int h = t.h + w * t.next_h;
+            const int begin = t.first + w * t.next_row + (warp & 3) * 32, end = min(begin + 32, t.seq_end);
             for (int row = begin; row < end; ++row)
-                if (!row_finite<__nv_bfloat16, D>(f.o + ((size_t)row * f.p.Hq + t.h) * D))
-                    recompute_row<D>(f, row, t.seq_start, t.h);
+                if (!row_finite<__nv_bfloat16, D>(f.o + ((size_t)row * f.p.Hq + h) * D))
+                    recompute_row<D>(f, row, t.seq_start, h);
         }
     }
     __syncthreads();
@@ -334,6 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     }
 }
 
+int fwd_heads(const AttnProblem &p) { return p.Hq / p.Hkv % 2 ? 1 : 2; }
+
 template <int D>
 cudaError_t launch(const AttnProblem &p, void *o, float *lse, void *workspace, cudaStream_t st)
 {
@@ -343,7 +357,8 @@ cudaError_t launch(const AttnProblem &p, void *o, float *lse, void *workspace, c
     f.o = static_cast<__nv_bfloat16 *>(o);
     f.lse = lse;
     f.status = reinterpret_cast<int *>(ws);
-    f.items = (int)(attn_tiles(p, kRows) * p.Hq);
+    f.heads = fwd_heads(p);
+    f.items = (int)(attn_tiles(p, fwd_rows(f.heads)) * (p.Hq / f.heads));
     const DebugKnobs dbg = debug_knobs();
     f.spin = dbg.wait_limit ? dbg.wait_limit : tc::kSpinLimit;
     f.starve = dbg.starve_carry;
@@ -353,17 +368,12 @@ cudaError_t launch(const AttnProblem &p, void *o, float *lse, void *workspace, c
         return cudaErrorInvalidValue;
     if (p.cu_seqlens) {
         f.tiles = reinterpret_cast<const AttnTile *>(
-            ws + attn_workspace_layout(p, kRows, false).tiles);
-        const cudaError_t e = launch_attn_plan(p, kRows, workspace, st);
+            ws + attn_workspace_layout(p, fwd_rows(f.heads), false).tiles);
+        const cudaError_t e = launch_attn_plan(p, fwd_rows(f.heads), workspace, st);
         if (e != cudaSuccess) return e;
     }
-    const cudaError_t e = cudaFuncSetAttribute(
-        attn_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdShape<D>::kBytes);
-    if (e != cudaSuccess) return e;
-    attn_fwd_kernel<D><<<(unsigned)(f.items < 148 ? f.items : 148), kThreads, FwdShape<D>::kBytes,
-                         st>>>(f);
-    note_launch();
-    return cudaGetLastError();
+    return launch_kernel(attn_fwd_kernel<D>, f, f.items < 148 ? f.items : 148, kThreads, FwdShape<D>::kBytes,
+                         1, p.cu_seqlens != nullptr, st);
 }
 
 }  // namespace
@@ -382,7 +392,7 @@ bool encode_attn_map(CUtensorMap *tm, const void *base, int H, int D, long long 
            CUDA_SUCCESS;
 }
 
-int attn_tc_fwd_rows() { return kRows; }
+int attn_tc_fwd_rows(const AttnProblem &p) { return fwd_rows(fwd_heads(p)); }
 
 cudaError_t launch_attn_tc_fwd(const AttnProblem &p, void *o, float *lse, void *workspace,
                                cudaStream_t st)

@@ -52,6 +52,7 @@ attn_plan_kernel(const int32_t *__restrict__ cu, int N, int T, int tokens, int r
     __shared__ int s_carry;
     __shared__ int s_len[kRankMax], s_tiles[kRankMax];
     const int tid = threadIdx.x;
+    let_next_start();
     if (tid == 0) *status = 0;
     // sanitised starts
     if (tid == 0) s_carry = 0;
