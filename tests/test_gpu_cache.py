@@ -67,6 +67,12 @@ def test_tables(N, M, P, page, longest):
     assert not refs.any() and not lens.any() and (table == -1).all()
 
 
+def test_tables_of_many_rows():
+    """More rows than one block's threads, and than it keeps the places of on the chip."""
+    test_tables(1500, 5, 9000, 8, 25)
+    test_tables(5000, 4, 17000, 16, 40)
+
+
 def test_reserve_all_or_nothing():
     attn = api()
     refs, table, lens = ints([1, 1, 0, 1]), ints([[0, 3], [1, -1]]), ints([7, 4])
