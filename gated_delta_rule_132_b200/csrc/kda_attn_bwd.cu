@@ -61,7 +61,7 @@ enum : int { kErrStay = 111, kErrA, kErrB, kErrFree, kErrS, kErrDp, kErrP, kErrD
              kErrBwdDrain };
 
 struct Bars {
-    uint64_t *stay, *stay_free, *done, *full0, *free0, *full1, *free1, *s_full, *s_free, *dp_full, *p_full, *ds_full, *acc;
+    uint64_t *stay, *stay_free, *done, *full0, *free0, *full1, *free1, *s_full, *s_free, *dp_full, *ds_full, *acc;
     uint32_t *tmem_slot;
     volatile int *abort;
     volatile uint32_t *odd_rows;  // whether a row is not finite
@@ -72,8 +72,8 @@ struct Bars {
         stay_free = stay + 1; done = stay + 2;
         full0 = stay + 3; free0 = full0 + kMost;
         full1 = free0 + kMost; free1 = full1 + kMost;
-        s_full = free1 + kMost; s_free = s_full + 2; dp_full = s_free + 2; p_full = dp_full + 1;
-        ds_full = p_full + 1; acc = ds_full + 1;
+        s_full = free1 + kMost; s_free = s_full + 2; dp_full = s_free + 2;
+        ds_full = dp_full + 1; acc = ds_full + 1;
         tmem_slot = reinterpret_cast<uint32_t *>(acc + 1);
         abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
         odd_rows = tmem_slot + 2;
@@ -101,7 +101,6 @@ __device__ __forceinline__ uint32_t start_cta(const Bars &b, int full0_count, in
         tc::mbar_init(b.s_free, 8);
         tc::mbar_init(b.s_free + 1, 8);
         tc::mbar_init(b.dp_full, 1);
-        tc::mbar_init(b.p_full, 8);
         tc::mbar_init(b.ds_full, 8);
         tc::mbar_init(b.acc, 1);
         *b.abort = 0;
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     if (warp >= 8) {
         tc::fewer_registers<kRegsOther>();
         if (warp == 9 && !f.starve) {
-            int g = 0, n = 0;  // stages filled, items begun
+            int g0 = 0, g = 0, n = 0;  // stages filled in either ring, items begun
             bool go = true;
             for (; go && t.get(f, n, rank); ++n) {
                 if (n && !__all_sync(0xffffffffu, tc::mbar_wait(b.stay_free, (n - 1) & 1, b.abort, f.status, kErrFree, f.spin)))
@@ -258,11 +257,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
                     tc::load_tile<D>(sm + S::kStay, &f.k, t.hk, t.first, b.stay);
                     tc::load_tile<D>(sm + S::kStay + S::kTile, &f.v, t.hk, t.first, b.stay);
                 }
-                for (int it = 0; it < t.steps; ++it, ++g) {
-                    const int st = g % S::kStages, use = g / S::kStages;
+                auto wait_free = [&](uint64_t *bar, int use) {
+                    return !use || __all_sync(0xffffffffu, tc::mbar_wait(bar, (use - 1) & 1, b.abort, f.status, kErrFree, f.spin));
+                };
+                for (int it = 0; it < t.steps; ++it) {
+                    const int st = g0 % S::kStages, use = g0 / S::kStages;
                     const int h = t.head(f, it, rank), token = t.token(it);
-                    go = !use || tc::wait_both(b.free0 + st, use - 1, b.free1 + st, use - 1, b.abort, f.status, kErrFree, f.spin);
-                    if (!go) break;
+                    if (!(go = wait_free(b.free0 + st, use))) break;
                     float *to = reinterpret_cast<float *>(sm + S::kStats) + st * 256;
                     const size_t base = (size_t)h * f.p.tokens;
 #pragma unroll
@@ -275,23 +276,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
                     if (lane == 0) {
                         tc::mbar_arrive_expect_tx(b.full0 + st, S::kTile);
                         tc::load_tile<D>(sm + S::kRing0 + st * S::kTile, &f.q, h, token, b.full0 + st);
+                    }
+                    __syncwarp();
+                    ++g0;
+                    if (!(go = wait_free(b.free1 + st, use))) break;
+                    if (lane == 0) {
                         tc::mbar_arrive_expect_tx(b.full1 + st, S::kTile);
                         tc::load_tile<D>(sm + S::kRing1 + st * S::kTile, &f.dO, h, token, b.full1 + st);
                     }
                     __syncwarp();
+                    ++g;
                 }
             }
             if (lane == 0) {  // whatever the other warps do, the copies land before the memory is let go
                 if (n) tc::mbar_drain(b.stay, (n - 1) & 1, f.status, kErrBwdDrain);
-                for (int i = max(0, g - S::kStages); i < g; ++i) {
+                for (int i = max(0, g0 - S::kStages); i < g0; ++i)
                     tc::mbar_drain(b.full0 + i % S::kStages, (i / S::kStages) & 1, f.status, kErrBwdDrain);
+                for (int i = max(0, g - S::kStages); i < g; ++i)
                     tc::mbar_drain(b.full1 + i % S::kStages, (i / S::kStages) & 1, f.status, kErrBwdDrain);
-                }
             }
         }
-        // One warp issues: dV and the next S when P is there, dK and the next dP when dS is.
-        // What a product reads in TMEM a later one overwrites, in the order of issue. (A
-        // warp each for S, dV and for dP, dK: 5% slower, as their products hold each other up.)
+        // One warp issues: dK, dV and the next dP when P and dS are there, then S of the step
+        // after. What a product reads in TMEM a later one overwrites, in the order of issue.
         if (warp == 8) {
             const uint32_t lead = lane == 0;
             const uint32_t k = tc::smem_u32(sm + S::kStay), v = k + S::kTile;
@@ -299,42 +305,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
             auto wait = [&](uint64_t *x, int nx, uint64_t *y, int ny, int code) {
                 return tc::wait_both(x, nx, y, ny, b.abort, f.status, code, f.spin);
             };
+            // S of step s, whose place the step before has read
+            auto scores = [&](int s) {
+                uint64_t *full = b.full0 + s % S::kStages;
+                const int use = s / S::kStages;
+                if (!wait(full, use, s ? b.s_free : full, s ? s - 1 : use, kErrA)) return false;
+                tc::tc_fence_after_sync();
+                tc::mma_rows_rows<D>(tmem + kS, k, q + s % S::kStages * S::kTile, lead);
+                tc::commit(b.s_full, lead);
+                return true;
+            };
             int g = 0;  // steps of all items
             bool go = true;
             for (int n = 0; go && t.get(f, n, rank); ++n) {
                 const int end = g + t.steps;
-                const int st0 = g % S::kStages, use0 = g / S::kStages;
-                go = wait(b.stay, n, b.full0 + st0, use0, kErrStay);
+                go = wait(b.stay, n, b.full1 + g % S::kStages, g / S::kStages, kErrStay) && scores(g);
                 if (!go) break;
-                tc::mma_rows_rows<D>(tmem + kS, k, q + st0 * S::kTile, lead);
-                tc::commit(b.s_full, lead);
-                go = wait(b.full1 + st0, use0, b.full1 + st0, use0, kErrB);
-                if (!go) break;
-                tc::mma_rows_rows<D>(tmem + kDp, v, dO + st0 * S::kTile, lead);
+                tc::mma_rows_rows<D>(tmem + kDp, v, dO + g % S::kStages * S::kTile, lead);
                 tc::commit(b.dp_full, lead);
                 if (t.steps == 1) tc::commit(b.stay_free, lead);
-                for (bool first = true; g < end; ++g, first = false) {
+                go = t.steps == 1 || scores(g + 1);
+                for (bool first = true; g < end && go; ++g, first = false) {
                     const int st = g % S::kStages, nst = (g + 1) % S::kStages, use = (g + 1) / S::kStages;
                     const bool more = g + 1 < end;
-                    go = more ? wait(b.p_full, g, b.full0 + nst, use, kErrP) : wait(b.p_full, g, b.p_full, g, kErrP);
-                    if (!go) break;
-                    tc::tc_fence_after_sync();
-                    tc::mma_weights_rows<D, 64>(tmem + kDv, tmem + kS, dO + st * S::kTile, !first, lead);
-                    if (more) {
-                        tc::mma_rows_rows<D>(tmem + kS, k, q + nst * S::kTile, lead);
-                        tc::commit(b.s_full, lead);
-                    }
-                    tc::commit(b.free1 + st, lead);
                     go = more ? wait(b.ds_full, g, b.full1 + nst, use, kErrDs) : wait(b.ds_full, g, b.ds_full, g, kErrDs);
                     if (!go) break;
                     tc::tc_fence_after_sync();
-                    tc::mma_weights_rows<D, 64>(tmem + kDk, tmem + kDp, q + st * S::kTile, !first, lead);
+                    tc::mma_weights_rows<D, 64>(tmem + kDk, tmem + kDp + 32, q + st * S::kTile, !first, lead);
+                    tc::commit(b.free0 + st, lead);
+                    tc::mma_weights_rows<D, 64>(tmem + kDv, tmem + kDp, dO + st * S::kTile, !first, lead);
                     if (more) {
                         tc::mma_rows_rows<D>(tmem + kDp, v, dO + nst * S::kTile, lead);
                         tc::commit(b.dp_full, lead);
                         if (g + 2 == end) tc::commit(b.stay_free, lead);
                     }
-                    tc::commit(b.free0 + st, lead);
+                    tc::commit(b.free1 + st, lead);
+                    if (g + 2 < end) go = scores(g + 2);
                 }
                 if (go) tc::commit(b.acc, lead);
             }
@@ -364,6 +370,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
                 tc::tmem_start(ts + 32, x + 32);
                 tc::tmem_ready(x);
                 tc::tmem_ready(x + 32);
+                tc::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(b.s_free);
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
                     const float4 z = *reinterpret_cast<const float4 *>(lse2 + j);
@@ -379,8 +388,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
 #pragma unroll
                     for (int j = 0; j < 64; ++j) x[j] = j >= before && j < behind ? x[j] : 0.f;
                 }
-                store_weights(ts, x);
-                weights_done(b.p_full);
                 go = __all_sync(0xffffffffu, tc::mbar_wait(b.dp_full, g & 1, b.abort, f.status, kErrDp, f.spin));
                 if (!go) break;
                 tc::tc_fence_after_sync();
@@ -389,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
                 tc::tmem_start(td + 32, y + 32);
                 tc::tmem_ready(y);
                 tc::tmem_ready(y + 32);
+                store_weights(td, x);  // P and dS take the place of the half's dP
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
                     const float4 z = *reinterpret_cast<const float4 *>(del + j);
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
                                          tc::add2(tc::pack2(y[j + 2], y[j + 3]), tc::pack2(-z.z, -z.w))),
                                 x[j + 2], x[j + 3]);
                 }
-                store_weights(td, x);
+                store_weights(td + 32, x);
                 weights_done(b.ds_full);
             }
             go = __all_sync(0xffffffffu, go && tc::mbar_wait(b.acc, n & 1, b.abort, f.status, kErrAcc, f.spin));
