@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     KeyItem t;
     if (f.split > 1 && !t.get(f, 0, rank)) return;  // all of a cluster
 
-    const uint32_t tmem = start_cta(b, 1 + 32, 1);
+    const uint32_t tmem = start_cta(b, 1 + 32, 2);
     constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 256 + D;
     const float *stats = reinterpret_cast<const float *>(sm + S::kStats);
 
@@ -296,52 +296,57 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
                     tc::mbar_drain(b.full1 + i % S::kStages, (i / S::kStages) & 1, f.status, kErrBwdDrain);
             }
         }
-        // One warp issues: dK, dV and the next dP when P and dS are there, then S of the step
-        // after. What a product reads in TMEM a later one overwrites, in the order of issue.
-        if (warp == 8) {
+        // Warp 8 issues dK, dV and the next dP when P and dS are there, warp 10 S as soon as
+        // the step before has read its place. What a product reads in TMEM a later one
+        // overwrites, in the order of issue. (One warp for all: its polls and commits, 1100
+        // cycles of a step, add to the products' 2250.)
+        if (warp == 8 || warp == 10) {
             const uint32_t lead = lane == 0;
             const uint32_t k = tc::smem_u32(sm + S::kStay), v = k + S::kTile;
             const uint32_t q = tc::smem_u32(sm + S::kRing0), dO = tc::smem_u32(sm + S::kRing1);
             auto wait = [&](uint64_t *x, int nx, uint64_t *y, int ny, int code) {
                 return tc::wait_both(x, nx, y, ny, b.abort, f.status, code, f.spin);
             };
-            // S of step s, whose place the step before has read
-            auto scores = [&](int s) {
-                uint64_t *full = b.full0 + s % S::kStages;
-                const int use = s / S::kStages;
-                if (!wait(full, use, s ? b.s_free : full, s ? s - 1 : use, kErrA)) return false;
-                tc::tc_fence_after_sync();
-                tc::mma_rows_rows<D>(tmem + kS, k, q + s % S::kStages * S::kTile, lead);
-                tc::commit(b.s_full, lead);
-                return true;
-            };
             int g = 0;  // steps of all items
             bool go = true;
             for (int n = 0; go && t.get(f, n, rank); ++n) {
-                const int end = g + t.steps;
-                go = wait(b.stay, n, b.full1 + g % S::kStages, g / S::kStages, kErrStay) && scores(g);
-                if (!go) break;
-                tc::mma_rows_rows<D>(tmem + kDp, v, dO + g % S::kStages * S::kTile, lead);
-                tc::commit(b.dp_full, lead);
-                if (t.steps == 1) tc::commit(b.stay_free, lead);
-                go = t.steps == 1 || scores(g + 1);
-                for (bool first = true; g < end && go; ++g, first = false) {
-                    const int st = g % S::kStages, nst = (g + 1) % S::kStages, use = (g + 1) / S::kStages;
-                    const bool more = g + 1 < end;
-                    go = more ? wait(b.ds_full, g, b.full1 + nst, use, kErrDs) : wait(b.ds_full, g, b.ds_full, g, kErrDs);
+                const int begin = g, end = g + t.steps;
+                go = wait(b.stay, n, b.stay, n, kErrStay);
+                if (warp == 10) {
+                    for (; g < end && go; ++g) {
+                        const int st = g % S::kStages, use = g / S::kStages;
+                        go = wait(b.full0 + st, use, g ? b.s_free : b.full0 + st, g ? g - 1 : use, kErrA);
+                        if (!go) break;
+                        tc::tc_fence_after_sync();
+                        tc::mma_rows_rows<D>(tmem + kS, k, q + st * S::kTile, lead);
+                        tc::commit(b.s_full, lead);
+                        tc::commit(b.free0 + st, lead);
+                        if (g + 1 == end) tc::commit(b.stay_free, lead);
+                    }
+                    continue;
+                }
+                for (; g <= end && go; ++g) {  // dK and dV of step g - 1 and dP of step g
+                    const int st = g % S::kStages, use = g / S::kStages, before = (g + S::kStages - 1) % S::kStages;
+                    const bool dp = g < end, sums = g > begin;
+                    // dS says that the step's S was formed, so that its queries are there
+                    go = !sums ? wait(b.full1 + st, use, b.full1 + st, use, kErrB)
+                         : !dp ? wait(b.ds_full, g - 1, b.ds_full, g - 1, kErrDs)
+                               : wait(b.full1 + st, use, b.ds_full, g - 1, kErrDs);
                     if (!go) break;
                     tc::tc_fence_after_sync();
-                    tc::mma_weights_rows<D, 64>(tmem + kDk, tmem + kDp + 32, q + st * S::kTile, !first, lead);
-                    tc::commit(b.free0 + st, lead);
-                    tc::mma_weights_rows<D, 64>(tmem + kDv, tmem + kDp, dO + st * S::kTile, !first, lead);
-                    if (more) {
-                        tc::mma_rows_rows<D>(tmem + kDp, v, dO + nst * S::kTile, lead);
-                        tc::commit(b.dp_full, lead);
-                        if (g + 2 == end) tc::commit(b.stay_free, lead);
+                    if (sums) {
+                        tc::mma_weights_rows<D, 64>(tmem + kDk, tmem + kDp + 32, q + before * S::kTile, g - 1 > begin, lead);
+                        tc::commit(b.free0 + before, lead);
+                        tc::mma_weights_rows<D, 64>(tmem + kDv, tmem + kDp, dO + before * S::kTile, g - 1 > begin, lead);
                     }
-                    tc::commit(b.free1 + st, lead);
-                    if (g + 2 < end) go = scores(g + 2);
+                    if (dp) {
+                        tc::mma_rows_rows<D>(tmem + kDp, v, dO + st * S::kTile, lead);
+                        tc::commit(b.dp_full, lead);
+                        if (g + 1 == end) tc::commit(b.stay_free, lead);
+                    }
+                    if (sums) tc::commit(b.free1 + before, lead);
                 }
+                g = end;  // the next item's first dP comes with no sums
                 if (go) tc::commit(b.acc, lead);
             }
             tc::commit(b.done, lead);
