@@ -9,9 +9,20 @@
 //
 // In both, two products give S and dP in TMEM (transposed in the first kernel: a row
 // is a key); eight warps turn them into P and dS = P (dP - D) in registers, two
-// threads per row with 64 columns each, and write them in bf16 over S and dP, from
-// where the gradient products read them as their TMEM operand. scale is applied to
-// the finished sums.
+// threads per row with 64 columns each, and write them in bf16 over dP, from where the
+// gradient products read them as their TMEM operand; S is free for a later step as soon
+// as it has been read. scale is applied to the finished sums.
+//
+// Roundings: P and dS are operands of bf16 products, each off by at most 2^-8 relative
+// to itself and independently of one another, so a sum over them is off by about as much
+// as its own rounding to bf16 at the end; D comes from the o that is given, itself
+// rounded. Sums, P, dP and D are fp32.
+//
+// Bound: 16384 tokens, 32 query heads over 8 of 128 channels, forward and backward: 9.3 ms,
+// at the power limit. A step of the first kernel takes 3600 cycles, its four products
+// 2250; of the second 2700, its three 1710. The rest is the eight warps' arithmetic (P: some
+// 1000 cycles of issue per warp, two warps to a scheduler), which the products overlap but
+// for the way from dS to the next dP.
 //
 // Rows whose result is not finite are computed again from the visible pairs alone, at the
 // CTA's end, as in the forward (0 times what a masked place holds may be NaN).

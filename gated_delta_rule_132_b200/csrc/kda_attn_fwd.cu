@@ -4,15 +4,25 @@
 // the diagonal down to the sequence's first tile: 128 tokens of two heads of one key/value
 // head where those come in pairs, else 256 tokens of one head, whose first tile sits out
 // a step and whose second is absent from every other sequence's end (24 packed prompts
-// of up to 700 tokens, 16 heads: HEADS_US against TOKENS_US us). One
-// persistent CTA per SM takes items in order of falling work; its loads and products
-// run on into the next item while the rows of the last one are written. (With a CTA per
-// item, beginning and end cost 8 us of an SM, as much as five steps.)
+// of up to 700 tokens, 16 heads: 43 against 47 us). One persistent CTA per SM takes items
+// in order of falling work; its loads and products run on into the next item while the
+// rows of the last one are written. (With a CTA per item, beginning and end cost 8 us of
+// an SM, as much as five steps.)
+//
 // Per tile pair S = Q K^T goes to TMEM, one thread per row turns it into
 // P = 2^(c s - c m) (c = scale log2 e, m the row's running reference) in registers,
 // writes P in bf16 over S, and O += P V reads it from there. Warps 0-3 own the rows of
-// query tile 0, warps 4-7 those of tile 1; warp 8 issues the MMAs, ordered so that one
-// tile's products run while the other tile's rows are in the softmax; warp 9 loads.
+// query tile 0, warps 4-7 those of tile 1; warps 8 and 10 issue the MMAs of a tile each;
+// warp 9 loads. A step goes in halves of 64 keys: the first half's P V and next S run
+// while the second half is in the softmax.
+//
+// Bound: 32768 tokens, 32 query heads over 8 of 128 channels: 8.4 ms, 1.05 PFLOP/s, 0.64 of
+// the measured burst rate and, at the power limit where such a call runs, 0.76 of the
+// sustained one. A step of both tiles takes about 3900 cycles: 64-wide products of S cost
+// as much as 128-wide ones (645 cycles a half, as all of Q is read either way), 3650 in
+// all, and the softmax issues for some 1000 cycles per 64 keys and warp, two warps to a
+// scheduler, half of that in 2^x. One 128-wide product of S costs less but waits for both
+// halves of P: 10.0 ms.
 //
 // The reference m moves only when the row maximum has grown by more than 2^8 in
 // weight: P stays below 2^8, its bf16 relative error and the fp32 sums do not depend
@@ -29,7 +39,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 384;  // two softmax warpgroups; MMA, load and two idle warps
-// 384 threads start with 168 registers; the softmax keeps a row of 128 scores.
+// 384 threads start with 168 registers; the softmax keeps 64 scores and their weights.
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
 constexpr float kRescale = 8.f;  // log2 of the growth that moves the reference

@@ -188,16 +188,15 @@ __device__ __forceinline__ void mma_weights_half(uint32_t acc, uint32_t w, uint3
                lead);
 }
 
-// acc[128 x D] (+)= W Y over the tokens 16 kFrom .. 16 kTo of 128: W [128 x 128] bf16 in
-// TMEM, 32 columns for the first 64 tokens and 32 more that begin kHalf columns on; Y a
-// tile read along its tokens.
-template <int D, int kHalf, int kFrom = 0, int kTo = kTileRows / 16>
+// acc[128 x D] (+)= W Y over 128 tokens: W [128 x 128] bf16 in TMEM, 32 columns for the
+// first 64 tokens and 32 more that begin kHalf columns on; Y a tile read along its tokens.
+template <int D, int kHalf>
 __device__ __forceinline__ void mma_weights_rows(uint32_t acc, uint32_t w, uint32_t y,
                                                  bool accumulate, uint32_t lead)
 {
     const uint64_t b = smem_desc(y, kBlockBytes, 1024);
 #pragma unroll
-    for (int k = kFrom; k < kTo; ++k)
+    for (int k = 0; k < kTileRows / 16; ++k)
         mma_ts(acc, w + (k >> 2) * kHalf + (k & 3) * 8, b + ((k * 2048) >> 4),
                idesc_bf16(128, D, 0, 1), accumulate || k > 0, lead);
 }

@@ -16,7 +16,8 @@
 // than eight tokens), three stages deep; the other warps multiply with mma.sync, whose
 // rate such few rows do not need all of. One warp that loads and knows the table takes
 // a tile's cost from 716 instructions a warp (each thread copying, with a table lookup
-// per key: 4.8 TB/s for one token of 256 sequences) to about 200.
+// per key: 4.8 TB/s for one token of 256 sequences) to about 200: that case takes 694 us,
+// 6.65 TB/s, all of the measured rate.
 // fp32: 32 keys by 16-byte copies, CUDA cores.
 // A key without a page, or behind the sequence, is filled with zeros and masked.
 //
@@ -576,8 +577,8 @@ TreeParams plan(const TreeProblem &p)
     f.tile_keys = many_rows(p) ? 128 : 64;
     // mma.sync: two CTAs to an SM, a chunk's fixed cost is about a tile's: six rounds of
     // them balance the SMs. Many rows: one CTA to an SM, whose beginning and end cost four
-    // tiles or so: three rounds (24 drafts over 16 contexts of 1024..65536: 599 us; chunks
-    // of 2048 keys 731 us).
+    // tiles or so: three rounds (24 drafts over 16 contexts of 1024..65536: 590 us; chunks
+    // of 2048 keys 731 us; chunks chosen so that they fill two to five whole rounds 623 us).
     const long long longest = (long long)p.M << p.page_shift;
     const long long units = (long long)p.N * p.Hkv * f.row_tiles;
     const long long ctas = many_rows(p) ? 148 * 8 : 8192;

@@ -437,7 +437,9 @@ kda_status_t kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  * dtype, from the forward's inputs, its o and its lse:
  *     p_rc = e^(s_rc - lse_r),  D_r = <dO_r, o_r>,  ds_rc = scale p_rc (<dO_r, v_c> - D_r),
  *     grad_q_r = sum_c ds_rc k_c,  grad_k_c = sum_r ds_rc q_r,  grad_v_c = sum_r p_rc dO_r
- * (grad_k and grad_v summed over the group's query heads in fp32 before rounding).
+ * (grad_k and grad_v summed over the group's query heads in fp32 before rounding). D comes
+ * from the o that is given, rounded as it is; in bf16 p and ds are rounded to bf16 for the
+ * products that sum them, which are in fp32.
  *
  * Errors as for kda_chunk_fwd. kda_attn_status reads the status word of the last
  * kda_attn_fwd, kda_attn_bwd or kda_attn_tree on a workspace, as kda_chunk_fwd_status does.
