@@ -18,7 +18,7 @@
 // as its own rounding to bf16 at the end; D comes from the o that is given, itself
 // rounded. Sums, P, dP and D are fp32.
 //
-// Bound: 16384 tokens, 32 query heads over 8 of 128 channels, forward and backward: 9.3 ms,
+// Bound: 16384 tokens, 32 query heads over 8 of 128 channels, forward and backward: 9.4 ms,
 // at the power limit. A step of the first kernel takes 3600 cycles, its four products
 // 2250; of the second 2700, its three 1710. The rest is the eight warps' arithmetic (P: some
 // 1000 cycles of issue per warp, two warps to a scheduler), which the products overlap but
