@@ -81,7 +81,7 @@ cudaError_t launch_attn_delta(const AttnProblem &p, const void *o, const float *
 // group's query heads; the partial sums are added in rank order through distributed
 // shared memory. That pays where the key tiles alone make too few CTAs (below `enough`):
 // one per SM on the tensor cores, whose CTAs take an SM each and some 10 us to begin and to
-// be joined (nine packed documents, 320 CTAs: 125 us, split in two 192 us), four per SM
+// be joined (nine packed documents, 272 CTAs: 110 us, split in two 130 us), four per SM
 // in fp32 (B = 2, T = 777, 8/4 heads of 64, 200 CTAs: 180 us, split in two 122 us).
 inline int attn_head_split(const AttnProblem &p, int rows, int enough)
 {

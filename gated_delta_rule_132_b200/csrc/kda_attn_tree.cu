@@ -507,14 +507,17 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 {
     constexpr int V = D / 32;
     __shared__ float s_acc[8][D], s_l[8];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kWarps;
     const long long unit = (long long)blockIdx.x * (8 / kWarps) + warp / kWarps;
     if (unit >= (long long)f.p.N * f.p.R * f.p.Hq) return;  // whole blocks where kWarps is 8
     const int G = f.p.Hq / f.p.Hkv;
     const int h = (int)(unit % f.p.Hq), i = (int)(unit / f.p.Hq % f.p.R),
               n = (int)(unit / f.p.Hq / f.p.R);
-    const int end = end_of(f.p, n), chunk = chunk_of(f, end);
+    int end;
+    const int chunk = chunk_of(f, n, end);
+    // an absent token's sums mean nothing
+    const bool absent = f.p.parents && ancestors(f.p.parents + (size_t)n * f.p.R, i) == 0;
+    wait_for_previous();
     if (end <= chunk) return;
     const int count = (end + chunk - 1) / chunk;
     const size_t base = ((size_t)n * f.p.Hkv + h / G) * f.chunks * f.rows + i * G + h % G;
@@ -549,22 +552,20 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
             for (int e = 0; e < V; ++e) acc[e] += s_acc[w][lane * V + e];
         }
     }
-    // an absent token's sums mean nothing
-    bool absent = false;
-    if (f.p.parents) absent = ancestors(f.p.parents + (size_t)n * f.p.R, i) == 0;
     finish_row<T, D>(f.p, n, i, h, m, l, absent, acc);
 }
 
 // ---------------------------------------------------------------- host
-// More than 64 rows go to the tensor cores' kernel, where HBM bounds the call again
-// (96 rows over 33,000 cached tokens: 1.21 ms by mma.sync, whose rate bounds it).
-bool many_rows(const TreeProblem &p) { return p.R * (p.Hq / p.Hkv) > 64 && tree_tc_rows(p) > 0; }
+// More than 32 rows go to the tcgen05 kernel (64 rows of 16 sequences of 8000 tokens: 153 us,
+// by mma.sync, whose rate bounds it, 198; 48 rows of 64 of 4000: 247, 380; 64 rows of one of
+// 900: 21.5, 19.5). 32 rows and fewer are as quick either way where there is much to read.
+bool many_rows(const TreeProblem &p) { return p.R * (p.Hq / p.Hkv) > 32 && tree_tc_rows(p) > 0; }
 
 int rows_per_cta(const TreeProblem &p)
 {
     const int rows = p.R * (p.Hq / p.Hkv);
     if (p.dtype == KDA_DTYPE_F32 || rows <= 16) return 16;
-    return rows <= 32 ? 32 : many_rows(p) ? tree_tc_rows(p) : 64;
+    return many_rows(p) ? tree_tc_rows(p) : 32;
 }
 
 TreeParams plan(const TreeProblem &p)
@@ -575,16 +576,25 @@ TreeParams plan(const TreeProblem &p)
     f.tile_rows = rows_per_cta(p);
     f.row_tiles = (f.rows + f.tile_rows - 1) / f.tile_rows;
     f.tile_keys = many_rows(p) ? 128 : 64;
-    // mma.sync: two CTAs to an SM, a chunk's fixed cost is about a tile's: six rounds of
-    // them balance the SMs. Many rows: one CTA to an SM, whose beginning and end cost four
-    // tiles or so: three rounds (24 drafts over 16 contexts of 1024..65536: 590 us; chunks
-    // of 2048 keys 731 us; chunks chosen so that they fill two to five whole rounds 623 us).
+    // mma.sync: two CTAs to an SM, many rows: one. A chunk's beginning and end cost as much as
+    // four tiles or so. So short calls get one CTA to a place, longer ones chunks of 1024
+    // keys until these make six rounds (three) of CTAs, which balance the SMs (in us, against
+    // six rounds for all: one token of 8 sequences of 2000 tokens 34, 42; of 16 of 8168: 112,
+    // 134; 4 of 32 of 1000..2147: 62, 101; 8 of 4 of 16000: 77, 122. 24 drafts over 16
+    // contexts of 1024..65536, three rounds: 590; chunks of 2048 keys 731; chunks that fill
+    // whole rounds 623). A sequence can have as many chunks as make 2048 CTAs of equal ones,
+    // or up to four that make 8192: half of that costs batches of unequal lengths more (64000
+    // tokens and 15 times 1000: 89 and 124) than CTAs without a chunk cost others (8 of 2000:
+    // 34 and 30).
     const long long longest = (long long)p.M << p.page_shift;
     const long long units = (long long)p.N * p.Hkv * f.row_tiles;
-    const long long ctas = many_rows(p) ? 148 * 8 : 8192;
-    f.places = many_rows(p) ? 148 * 3 : 148 * 2 * 6;
-    f.most_keys = many_rows(p) ? 1 << 20 : 2048;
-    f.chunks = (int)std::min({(longest + f.tile_keys - 1) / f.tile_keys, std::max(ctas / units, 1ll), 256ll});
+    const bool many = many_rows(p);
+    const long long most = many ? 148 * 8 / units : std::max(2048 / units, std::min(8192 / units, 4ll));
+    f.share = (float)(p.Hkv * f.row_tiles) / (many ? 148 : 148 * 2);
+    f.per_round = 1.f / (many ? 3 : 6);
+    f.least_keys = 1024;
+    f.most_keys = many ? 1 << 20 : 2048;
+    f.chunks = (int)std::min({(longest + f.tile_keys - 1) / f.tile_keys, std::max(most, 1ll), 256ll});
     return f;
 }
 
@@ -663,8 +673,7 @@ cudaError_t launch(const TreeProblem &p, void *workspace, cudaStream_t st)
             return cudaErrorInvalidValue;
         e = f.tile_rows == 16   ? start_mma<D, 1, 4>(f, ctas, st)
             : f.tile_rows == 32 ? start_mma<D, 2, 2>(f, ctas, st)
-            : many_rows(p)      ? launch_tree_tc(f, ctas, st)
-                                : start_mma<D, 4, 1>(f, ctas, st);
+                                : launch_tree_tc(f, ctas, st);
     }
     if (e != cudaSuccess || f.chunks == 1) return e;
     const long long rows = (long long)p.N * p.R * p.Hq;

@@ -32,8 +32,9 @@ struct TreeParams {
     int row_tiles;  // CTAs that share a chunk's keys
     int tile_keys;  // chunks are multiples of this
     int chunks;     // most chunks of a sequence
-    int places;     // CTAs that a call should have
-    int most_keys;  // of a chunk, where there is a choice
+    float share, per_round;  // (kv heads x row tiles) / places, the CTAs that run at a time; and 1 /
+                             // the rounds of them that a long call should have
+    int least_keys, most_keys;  // of a chunk in more rounds than one, and of any
     float *part_o;  // [n, hk, chunk, row, D]: sums over e^(s - m) v
     float2 *part_ml;
     // bf16: the pools as rows of a head's channels, q as tokens of a kv head's G heads
@@ -64,23 +65,35 @@ __device__ __forceinline__ int end_of(const TreeProblem &p, int n)
     return min(ctx_of(p, n) + p.R, p.M << p.page_shift);
 }
 
-// Keys per chunk of a sequence of `end` keys. Lengths are known on the device only, so
-// every warp adds them up: chunks are to give about f.places CTAs, no smaller than a
-// tile and no larger than f.most_keys.
-__device__ __forceinline__ int chunk_of(const TreeParams &f, int end)
+// Keys per chunk of sequence n, and its length. Lengths are known on the device only, so
+// every warp adds them up: chunks are to give one CTA to every place and not more, and of
+// long calls up to f.rounds to a place, as long as they keep f.least_keys; no smaller than a
+// tile and no larger than f.most_keys. In fp32, whose divisions are quick: most CTAs of a
+// short call find here that they have no chunk.
+__device__ __forceinline__ int chunk_of(const TreeParams &f, int n, int &end)
 {
-    if (f.chunks == 1) return INT32_MAX;
     constexpr int kCounted = 1024;  // sequences whose lengths are added up
-    int target = 2048;
-    if (f.p.N <= kCounted) {
-        long long total = 0;
-        for (int n = threadIdx.x & 31; n < f.p.N; n += 32) total += end_of(f.p, n);
+    int ctx = f.p.ctx_lens[n];
+    const int lane = threadIdx.x & 31, most = f.p.M << f.p.page_shift;
+    float total = 0.f;
+    if (f.chunks > 1 && f.p.N <= kCounted) {
+        for (int i = lane; i < f.p.N; i += 32) total += (float)end_of(f.p, i);
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-        total = total * f.p.Hkv * f.row_tiles / f.places;
-        target = (int)min(max(total, (long long)f.tile_keys), (long long)f.most_keys);
     }
-    const int count = max(1, min(f.chunks, (end + target - 1) / target));
+    ctx = min(max(ctx, 0), most);
+    end = min(ctx + f.p.R, most);
+    if (f.chunks == 1) return INT32_MAX;
+    float target = 2048.f;
+    bool once = false;  // one CTA to a place
+    if (f.p.N <= kCounted) {
+        const float one = total * f.share, least = (float)f.least_keys;
+        once = one <= least;
+        target = fmaxf(one * f.per_round, fminf(one, least));
+        target = fminf(fmaxf(target, (float)f.tile_keys), (float)f.most_keys);
+    }
+    const float parts = __fdividef((float)end, target);
+    const int count = max(1, min(f.chunks, (int)(once ? parts : ceilf(parts))));
     return ((end + count - 1) / count + f.tile_keys - 1) / f.tile_keys * f.tile_keys;
 }
 
@@ -156,8 +169,9 @@ __device__ __forceinline__ bool share_of(const TreeParams &f, Share &s)
     s.hk = x % f.p.Hkv; x /= f.p.Hkv;
     s.n = x % f.p.N;
     s.chunk = x / f.p.N;
+    int end;
+    const int chunk = chunk_of(f, s.n, end);
     s.ctx = ctx_of(f.p, s.n);
-    const int end = end_of(f.p, s.n), chunk = chunk_of(f, end);
     s.alone = end <= chunk;
     if (s.chunk && (s.alone || (long long)s.chunk * chunk >= end)) return false;
     s.first = s.chunk ? s.chunk * chunk : 0;

@@ -1,4 +1,4 @@
-// kda_attn_tree_tc.cu — tree attention of more than 64 rows per key/value head on the
+// kda_attn_tree_tc.cu — tree attention of more than 32 rows per key/value head on the
 // tcgen05 tensor cores (bf16).
 //
 // The prompt forward's pipeline over a chunk of a paged cache: S = Q K^T in TMEM, one
