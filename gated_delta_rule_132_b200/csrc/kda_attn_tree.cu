@@ -16,8 +16,8 @@
 // than eight tokens), three stages deep; the other warps multiply with mma.sync, whose
 // rate such few rows do not need all of. One warp that loads and knows the table takes
 // a tile's cost from 716 instructions a warp (each thread copying, with a table lookup
-// per key: 4.8 TB/s for one token of 256 sequences) to about 200: that case takes 694 us,
-// 6.65 TB/s, all of the measured rate.
+// per key: 4.8 TB/s for one token of 256 sequences) to about 200: that case takes 691 us,
+// 6.69 TB/s, all of the measured rate.
 // fp32: 32 keys by 16-byte copies, CUDA cores.
 // A key without a page, or behind the sequence, is filled with zeros and masked.
 //

@@ -270,3 +270,13 @@ def test_refusals():
         attn.kda_attn_tree(q.repeat(1, 40, 1, 1), kp, vp, table, ctx)
     with pytest.raises(ValueError):
         attn.kda_attn_tree(q, kp, vp, table.cpu(), ctx)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n_draft", [1, 9, 20])
+def test_batches_of_unequal_lengths(n_draft, dtype):
+    """One long sequence among short ones, and more sequences than lengths are added up for."""
+    x = cache(31, [20000] + [40 * n for n in range(40)], n_draft, 64, 4, 2, 64, DT[dtype])
+    check(x, random_parents(32, 41, n_draft))
+    x = cache(33, [(37 * n) % 90 for n in range(1300)], n_draft, 16, 2, 1, 32, DT[dtype], M=300)
+    check(x, None)
