@@ -12,7 +12,7 @@
 // 32 heads over 16 contexts of 1024..65536 tokens, 618,000 in all: 583 us, 4.35 TB/s, 0.66
 // of the measured rate. While all SMs have keys to read the cache's bytes bound it; the
 // difference is chunks that begin (four tiles' time) and end at different times, and the
-// partial sums' join (20 us).
+// partial sums' join (15 us).
 #include "kda_attn_tree.cuh"
 
 namespace kda {
