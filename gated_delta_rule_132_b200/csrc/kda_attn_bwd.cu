@@ -68,7 +68,7 @@ struct BwdShape {
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-enum : int { kErrStay = 111, kErrA, kErrB, kErrFree, kErrS, kErrDp, kErrP, kErrDs, kErrAcc,
+enum : int { kErrStay = 111, kErrA, kErrB, kErrFree, kErrS, kErrDp, kErrDs, kErrAcc,
              kErrBwdDrain };
 
 struct Bars {

@@ -23,7 +23,7 @@ constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
 constexpr float kRescale = 8.f;  // log2 of the growth that moves the reference
 
-enum : int { kErrQ = 131, kErrK, kErrV, kErrFree, kErrS, kErrP, kErrO, kErrDrain };
+enum : int { kErrQ = 131, kErrV, kErrFree, kErrS, kErrP, kErrO, kErrDrain };
 
 template <int D, bool kPair>
 struct TcShape {
