@@ -114,10 +114,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kBars);
     uint64_t *q_full = bars, *q_free = bars + 1, *done = bars + 2;
     uint64_t *kv_full = bars + 3, *kv_free = kv_full + S::kStages;
-    uint64_t *s_full = kv_free + S::kStages;  // [tile][half] scores are in TMEM; once more behind an
-                                              // item's last step: the products of that half are done
+    uint64_t *s_full = kv_free + S::kStages;  // [tile][half] scores are in TMEM
     uint64_t *p_full = s_full + 4;            // [tile][half] probabilities are (one arrival per warp)
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(p_full + 4);
+    // [tile][half] an item's products of that half are done. Not one more phase of s_full: the
+    // next item's first scores follow without an arrival by the softmax, which may then see
+    // neither; the next phase here takes that item's probabilities.
+    uint64_t *o_full = p_full + 4;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_full + 4);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -134,6 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(s_full + i, 1);
             tc::mbar_init(p_full + i, 4);
+            tc::mbar_init(o_full + i, 1);
         }
         *abort = 0;
         tc::fence_mbar_init();
@@ -202,9 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                             tc::mma_weights_half<D>(o_acc, s_acc + h2 * 64, v, h2, it - 1 > begin || h2 > 0, lead);
                         }
                         if (!go || it < begin) continue;
-                        // behind the last step the arrival alone is due: those products are done
                         if (it < steps) tc::mma_rows_half<D>(s_acc + h2 * 64, q, k, h2, lead);
-                        tc::commit(s_full + 2 * w + h2, lead);
+                        tc::commit((it < steps ? s_full : o_full) + 2 * w + h2, lead);
                     }
                     weights += both;
                     if (!go) break;
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const uint32_t ts = tmem + lanes + S::kTmemS + w * 128;
         const uint32_t to = tmem + lanes + S::kTmemO + w * D;
         const float c = f.p.scale * 1.44269504088896340736f;
-        int base = 0;  // phases of s_full before this item (of either half)
+        int base = 0, items = 0;  // phases of s_full and of o_full before this item (of either half)
         bool go = true, odd_rows = false;
         for (int n = 0; go && t.get(f, n); ++n) {
             if (w && !t.two) continue;
@@ -280,9 +283,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         l += sa + sb;
                         break;
                     }
-                    // the next scores' arrival says that the products so far are complete
-                    go = __all_sync(0xffffffffu, tc::mbar_wait(s_full + 2 * w + (half ^ 1), (base + ((u + 1) >> 1)) & 1,
-                                                               abort, f.status, kErrS, f.spin));
+                    // the next arrival says that the products so far are complete
+                    const bool end = u + 1 == units;
+                    go = __all_sync(0xffffffffu, tc::mbar_wait((end ? o_full : s_full) + 2 * w + (half ^ 1),
+                                                               (end ? items : base + ((u + 1) >> 1)) & 1, abort,
+                                                               f.status, kErrS, f.spin));
                     if (!go) break;
                     tc::tc_fence_after_sync();
                     const float m_new = fmaxf(m, top);
@@ -305,9 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(p_full + 2 * w + half);
             }
-            // the arrivals behind the last step: all products are done
-            base += units / 2 + 1;
-            go = go && tc::wait_both(s_full + 2 * w, base - 1, s_full + 2 * w + 1, base - 1, abort, f.status, kErrO, f.spin);
+            base += units / 2;
+            go = go && tc::wait_both(o_full + 2 * w, items, o_full + 2 * w + 1, items, abort, f.status, kErrO, f.spin);
+            ++items;
             if (!go || *abort) break;
             tc::tc_fence_after_sync();
             const bool mine = row < t.seq_end;
