@@ -1,55 +1,14 @@
-// attn_fwd_host.cpp — the prompt forward's source (kda_attn_fwd.cu, copied beside the host's
-// tc_primitives.cuh) with its host side, launched on the emulated device.
-#include "tc_primitives.cuh"
+// attn_fwd_host.cpp — the prompt forward's source on the emulated device.
+#include "attn_host.h"
 
 #include "kda_attn_fwd.cu"
-
-namespace kda {
-namespace {
-alignas(1024) uint8_t smem_raw[256 * 1024];  // the kernel's dynamic shared memory
-}
-
-static CUresult encode(CUtensorMap *tm, CUtensorMapDataType, cuuint32_t, void *base, const cuuint64_t *dims,
-                       const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                       CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill)
-{
-    const tc::Map m{static_cast<const uint16_t *>(base), dims[0], dims[1], dims[2]};
-    std::memcpy(tm, &m, sizeof m);
-    return CUDA_SUCCESS;
-}
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encode; }
-DebugKnobs debug_knobs() { return {0, 0}; }
-void note_launch() {}
-
-// The list as the plan kernel's order allows it: each sequence's last tile first.
-cudaError_t launch_attn_plan(const AttnProblem &p, int rows, void *workspace, cudaStream_t)
-{
-    char *ws = static_cast<char *>(workspace);
-    AttnTile *t = reinterpret_cast<AttnTile *>(ws + attn_workspace_layout(p, rows, false).tiles);
-    const long long most = attn_tiles(p, rows);
-    long long n = 0;
-    *reinterpret_cast<int *>(ws) = 0;
-    for (int s = 0; s < p.N; ++s) {
-        const int a = p.cu_seqlens[s], b = p.cu_seqlens[s + 1];
-        for (int i = (b - a + rows - 1) / rows - 1; i >= 0; --i) t[n++] = AttnTile{a + i * rows, a, b, 0};
-    }
-    for (; n < most; ++n) t[n] = AttnTile{0, 0, 0, 0};
-    return cudaSuccess;
-}
-}  // namespace kda
 
 // Returns the status word, or -1 for an error of the host side.
 extern "C" int attn_fwd_host_run(const void *q, const void *k, const void *v, const int *cu, int N, int B, int T,
                                  int Hq, int Hkv, int d, float scale, void *o, float *lse, void *ws, int ctas,
-                                 unsigned s)
+                                 unsigned seed)
 {
-    emu::ctas = ctas;
-    emu::seed = s;
-    emu::shared_memory = kda::smem_raw;
-    kda::AttnProblem p{};
-    p.q = q; p.k = k; p.v = v; p.cu_seqlens = cu;
-    p.N = N; p.B = B; p.T = T; p.Hq = Hq; p.Hkv = Hkv; p.d = d;
-    p.scale = scale; p.dtype = KDA_DTYPE_BF16; p.tokens = (long long)B * T;
+    const kda::AttnProblem p = problem(q, k, v, cu, N, B, T, Hq, Hkv, d, scale, ctas, seed);
     if (kda::launch_attn_tc_fwd(p, o, lse, ws, nullptr) != cudaSuccess) return -1;
     return *static_cast<int *>(ws);
 }

@@ -43,7 +43,8 @@ struct Cta {
     // meetings of a warp's lanes and of the block's threads
     struct Meeting { int in = 0; unsigned long long round = 0; };
     std::vector<Meeting> warps;
-    Meeting block;
+    Meeting block, parts[16];
+    std::vector<std::vector<std::function<void()>>> own_copies;  // of a thread, until it asks for their arrival
     std::vector<uint32_t> slot;
     std::function<void()> body;
 };
@@ -91,6 +92,7 @@ inline void run(int threads, unsigned x, unsigned blocks, uint32_t seed, std::fu
     c.state.assign(threads, 0);
     c.warps.resize(warps);
     c.slot.assign(threads, 0);
+    c.own_copies.resize(threads);
     c.rank.resize(warps + 2);
     for (int i = 0; i < warps + 2; ++i) c.rank[i] = i;
     for (int t = 0; t < threads; ++t) {
@@ -148,6 +150,10 @@ inline void meet(Cta::Meeting &m, int of)
 inline int lane() { return cta()->cur & 31; }
 inline Cta::Meeting &warp() { return cta()->warps[cta()->cur >> 5]; }
 
+// bar.sync id, n: the first n threads here.
+inline void part_sync(int id, int n) { meet(cta()->parts[id], n); }
+inline void absent() { std::fprintf(stderr, "this instruction is not emulated\n"); std::abort(); }
+
 // What every lane brings, as all of them see it.
 inline std::vector<uint32_t> exchange(uint32_t mine)
 {
@@ -168,7 +174,6 @@ inline std::vector<uint32_t> exchange(uint32_t mine)
 #define threadIdx (emu::Index{(unsigned)emu::cta()->cur})
 #define __noinline__
 #define __launch_bounds__(...)
-asm(".macro griddepcontrol.wait\n.endm\n.macro griddepcontrol.launch_dependents\n.endm");
 
 inline bool __all_sync(unsigned, bool x)
 {
@@ -190,6 +195,7 @@ inline float __shfl_xor_sync(unsigned, float x, int mask)
 }
 inline void __syncwarp() { emu::meet(emu::warp(), 32); }
 inline void __syncthreads() { emu::meet(emu::cta()->block, emu::cta()->threads); }
+template <typename T> inline T __ldg(const T *p) { return *p; }
 inline uint32_t __float_as_uint(float x) { uint32_t u; std::memcpy(&u, &x, 4); return u; }
 using std::max;
 using std::min;
@@ -199,6 +205,15 @@ using std::min;
 namespace emu {
 inline unsigned ctas = 1;
 inline uint32_t seed = 0;
+}
+inline cudaError_t cudaGetLastError() { return cudaSuccess; }
+// kernel<<<...>>>(args): every block of the grid.
+namespace emu {
+template <typename... A, typename... B>
+inline void launch(void (*kernel)(A...), unsigned blocks, int threads, int, cudaStream_t, B... args)
+{
+    for (unsigned x = 0; x < blocks; ++x) run(threads, x, blocks, seed++, [&] { kernel(A(args)...); });
+}
 }
 template <typename F> inline cudaError_t cudaFuncSetAttribute(F *, cudaFuncAttribute, int) { return cudaSuccess; }
 template <typename P>

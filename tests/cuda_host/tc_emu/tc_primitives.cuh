@@ -93,6 +93,19 @@ template <int D> inline void load_tile(uint8_t *dst, const void *map, int head, 
     for (int b = 0; b < (D + 63) / 64; ++b) load_box(dst + b * 16384, map, b * 64, head, token, bar);
 }
 inline void fence_proxy_async_smem() {}
+inline void cp_async4(void *dst, const void *src)
+{
+    emu::cta()->own_copies[emu::cta()->cur].push_back([=] { std::memcpy(dst, src, 4); });
+}
+inline void cp_async_arrive(uint64_t *bar)
+{
+    auto &own = emu::cta()->own_copies[emu::cta()->cur];
+    emu::cta()->copies.push_back([bar, all = std::move(own)] {
+        for (auto &f : all) f();
+        arrived(bar);
+    });
+    own.clear();
+}
 
 // ---------------------------------------------------------------- tensor memory
 inline void tmem_alloc(uint32_t *slot, uint32_t) { *slot = 0; }
@@ -126,6 +139,35 @@ inline float in_tile(uint32_t tile, int r, int c)
     uint16_t v;
     std::memcpy(&v, shared_at(tile + (c >> 6) * 16384 + r * 128 + (c & 63) * 2), 2);
     return bf(v);
+}
+template <int D> inline void mma_rows_rows(uint32_t acc, uint32_t x, uint32_t y, uint32_t lead)
+{
+    if (!lead) return;
+    emu::cta()->products.push_back([=] {
+        for (int r = 0; r < 128; ++r)
+            for (int j = 0; j < 128; ++j) {
+                float s = 0;
+                for (int c = 0; c < D; ++c) s += in_tile(x, r, c) * in_tile(y, j, c);
+                cell(r, acc + j) = s;
+            }
+    });
+}
+template <int D, int kHalf>
+inline void mma_weights_rows(uint32_t acc, uint32_t w, uint32_t y, bool accumulate, uint32_t lead)
+{
+    if (!lead) return;
+    emu::cta()->products.push_back([=] {
+        for (int r = 0; r < 128; ++r)
+            for (int c = 0; c < D; ++c) {
+                float s = accumulate ? cell(r, acc + c) : 0.f;
+                for (int j = 0; j < 128; ++j) {
+                    uint32_t two;
+                    std::memcpy(&two, &cell(r, w + (j >> 6) * kHalf + (j & 63) / 2), 4);
+                    s += bf(j & 1 ? two >> 16 : two & 0xffff) * in_tile(y, j, c);
+                }
+                cell(r, acc + c) = s;
+            }
+    });
 }
 template <int D> inline void mma_rows_half(uint32_t acc, uint32_t x, uint32_t y, int h, uint32_t lead)
 {

@@ -3,38 +3,17 @@ orders drawn from seeds, each as late as it can be after any arrival, copies lan
 and products when the scheduler takes them. Results against the fp64 form, and no wait may run
 out in any order."""
 import ctypes
-import glob
-import os
-import shutil
-import subprocess
 
 import pytest
 import torch
 
 import attn_ref as R
-
-HERE = os.path.dirname(os.path.abspath(__file__))
-ROOT = os.path.dirname(HERE)
-CSRC = os.path.join(ROOT, "gated_delta_rule_132_b200", "csrc")
+import host_kernels
 
 
 @pytest.fixture(scope="module")
 def host(tmp_path_factory):
-    gxx = shutil.which("g++")
-    if gxx is None:
-        pytest.skip("g++ is not available")
-    # beside one another: quoted includes are looked for there first
-    at = tmp_path_factory.mktemp("attn_fwd")
-    for f in glob.glob(os.path.join(HERE, "cuda_host", "tc_emu", "*")) + [
-            os.path.join(HERE, "cuda_host", "attn_fwd_host.cpp")] + [
-            os.path.join(CSRC, n) for n in ("kda_attn_fwd.cu", "kda_attn.cuh", "kda_attn_rows.cuh",
-                                            "kda_attn_tc.cuh", "kda_internal.cuh")]:
-        shutil.copy(f, at)
-    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
-    so = str(at / "attn_fwd_host.so")
-    subprocess.run([gxx, "-O2", "-std=c++17", "-w", "-fPIC", "-shared", "-I", cuda, "-I",
-                    os.path.join(ROOT, "include"), "-o", so, str(at / "attn_fwd_host.cpp")], check=True)
-    return ctypes.CDLL(so)
+    return host_kernels.build(tmp_path_factory.mktemp("attn_fwd"), ("kda_attn_fwd.cu",), "attn_fwd_host.cpp")
 
 
 def inputs(seed, T, Hq, Hkv, d):
