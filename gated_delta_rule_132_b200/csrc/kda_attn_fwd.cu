@@ -13,7 +13,7 @@
 // P = 2^(c s - c m) (c = scale log2 e, m the row's running reference) in registers,
 // writes P in bf16 over S, and O += P V reads it from there. Warps 0-3 own the rows of
 // query tile 0, warps 4-7 those of tile 1; warps 8 and 10 issue the MMAs of a tile each;
-// warp 9 loads. A step goes in halves of 64 keys: the first half's P V and next S run
+// warp 9 loads, warp 11 clears values behind a sequence's end. A step goes in halves of 64 keys: the first half's P V and next S run
 // while the second half is in the softmax.
 //
 // Bound: 32768 tokens, 32 query heads over 8 of 128 channels: 8.4 ms, 1.05 PFLOP/s, 0.64 of
@@ -28,9 +28,11 @@
 // weight: P stays below 2^8, its bf16 relative error and the fp32 sums do not depend
 // on the reference, and O is hardly ever rescaled. Sums use P before its rounding.
 //
-// A masked probability is 0, but 0 times an infinity or NaN in a later token's (or
-// another sequence's) value row is NaN. Rows with a result that is not finite are
-// therefore computed again from the visible keys alone, once the CTA is through with its
+// A masked probability is 0, but 0 times an infinity or NaN in a value row is NaN. Values
+// behind the sequence's end (padding may hold anything, and nobody need have written it) do
+// not get that far: the products leave out whole sixteens of tokens, and of the sixteen with
+// the end warp 11 clears the rest. Rows that a later token of the sequence itself makes not
+// finite are computed again from the visible keys alone, once the CTA is through with its
 // items: until then other warps wait for the ones that would do it.
 #include "kda_attn_rows.cuh"
 #include "kda_attn_tc.cuh"
@@ -38,7 +40,7 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 384;  // two softmax warpgroups; MMA, load and two idle warps
+constexpr int kThreads = 384;  // two softmax warpgroups; MMA, load, MMA, and the values' ends
 // 384 threads start with 168 registers; the softmax keeps 64 scores and their weights.
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
@@ -120,7 +122,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     // next item's first scores follow without an arrival by the softmax, which may then see
     // neither; the next phase here takes that item's probabilities.
     uint64_t *o_full = p_full + 4;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_full + 4);
+    uint64_t *clean = o_full + 4;             // a stage's values are without what lies behind the sequence
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(clean + S::kStages);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -132,7 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         tc::mbar_init(done, 2);
         for (int i = 0; i < S::kStages; ++i) {
             tc::mbar_init(kv_full + i, 1);
-            tc::mbar_init(kv_free + i, 2);
+            tc::mbar_init(kv_free + i, 3);
+            tc::mbar_init(clean + i, 1);
         }
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(s_full + i, 1);
@@ -177,6 +181,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             for (int i = max(0, g - S::kStages); i < g; ++i)
                 tc::mbar_drain(kv_full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
         }
+        // One warp looks after the values that come with a sequence's end. It lets go of every
+        // stage too, so that it is never behind on one that is filled again.
+        if (warp == 11) {
+            int g = 0;
+            bool go = true;
+            for (int n = 0; go && t.get(f, n); ++n) {
+                const int rows = t.seq_end - t.seq_start - t.last * kTileRows;
+                for (int p = 0; p <= t.steps; ++p, ++g) {
+                    const int st = g % S::kStages;
+                    go = __all_sync(0xffffffffu, tc::mbar_wait(kv_full + st, (g / S::kStages) & 1, abort, f.status,
+                                                               kErrKv, f.spin));
+                    if (!go) break;
+                    if (p == 1 && rows < kTileRows) clear_rows<D>(sm + S::kRing + (st * 2 + 1) * S::kTile, rows, (rows + 15) & ~15);
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::mbar_arrive(clean + st);
+                        tc::mbar_arrive(kv_free + st);
+                    }
+                }
+            }
+        }
         // one warp issues for each query tile
         if (warp == 8 || warp == 10) {
             const int w = warp == 10;
@@ -190,20 +216,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             bool go = true;
             for (int n = 0; go && t.get(f, n); ++n) {
                 const int begin = t.begin(w), steps = t.steps;
+                // sixteens of step 0's keys that are the sequence's
+                const int groups = (t.seq_end - t.seq_start - t.last * kTileRows + 15) >> 4;
                 go = wait(q_full, n, kErrQ);
                 for (int it = 0; it <= steps && go; ++it, ++g) {
                     const uint32_t k = ring + g % S::kStages * 2 * S::kTile, v = k + S::kTile;
                     const bool both = it > begin;  // and the first half's probabilities
-                    uint64_t *kv = kv_full + g % S::kStages;
-                    go = tc::wait_both(kv, g / S::kStages, both ? p_full + 2 * w : kv, both ? weights : g / S::kStages,
-                                       abort, f.status, kErrKv, f.spin);
+                    const int st = g % S::kStages, use = g / S::kStages;
+                    uint64_t *kv = kv_full + st;
+                    go = tc::wait_three(kv, use, both ? p_full + 2 * w : kv, both ? weights : use,
+                                        it == 1 ? clean + st : kv, use, abort, f.status, kErrKv, f.spin);
 #pragma unroll
                     for (int h2 = 0; h2 < 2; ++h2) {
                         if (go && both) {  // O += P V of the same half of the step before
                             if (h2) go = wait(p_full + 2 * w + 1, weights, kErrP);
                             if (!go) break;
                             tc::tc_fence_after_sync();
-                            tc::mma_weights_half<D>(o_acc, s_acc + h2 * 64, v, h2, it - 1 > begin || h2 > 0, lead);
+                            tc::mma_weights_half<D>(o_acc, s_acc + h2 * 64, v, h2, it == 1 ? groups - 4 * h2 : 4,
+                                                    it - 1 > begin || h2 > 0, lead);
                         }
                         if (!go || it < begin) continue;
                         if (it < steps) tc::mma_rows_half<D>(s_acc + h2 * 64, q, k, h2, lead);

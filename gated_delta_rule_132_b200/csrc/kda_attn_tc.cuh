@@ -50,6 +50,18 @@ __device__ __forceinline__ int nth_item(int n, int items)
     return at < items ? (int)at : -1;
 }
 
+// Rows [first, end) of a tile become zero, by one warp: what a token behind the sequence holds
+// is not to meet a weight of 0. The tile's copies have landed; the caller's fence
+// (fence_proxy_async_smem) comes before the arrival that lets a product or a later copy have it.
+template <int D> __device__ __forceinline__ void clear_rows(uint8_t *tile, int first, int end)
+{
+    for (int u = first * 8 + (threadIdx.x & 31); u < end * 8; u += 32) {  // 16 bytes in each block
+#pragma unroll
+        for (int b = 0; b < TileShape<D>::kBlocks; ++b)
+            reinterpret_cast<uint4 *>(tile + b * kBlockBytes)[u] = make_uint4(0, 0, 0, 0);
+    }
+}
+
 #ifdef __CUDACC__
 namespace tc {
 
@@ -176,16 +188,17 @@ __device__ __forceinline__ void mma_rows_half(uint32_t acc, uint32_t x, uint32_t
     }
 }
 
-// acc[128 x D] (+)= W Y_h over half h of tile y's tokens: W [128 x 64] bf16 in 32 columns.
+// acc[128 x D] (+)= W Y_h over half h of tile y's tokens, of which the first 16 * groups count:
+// W [128 x 64] bf16 in 32 columns.
 template <int D>
-__device__ __forceinline__ void mma_weights_half(uint32_t acc, uint32_t w, uint32_t y, int h,
+__device__ __forceinline__ void mma_weights_half(uint32_t acc, uint32_t w, uint32_t y, int h, int groups,
                                                  bool accumulate, uint32_t lead)
 {
     const uint64_t b = smem_desc(y + h * 4 * 2048, kBlockBytes, 1024);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         mma_ts(acc, w + k * 8, b + ((k * 2048) >> 4), idesc_bf16(128, D, 0, 1), accumulate || k > 0,
-               lead);
+               k < groups ? lead : 0);
 }
 
 // acc[128 x D] (+)= W Y over 128 tokens: W [128 x 128] bf16 in TMEM, 32 columns for the
@@ -288,11 +301,12 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return r;
 }
 
-// 4-byte asynchronous copy global -> shared, and an arrival on `bar` once this thread's
-// copies so far have landed (the barrier counts it like any arrival).
-__device__ __forceinline__ void cp_async4(void *dst, const void *src)
+// 4-byte asynchronous copy global -> shared, of zero where it is not `real`, and an arrival on
+// `bar` once this thread's copies so far have landed (the barrier counts it like any arrival).
+__device__ __forceinline__ void cp_async4(void *dst, const void *src, bool real)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"(real ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
 {

@@ -71,6 +71,14 @@ inline bool wait_both(uint64_t *a, int na, uint64_t *b, int nb, volatile int *ab
     return __all_sync(~0u, mbar_wait(odd ? b : a, (odd ? nb : na) & 1, abort, err, code));
 }
 
+inline bool wait_three(uint64_t *a, int na, uint64_t *b, int nb, uint64_t *c, int nc, volatile int *abort, int *err,
+                       int code, uint32_t)
+{
+    const int which = emu::lane() % 3;
+    return __all_sync(~0u, mbar_wait(which == 0 ? a : which == 1 ? b : c, (which == 0 ? na : which == 1 ? nb : nc) & 1,
+                                     abort, err, code));
+}
+
 // ---------------------------------------------------------------- copies
 // A tensor map holds {base, channels, heads, tokens} here.
 struct Map { const uint16_t *base; uint64_t d, heads, tokens; };
@@ -93,10 +101,14 @@ template <int D> inline void load_tile(uint8_t *dst, const void *map, int head, 
     for (int b = 0; b < (D + 63) / 64; ++b) load_box(dst + b * 16384, map, b * 64, head, token, bar);
 }
 inline void fence_proxy_async_smem() {}
-inline void cp_async4(void *dst, const void *src)
+inline void cp_async4(void *dst, const void *src, bool real)
 {
-    emu::cta()->own_copies[emu::cta()->cur].push_back([=] { std::memcpy(dst, src, 4); });
+    emu::cta()->own_copies[emu::cta()->cur].push_back([=] {
+        if (real) std::memcpy(dst, src, 4);
+        else std::memset(dst, 0, 4);
+    });
 }
+inline void cp_async_wait_all() {}
 inline void cp_async_arrive(uint64_t *bar)
 {
     auto &own = emu::cta()->own_copies[emu::cta()->cur];
@@ -182,14 +194,14 @@ template <int D> inline void mma_rows_half(uint32_t acc, uint32_t x, uint32_t y,
     });
 }
 template <int D>
-inline void mma_weights_half(uint32_t acc, uint32_t w, uint32_t y, int h, bool accumulate, uint32_t lead)
+inline void mma_weights_half(uint32_t acc, uint32_t w, uint32_t y, int h, int groups, bool accumulate, uint32_t lead)
 {
     if (!lead) return;
     emu::cta()->products.push_back([=] {
         for (int r = 0; r < 128; ++r)
             for (int c = 0; c < D; ++c) {
                 float s = accumulate ? cell(r, acc + c) : 0.f;
-                for (int j = 0; j < 64; ++j) {
+                for (int j = 0; j < 16 * std::min(groups, 4); ++j) {
                     uint32_t two;
                     std::memcpy(&two, &cell(r, w + j / 2), 4);
                     s += bf(j & 1 ? two >> 16 : two & 0xffff) * in_tile(y, h * 64 + j, c);

@@ -55,3 +55,20 @@ def test_any_order(host, lens, packed, H, d, ctas):
             for g, w, t in zip(got, want, tol):
                 R.close(g, w, t)
         assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("d,lens", [(32, [30, 150]), (128, [200]), (64, [70])])
+def test_padding_takes_no_other_way(host, d, lens, bad):
+    """What lies behind the last sequence changes no bit: no row is computed again because of it."""
+    spare = 60
+    x = inputs(3, lens, 1, 1, d, spare)
+    for seed in range(3):
+        want = run(host, x, lens, True, 1, 10 * seed)
+        for what in (range(6), [3, 4], [5], [0, 1, 2]):  # all, o and lse that nobody wrote, dO, q k v
+            y = [t.clone() for t in x]
+            for i in what:
+                y[i][-spare:] = bad
+            got = run(host, y, lens, True, 1, 10 * seed)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all((t[-spare:] == 7.0).all() for t in got)

@@ -77,3 +77,18 @@ def test_moving_reference(host, heads):
         k[a:a + n, 0, 0] = torch.linspace(40, -40, n).bfloat16()
     for seed in range(8):
         check(run(host, (q, k, v), lens, True, 1, 50 * seed), (q, k, v), lens)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("Hq,Hkv,d,lens", [(2, 1, 32, [30, 150]), (1, 1, 128, [300]), (1, 1, 64, [70])])
+def test_padding_takes_no_other_way(host, Hq, Hkv, d, lens, bad):
+    """What lies behind the last sequence changes no bit: no row is computed again because of it."""
+    spare = 60
+    q, k, v = inputs(3, sum(lens) + spare, Hq, Hkv, d)
+    for seed in range(4):
+        want = run(host, (q, k, v), lens, True, 1, 10 * seed, spare)
+        x = [t.clone() for t in (q, k, v)]
+        for t in x:
+            t[-spare:] = bad
+        got = run(host, x, lens, True, 1, 10 * seed, spare)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -27,3 +27,29 @@ def test_many_short_items_follow_one_another(d, Hq, Hkv):
         again = attn.kda_attn_fwd(q, k, v, cu_seqlens=cu, workspace=ws)
         assert attn.kda_attn_status(ws) == (0, 0)
         assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 128), (3, 1, 64), (2, 2, 32)])
+def test_padding_takes_no_other_way(Hq, Hkv, d, bad, dtype):
+    """Tokens behind the last sequence, and what nobody wrote into their o and lse, change no bit
+    of the others' results: no row is computed again because of them. (A row that is computed
+    again rounds no probability to 16 bits, so its bits differ.)"""
+    attn, lens, spare = api(), [257, 1000], 70
+    T = sum(lens) + spare
+    x = inputs(41, T, Hq, Hkv, d, dtype)
+    cu = cu_of(lens)
+
+    def run(q, k, v, dO, fill):
+        o, lse = torch.full_like(q, fill), torch.full((1, T, Hq), fill, device="cuda")
+        attn.kda_attn_fwd(q, k, v, cu_seqlens=cu, o=o, lse=lse)
+        g = attn.kda_attn_bwd(q, k, v, o, lse, dO, cu_seqlens=cu)
+        return [t[:, :-spare] for t in (o, lse, *g.values())]
+
+    want = run(*x, 0.0)
+    for which in ([0, 1, 2, 3], [3], []):
+        y = [t.clone() for t in x]
+        for i in which:
+            y[i][:, -spare:] = bad
+        assert all(torch.equal(a, b) for a, b in zip(run(*y, bad), want))
