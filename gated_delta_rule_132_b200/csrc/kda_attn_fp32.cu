@@ -308,7 +308,10 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ F3
     __shared__ unsigned bad;
     float *q = smem, *g = q + kRows * D, *k = g + kRows * D, *v = k + kWalk * D, *w = v + kWalk * D;
     const AttnTile t = tile_of(f, blockIdx.x / f.p.Hq);
-    if (t.first >= t.seq_end) return;
+    if (t.first >= t.seq_end) {  // where all sequences are empty no other CTA waits
+        wait_for_previous();
+        return;
+    }
     const int h = blockIdx.x % f.p.Hq, hk = h / (f.p.Hq / f.p.Hkv);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     if (threadIdx.x == 0) bad = 0;

@@ -53,3 +53,22 @@ def test_padding_takes_no_other_way(Hq, Hkv, d, bad, dtype):
         for i in which:
             y[i][:, -spare:] = bad
         assert all(torch.equal(a, b) for a, b in zip(run(*y, bad), want))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_sequences_that_are_all_empty(dtype):
+    """Nothing is written, and calls with tokens on the same workspace are as they would be alone."""
+    attn, T = api(), 150
+    q, k, v, dO = inputs(42, T, 4, 2, 64, dtype)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    none, cu = torch.zeros(3, dtype=torch.int32, device="cuda"), cu_of([100, 50])
+    want = attn.kda_attn_fwd(q, k, v, cu_seqlens=cu)
+    grads = attn.kda_attn_bwd(q, k, v, *want, dO, cu_seqlens=cu)
+    o, lse = torch.full_like(q, 7.0), torch.full((1, T, 4), 7.0, device="cuda")
+    for _ in range(20):
+        attn.kda_attn_fwd(q, k, v, cu_seqlens=none, workspace=ws, o=o, lse=lse)
+        attn.kda_attn_bwd(q, k, v, o, lse, dO, cu_seqlens=none, workspace=ws)
+        got = attn.kda_attn_bwd(q, k, v, *want, dO, cu_seqlens=cu, workspace=ws)
+        assert all(torch.equal(got[n], grads[n]) for n in grads)
+    assert attn.kda_attn_status(ws) == (0, 0)
+    assert (o == 7.0).all() and (lse == 7.0).all()
