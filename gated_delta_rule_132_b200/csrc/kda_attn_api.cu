@@ -15,6 +15,9 @@ bool attn_dtype_ok(kda_dtype_t t) { return t == KDA_DTYPE_F32 || t == KDA_DTYPE_
 bool attn_head_ok(int d) { return d == 32 || d == 64 || d == 128; }
 int elem_bytes(kda_dtype_t t) { return t == KDA_DTYPE_F32 ? 4 : 2; }
 
+// Rows, pages, sequences and tiles are walked in 32 bits, up to 8192 at a time.
+constexpr int kMostWalked = INT32_MAX - 16384;
+
 // KDA_DEBUG_SYNC=1: wait for the call and report its status word.
 bool attn_debug_sync()
 {
@@ -41,7 +44,7 @@ kda_status_t sequences_ok(int B, int T, bool varlen, int n_seqs, long long *toke
     if (varlen && (B != 1 || n_seqs < 1)) return KDA_ERR_INVALID_ARG;
     *tokens = (long long)B * T;
     *N = varlen ? n_seqs : B;
-    if (*tokens > (long long)INT32_MAX - 1024) return KDA_ERR_UNSUPPORTED;
+    if (*tokens > (long long)INT32_MAX - 1024 || *N > kMostWalked) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -57,7 +60,7 @@ kda_status_t describe_attn(int B, int T, int Hq, int Hkv, int d, int n_seqs, boo
     // any non-null value: only whether offsets are given matters before the call
     p->cu_seqlens = varlen ? reinterpret_cast<const int32_t *>(16) : nullptr;
     // one CTA per tile and head in a one-dimensional grid, at least 32 tokens a tile
-    if ((kda::attn_tiles(*p, 32) + 1) * Hq > (long long)INT32_MAX ||
+    if ((kda::attn_tiles(*p, 32) + 1) * Hq > (long long)INT32_MAX || kda::attn_tiles(*p, 32) > kMostWalked ||
         p->tokens * Hq / 8 > (long long)INT32_MAX)  // and eight rows to a block at least
         return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
@@ -83,7 +86,8 @@ int log2_page(int page_size)
 kda_status_t table_ok(int N, int M, int P)
 {
     if (N < 1 || M < 1 || P < 1) return KDA_ERR_INVALID_ARG;
-    if ((long long)N * M > (long long)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if ((long long)N * M > (long long)INT32_MAX || N > kMostWalked || P > kMostWalked)
+        return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 

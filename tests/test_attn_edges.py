@@ -1,0 +1,25 @@
+"""Refusals of the full-attention calls at their limits, without a GPU."""
+import pytest
+
+from test_attn_abi import APPEND, FORK, RELEASE, RESERVE, L, at, bwd, call, fwd  # noqa: F401
+
+MOST = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("name,defaults", [("kda_cache_fork", FORK), ("kda_cache_reserve", RESERVE),
+                                           ("kda_cache_release", RELEASE)])
+@pytest.mark.parametrize("P", [MOST, MOST - 8191, MOST - 16383])
+def test_pools_whose_page_numbers_end_at_31_bits(L, name, defaults, P):  # noqa: F811
+    """A walk over the pages steps beyond the last one, which has to have a number."""
+    assert call(L, name, defaults, P=P) == 2
+
+
+@pytest.mark.parametrize("n", [MOST, MOST - 1023, MOST - 16383])
+def test_rows_and_sequences_that_end_at_31_bits(L, n):  # noqa: F811
+    for name, defaults in (("kda_cache_reserve", RESERVE), ("kda_cache_release", RELEASE)):
+        assert call(L, name, defaults, N=n, M=1) == 2
+    assert call(L, "kda_cache_append", APPEND, cu=at(), n=n, B=1, M=1) == 2
+    for prompt in (fwd, bwd):
+        assert prompt(L, cu=at(), n=n, T=64, Hq=1, Hkv=1) == 2
+        assert prompt(L, cu=at(), n=n - 1024, T=1 << 20, Hq=1, Hkv=1) == 2  # its tiles do
+    assert L.kda_cache_reserve_workspace_size(n, 1, 4) == 0
