@@ -347,6 +347,10 @@ kda_status_t kda_cache_compact(void *k_pages, void *v_pages, kda_dtype_t dt,
     if (R > 1024 || Hkv > 65535) return KDA_ERR_UNSUPPORTED;
     st = ints_ok({block_table, ctx_lens, path, new_lens});
     if (st != KDA_OK) return st;
+    // blocks of one row read these while one of them writes its new length
+    if (overlap(new_lens, N, ctx_lens, N) || overlap(new_lens, N, path, (long long)N * R) ||
+        overlap(new_lens, N, block_table, (long long)N * M))
+        return KDA_ERR_INVALID_ARG;
     return from_cuda(kda::launch_cache_compact(pool, block_table, ctx_lens, path, N, R, M,
                                                new_lens, static_cast<cudaStream_t>(stream)));
 }

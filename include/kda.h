@@ -519,7 +519,8 @@ kda_status_t kda_attn_tree(const void *q, const void *k_pages, const void *v_pag
  * kda_cache_compact (data): keeps the drafted tokens path[n, 0], path[n, 1], ... (an
  * increasing list of indices below R, ended by the first entry that is not one) of row
  * n, whose drafts begin at position ctx_lens[n]: moves them together to ctx_lens[n],
- * ctx_lens[n] + 1, ..., and writes ctx_lens[n] plus their number to new_lens[n].
+ * ctx_lens[n] + 1, ..., and writes ctx_lens[n] plus their number to new_lens[n]. new_lens
+ * must not overlap ctx_lens, path or block_table.
  *
  * kda_cache_copy_pages (data): copies page copies[c, 0] to page copies[c, 1] for every
  * c < C (at most 16384). A pair with a number outside [0, P), with a destination that

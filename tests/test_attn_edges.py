@@ -1,7 +1,7 @@
 """Refusals of the full-attention calls at their limits, without a GPU."""
 import pytest
 
-from test_attn_abi import APPEND, FORK, RELEASE, RESERVE, L, at, bwd, call, fwd  # noqa: F401
+from test_attn_abi import APPEND, COMPACT, FORK, RELEASE, RESERVE, L, at, bwd, call, fwd  # noqa: F401
 
 MOST = 2 ** 31 - 1
 
@@ -23,3 +23,11 @@ def test_rows_and_sequences_that_end_at_31_bits(L, n):  # noqa: F811
         assert prompt(L, cu=at(), n=n, T=64, Hq=1, Hkv=1) == 2
         assert prompt(L, cu=at(), n=n - 1024, T=1 << 20, Hq=1, Hkv=1) == 2  # its tiles do
     assert L.kda_cache_reserve_workspace_size(n, 1, 4) == 0
+
+
+@pytest.mark.parametrize("where", [0x10000, 0x20000, 0x20000 + 4 * 3, 0x20000 - 4 * 3, 0x30000 + 4 * 19,
+                                   0x10000 + 4 * 31])
+def test_compact_does_not_write_lengths_that_it_reads(L, where):  # noqa: F811
+    """Rows have several blocks, which all read the old lengths, the path and the table."""
+    kw = dict(table=at(0x10000), ctx=at(0x20000), path=at(0x30000))
+    assert call(L, "kda_cache_compact", COMPACT, new=at(where), **kw) == 1
