@@ -84,6 +84,8 @@ def _stream_of(device, stream):
 def _on(device, stream, body, *args):
     """``body(*args)`` with ``device`` and ``stream`` as the current ones: what a call allocates
     belongs to the stream that its work runs on."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, expected {device}")
     if stream is not None and stream != torch.cuda.current_stream(device):
         with _stream_of(device, stream):
             return body(*args)

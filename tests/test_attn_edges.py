@@ -1,5 +1,8 @@
 """Refusals of the full-attention calls at their limits, without a GPU."""
+import types
+
 import pytest
+import torch
 
 from test_attn_abi import APPEND, COMPACT, FORK, RELEASE, RESERVE, L, at, bwd, call, fwd  # noqa: F401
 
@@ -31,3 +34,11 @@ def test_compact_does_not_write_lengths_that_it_reads(L, where):  # noqa: F811
     """Rows have several blocks, which all read the old lengths, the path and the table."""
     kw = dict(table=at(0x10000), ctx=at(0x20000), path=at(0x30000))
     assert call(L, "kda_cache_compact", COMPACT, new=at(where), **kw) == 1
+
+
+def test_streams_of_another_device_are_refused():
+    """The work would run on the stream's device with pointers into the inputs'."""
+    from gated_delta_rule_132_b200 import attn
+    other = types.SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream is on cuda:1, expected cuda:0"):
+        attn._on(torch.device("cuda", 0), other, lambda: pytest.fail("launched"))
