@@ -124,6 +124,16 @@ def _out(t, name, like, dtype, shape):
     return t
 
 
+def _sequences(cu_seqlens, device):
+    """Checks of packed sequences' offsets: their number, 0 without offsets."""
+    if cu_seqlens is None:
+        return 0
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:  # empty ones have no address to tell them from none
+        raise ValueError(f"cu_seqlens must be [N + 1] with N >= 1, got {tuple(cu_seqlens.shape)}")
+    _check(cu_seqlens, "cu_seqlens", torch.int32, None, device)
+    return cu_seqlens.shape[0] - 1
+
+
 def _prompt(q, k, v, cu_seqlens, scale):
     """Checks of a prompt call: its sizes (B, T, Hq, Hkv, d), sequences, dtype and scale."""
     if q.dim() != 4 or k.dim() != 4:
@@ -134,11 +144,7 @@ def _prompt(q, k, v, cu_seqlens, scale):
     _check(q, "q", q.dtype, None, dev)
     _check(k, "k", q.dtype, (B, T, Hkv, d), dev)
     _check(v, "v", q.dtype, (B, T, Hkv, d), dev)
-    n_seqs = 0
-    if cu_seqlens is not None:
-        _check(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
-        n_seqs = cu_seqlens.shape[0] - 1
-    return (B, T, Hq, Hkv, d), n_seqs, dt, d ** -0.5 if scale is None else float(scale)
+    return (B, T, Hq, Hkv, d), _sequences(cu_seqlens, dev), dt, d ** -0.5 if scale is None else float(scale)
 
 
 def kda_attn_fwd(q, k, v, cu_seqlens=None, scale=None, o=None, lse=None, workspace=None,
@@ -320,10 +326,7 @@ def kda_cache_append(k_pages, v_pages, block_table, start, k_new, v_new, cu_seql
     B, T = k_new.shape[:2]
     _check(k_new, "k_new", k_pages.dtype, (B, T, Hkv, d), dev)
     _check(v_new, "v_new", k_pages.dtype, (B, T, Hkv, d), dev)
-    n_seqs = 0
-    if cu_seqlens is not None:
-        _ints(cu_seqlens, "cu_seqlens", None, dev)
-        n_seqs = cu_seqlens.shape[0] - 1
+    n_seqs = _sequences(cu_seqlens, dev)
     if N != (n_seqs if cu_seqlens is not None else B):
         raise ValueError(f"block_table has {N} rows for {n_seqs or B} sequences")
     _ints(start, "start", (N,), dev)

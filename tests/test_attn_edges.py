@@ -42,3 +42,11 @@ def test_streams_of_another_device_are_refused():
     other = types.SimpleNamespace(device=torch.device("cuda", 1))
     with pytest.raises(ValueError, match="stream is on cuda:1, expected cuda:0"):
         attn._on(torch.device("cuda", 0), other, lambda: pytest.fail("launched"))
+
+
+@pytest.mark.parametrize("shape", [(0,), (1,), (3, 0), (2, 3), ()])
+def test_offsets_of_another_shape_are_refused(shape):
+    """An empty tensor has no address: the call would have taken the tokens as one sequence."""
+    from gated_delta_rule_132_b200 import attn
+    with pytest.raises(ValueError, match="cu_seqlens must be"):
+        attn._sequences(torch.zeros(shape, dtype=torch.int32), torch.device("cuda", 0))

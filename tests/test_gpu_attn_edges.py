@@ -72,3 +72,18 @@ def test_sequences_that_are_all_empty(dtype):
         assert all(torch.equal(got[n], grads[n]) for n in grads)
     assert attn.kda_attn_status(ws) == (0, 0)
     assert (o == 7.0).all() and (lse == 7.0).all()
+
+
+def test_offsets_of_another_shape_are_refused():
+    attn = api()
+    q, k, v, dO = inputs(43, 8, 2, 1, 64, torch.bfloat16)
+    o, lse = attn.kda_attn_fwd(q, k, v)
+    kp = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for shape in ((0,), (1,), (3, 0), (2, 3), ()):
+        cu = torch.zeros(shape, dtype=torch.int32, device="cuda")
+        for call in (lambda: attn.kda_attn_fwd(q, k, v, cu_seqlens=cu),
+                     lambda: attn.kda_attn_bwd(q, k, v, o, lse, dO, cu_seqlens=cu),
+                     lambda: attn.kda_cache_append(kp, kp, one[None], one, k, v, cu_seqlens=cu)):
+            with pytest.raises(ValueError, match="cu_seqlens must be"):
+                call()
