@@ -514,7 +514,8 @@ kda_status_t kda_attn_tree(const void *q, const void *k_pages, const void *v_pag
  * lets go of the pages behind (new_lens = 0 frees the row).
  *
  * kda_cache_append (data): writes k_new and v_new ([B, T, Hkv, d], sequences as for the
- * prefill) into the rows' pages, sequence n from position start[n] on.
+ * prefill, offsets sanitised like the prompt calls') into the rows' pages, sequence n from
+ * position start[n] on.
  *
  * kda_cache_compact (data): keeps the drafted tokens path[n, 0], path[n, 1], ... (an
  * increasing list of indices below R, ended by the first entry that is not one) of row

@@ -87,3 +87,45 @@ def test_offsets_of_another_shape_are_refused():
                      lambda: attn.kda_cache_append(kp, kp, one[None], one, k, v, cu_seqlens=cu)):
             with pytest.raises(ValueError, match="cu_seqlens must be"):
                 call()
+
+
+def sanitised(offsets, T):
+    """(start, length) of every sequence as the prompt calls take malformed offsets."""
+    starts, most = [], 0
+    for x in offsets:
+        most = max(most, min(max(x, 0), T))
+        starts.append(most)
+    return [(a, b - a) for a, b in zip(starts, starts[1:])]
+
+
+@pytest.mark.parametrize("dtype,Hkv,d", [(torch.bfloat16, 2, 128), (torch.float32, 1, 32), (torch.bfloat16, 1, 32)])
+@pytest.mark.parametrize("offsets,T", [
+    ([0, 90, 40, 400], 200), ([-5, 20, 200], 200), ([7, 7, 3, 150, 150], 160), ([300, 400], 200), ([-9, -2], 50),
+    (list(range(0, 3000, 5)) + [10, -1, 2996], 3000),   # more offsets than a block's threads
+    (list(range(2, 1026)), 1100), (list(range(2, 1027)), 1100),  # at the border of many sequences
+    ([0] * 1600 + [64, 0, 1000, 5, 900, 2000], 1500),
+    ([0, 900, 100] * 6000 + [2000, 1900, 2100], 2500),  # several looks
+    ([0, 12345, 12346, 40000], 40000),
+])
+def test_append_takes_offsets_as_the_prompt_does(offsets, T, dtype, Hkv, d):
+    """Falling, negative and too large offsets: each token at the position that the attention of
+    the same prompt gives it."""
+    attn, page, spans = api(), 16, sanitised(offsets, T)
+    N, longest = len(spans), max(n for _, n in spans)
+    start = torch.arange(N, device="cuda", dtype=torch.int32) % 5
+    M = -(-(longest + 5) // page)
+    owners = [n for n, (_, count) in enumerate(spans) if count]
+    table = torch.full((N, M), -1, dtype=torch.int32, device="cuda")
+    for i, n in enumerate(owners):
+        table[n] = torch.arange(i * M, (i + 1) * M, device="cuda")
+    pools = [torch.zeros(max(len(owners), 1) * M, Hkv, page, d, dtype=dtype, device="cuda") for _ in range(2)]
+    new = [torch.randn(1, T, Hkv, d, device="cuda").to(dtype) for _ in range(2)]
+    want = [x.clone() for x in pools]
+    for n in owners:
+        a, count = spans[n]
+        pos = torch.arange(count, device="cuda") + start[n]
+        for w, x in zip(want, new):
+            w[table[n][pos // page].long(), :, pos % page] = x[0, a:a + count]
+    attn.kda_cache_append(*pools, table, start, *new,
+                          cu_seqlens=torch.tensor(offsets, dtype=torch.int32, device="cuda"))
+    assert torch.equal(pools[0], want[0]) and torch.equal(pools[1], want[1])
