@@ -559,12 +559,15 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 // More than 32 rows go to the tcgen05 kernel (64 rows of 16 sequences of 8000 tokens: 153 us,
 // by mma.sync, whose rate bounds it, 198; 48 rows of 64 of 4000: 247, 380; 64 rows of one of
 // 900: 21.5, 19.5). 32 rows and fewer are as quick either way where there is much to read.
-bool many_rows(const TreeProblem &p) { return p.R * (p.Hq / p.Hkv) > 32 && tree_tc_rows(p) > 0; }
+bool many_rows(const TreeProblem &p)
+{
+    return p.dtype == KDA_DTYPE_BF16 && p.R * (p.Hq / p.Hkv) > 32 && tree_tc_rows(p) > 0;
+}
 
 int rows_per_cta(const TreeProblem &p)
 {
     const int rows = p.R * (p.Hq / p.Hkv);
-    if (p.dtype == KDA_DTYPE_F32 || rows <= 16) return 16;
+    if (rows <= 16 || p.dtype == KDA_DTYPE_F32) return 16;
     return many_rows(p) ? tree_tc_rows(p) : 32;
 }
 

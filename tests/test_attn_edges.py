@@ -50,3 +50,12 @@ def test_offsets_of_another_shape_are_refused(shape):
     from gated_delta_rule_132_b200 import attn
     with pytest.raises(ValueError, match="cu_seqlens must be"):
         attn._sequences(torch.zeros(shape, dtype=torch.int32), torch.device("cuda", 0))
+
+
+@pytest.mark.parametrize("dtype,chunks", [(0, 32), (1, 16)])
+def test_tree_calls_are_planned_for_their_kernel(L, dtype, chunks):  # noqa: F811
+    """64 rows per key/value head over 2048 keys: in fp32 chunks of 64 keys at least (two CTAs
+    to an SM), in bf16 of 128."""
+    R, Hq, Hkv, d = 16, 32, 8, 128
+    size = L.kda_attn_tree_workspace_size(1, R, Hq, Hkv, d, 128, 16, dtype)
+    assert size == 256 + R * Hq * chunks * (8 + 4 * d)
