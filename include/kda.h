@@ -505,7 +505,8 @@ kda_status_t kda_attn_tree(const void *q, const void *k_pages, const void *v_pag
  * adds them to lens. Pages are the lowest-numbered free ones, handed out row after
  * row. A last page that is partly filled and held by other rows too is replaced by a
  * new one first; copies[n] = (old page, new page) then, else (-1, -1): pass it to
- * kda_cache_copy_pages for every layer. Of several rows that share such a page and
+ * kda_cache_copy_pages for every layer (of more than 16384 rows in parts: these pairs do not
+ * depend on one another). Of several rows that share such a page and
  * together are all its holders, the last one keeps it. All or nothing: status[0] = 0,
  * or the number of pages that are missing, or -1 - n for the first row n that would
  * need more than M pages; where it is not 0, nothing has changed and copies is all -1.

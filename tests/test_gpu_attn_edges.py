@@ -129,3 +129,48 @@ def test_append_takes_offsets_as_the_prompt_does(offsets, T, dtype, Hkv, d):
     attn.kda_cache_append(*pools, table, start, *new,
                           cu_seqlens=torch.tensor(offsets, dtype=torch.int32, device="cuda"))
     assert torch.equal(pools[0], want[0]) and torch.equal(pools[1], want[1])
+
+
+def test_copies_of_more_rows_than_one_call_takes():
+    """20000 rows that share their last pages in twos: each pair's second holder gets the page, the
+    first a copy, with the pairs handed over in parts."""
+    attn, N, page = api(), 20000, 4
+    i32 = dict(dtype=torch.int32, device="cuda")
+    P = N // 2 * 3
+    refs, lens = torch.zeros(P, **i32), torch.full((N,), 3, **i32)
+    refs[:N // 2] = 2
+    table = torch.full((N, 2), -1, **i32)
+    table[:, 0] = torch.arange(N, device="cuda") // 2
+    kp, vp = (torch.randn(P, 1, page, 32, device="cuda") for _ in range(2))
+    want = [x.clone() for x in (kp, vp)]
+    copies, status = attn.kda_cache_reserve(refs, table, lens, torch.ones(N, **i32), page)
+    assert status.item() == 0 and (lens == 4).all()
+    for part in copies.split(16384):
+        attn.kda_cache_copy_pages(kp, vp, part)
+    made = copies[::2]
+    assert (copies[1::2] == -1).all()
+    assert torch.equal(made[:, 0], torch.arange(N // 2, **i32))
+    assert torch.equal(made[:, 1], torch.arange(N // 2, N, **i32))
+    for w in want:
+        w[N // 2:N] = w[:N // 2]
+    assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+
+
+@pytest.mark.parametrize("C", [1, 100, 129, 300, 9000, 16384])
+def test_copies_in_lists_of_all_lengths(C):
+    """However many slices a page gets: pairs that are left out among pairs that are not."""
+    attn, P = api(), 2 * 16384 + 8
+    kp, vp = (torch.randn(P, 2, 64, 32, device="cuda").bfloat16() for _ in range(2))
+    order = torch.randperm(P, generator=torch.Generator().manual_seed(C))
+    src, dst = order[:C], order[C:2 * C].clone()
+    if C > 2:
+        dst[C - 1] = dst[0]  # an earlier pair's destination
+        dst[1] = src[2]      # another pair's source
+    real = torch.ones(C, dtype=torch.bool)
+    if C > 2:
+        real[[1, C - 1]] = False
+    want = [x.clone() for x in (kp, vp)]
+    for w in want:
+        w[dst[real].cuda()] = w[src[real].cuda()]
+    attn.kda_cache_copy_pages(kp, vp, torch.stack([src, dst], 1).int().cuda().contiguous())
+    assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
