@@ -6,23 +6,28 @@
 
 namespace kda {
 namespace {
+#ifdef FEW_ROWS  // kernels that are compiled and not run
+char smem_raw[1], smem[1];
+#else
 alignas(1024) uint8_t smem_raw[256 * 1024];  // the kernels' dynamic shared memory
+#endif
 }
 
-static CUresult encode(CUtensorMap *tm, CUtensorMapDataType, cuuint32_t, void *base, const cuuint64_t *dims,
-                       const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+static CUresult encode(CUtensorMap *tm, CUtensorMapDataType, cuuint32_t rank, void *base, const cuuint64_t *dims,
+                       const cuuint64_t *, const cuuint32_t *box, const cuuint32_t *, CUtensorMapInterleave,
                        CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill)
 {
-    const tc::Map m{static_cast<const uint16_t *>(base), dims[0], dims[1], dims[2]};
+    tc::Map m{static_cast<const uint16_t *>(base), dims[0], dims[1], rank > 2 ? dims[2] : 0, rank > 3 ? dims[3] : 0};
+    for (cuuint32_t i = 0; i < rank; ++i) m.box[i] = box[i];
     std::memcpy(tm, &m, sizeof m);
     return CUDA_SUCCESS;
 }
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encode; }
-DebugKnobs debug_knobs() { return {0, 0}; }
-void note_launch() {}
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encode; }
+inline DebugKnobs debug_knobs() { return {0, 0}; }
+inline void note_launch() {}
 
 // The list as the plan kernel's order allows it: each sequence's last tile first.
-cudaError_t launch_attn_plan(const AttnProblem &p, int rows, void *workspace, cudaStream_t)
+inline cudaError_t launch_attn_plan(const AttnProblem &p, int rows, void *workspace, cudaStream_t)
 {
     char *ws = static_cast<char *>(workspace);
     AttnTile *t = reinterpret_cast<AttnTile *>(ws + attn_workspace_layout(p, rows, false).tiles);
@@ -43,7 +48,7 @@ static kda::AttnProblem problem(const void *q, const void *k, const void *v, con
 {
     emu::ctas = ctas;
     emu::seed = seed;
-    emu::shared_memory = kda::smem_raw;
+    emu::shared_memory = reinterpret_cast<uint8_t *>(kda::smem_raw);
     kda::AttnProblem p{};
     p.q = q; p.k = k; p.v = v; p.cu_seqlens = cu;
     p.N = N; p.B = B; p.T = T; p.Hq = Hq; p.Hkv = Hkv; p.d = d;

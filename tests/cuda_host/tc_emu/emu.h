@@ -193,6 +193,24 @@ inline float __shfl_xor_sync(unsigned, float x, int mask)
     std::memcpy(&x, &u, 4);
     return x;
 }
+inline float __shfl_sync(unsigned, float x, int from)
+{
+    uint32_t u;
+    std::memcpy(&u, &x, 4);
+    u = emu::exchange(u)[from & 31];
+    std::memcpy(&x, &u, 4);
+    return x;
+}
+inline int __shfl_sync(unsigned, int x, int from) { return (int)emu::exchange((uint32_t)x)[from & 31]; }
+inline unsigned __ballot_sync(unsigned, bool x)
+{
+    unsigned bits = 0, i = 0;
+    for (uint32_t y : emu::exchange(x)) bits |= (y != 0) << i++;
+    return bits;
+}
+inline int __ffs(unsigned x) { return __builtin_ffs((int)x); }
+inline float __fdividef(float a, float b) { return a / b; }
+template <typename T> inline T atomicOr(T *p, T x) { const T old = *p; *p = old | x; return old; }
 inline void __syncwarp() { emu::meet(emu::warp(), 32); }
 inline void __syncthreads() { emu::meet(emu::cta()->block, emu::cta()->threads); }
 template <typename T> inline T __ldg(const T *p) { return *p; }
@@ -200,8 +218,8 @@ inline uint32_t __float_as_uint(float x) { uint32_t u; std::memcpy(&u, &x, 4); r
 using std::max;
 using std::min;
 
-// A launch: emu::ctas CTAs one after another, whatever was asked for (the kernels are
-// persistent), each with the next seed.
+// A launch: its CTAs one after another, each with the next seed; of persistent kernels
+// emu::ctas of them (0: as many as were asked for).
 namespace emu {
 inline unsigned ctas = 1;
 inline uint32_t seed = 0;
@@ -219,7 +237,8 @@ template <typename F> inline cudaError_t cudaFuncSetAttribute(F *, cudaFuncAttri
 template <typename P>
 inline cudaError_t cudaLaunchKernelEx(const cudaLaunchConfig_t *cfg, void (*kernel)(P), const P &params)
 {
-    for (unsigned x = 0; x < emu::ctas; ++x)
-        emu::run((int)cfg->blockDim.x, x, emu::ctas, emu::seed++, [&] { kernel(params); });
+    const unsigned ctas = emu::ctas ? emu::ctas : cfg->gridDim.x;
+    for (unsigned x = 0; x < ctas; ++x)
+        emu::run((int)cfg->blockDim.x, x, ctas, emu::seed++, [&] { kernel(params); });
     return cudaSuccess;
 }

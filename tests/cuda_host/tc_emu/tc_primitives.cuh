@@ -80,8 +80,8 @@ inline bool wait_three(uint64_t *a, int na, uint64_t *b, int nb, uint64_t *c, in
 }
 
 // ---------------------------------------------------------------- copies
-// A tensor map holds {base, channels, heads, tokens} here.
-struct Map { const uint16_t *base; uint64_t d, heads, tokens; };
+// A tensor map holds its base, its dimensions and its box here.
+struct Map { const uint16_t *base; uint64_t d, heads, tokens, last; uint32_t box[4]; };
 inline void load_box(uint8_t *dst, const void *map, int x, int head, int token, uint64_t *bar)
 {
     Map m;
@@ -100,6 +100,38 @@ template <int D> inline void load_tile(uint8_t *dst, const void *map, int head, 
 {
     for (int b = 0; b < (D + 63) / 64; ++b) load_box(dst + b * 16384, map, b * 64, head, token, bar);
 }
+// A map of rows of a head's channels, and one of queries {channel, head of a group, kv head, token}.
+inline void tma_load_2d(void *dst, const void *map, int x, int row, uint64_t *bar)
+{
+    Map m;
+    std::memcpy(&m, map, sizeof m);
+    emu::cta()->copies.push_back([=] {
+        for (uint64_t r = 0; r < m.box[1]; ++r)
+            for (int c = 0; c < 64; ++c) {
+                const bool in = x + c < (int)m.d && row + r < m.heads;
+                const uint16_t v = in ? m.base[(row + r) * m.d + x + c] : 0;
+                std::memcpy(static_cast<uint8_t *>(dst) + r * 128 + c * 2, &v, 2);
+            }
+        landed(bar, (int)m.box[1] * 128);
+    });
+}
+inline void tma_load_4d(void *dst, const void *map, int x, int y, int z, int w, uint64_t *bar)
+{
+    Map m;
+    std::memcpy(&m, map, sizeof m);
+    emu::cta()->copies.push_back([=] {
+        for (uint64_t t = 0; t < m.box[3]; ++t)
+            for (uint64_t g = 0; g < m.box[1]; ++g)
+                for (int c = 0; c < 64; ++c) {
+                    const bool in = x + c < (int)m.d && w + t < m.last;
+                    const uint16_t v =
+                        in ? m.base[(((w + t) * m.tokens + z) * m.heads + y + g) * m.d + x + c] : 0;
+                    std::memcpy(static_cast<uint8_t *>(dst) + (t * m.box[1] + g) * 128 + c * 2, &v, 2);
+                }
+        landed(bar, (int)(m.box[1] * m.box[3]) * 128);
+    });
+}
+inline uint32_t sw128(int row, int byte) { return row * 128 + byte; }
 inline void fence_proxy_async_smem() {}
 inline void cp_async4(void *dst, const void *src, bool real)
 {
@@ -108,7 +140,20 @@ inline void cp_async4(void *dst, const void *src, bool real)
         else std::memset(dst, 0, 4);
     });
 }
-inline void cp_async_wait_all() {}
+inline void copy16(uint32_t dst, const void *src, int bytes)
+{
+    emu::cta()->own_copies[emu::cta()->cur].push_back([=] {
+        std::memset(shared_at(dst), 0, 16);
+        std::memcpy(shared_at(dst), src, bytes);
+    });
+}
+inline void cp_async_wait_all()
+{
+    auto own = std::move(emu::cta()->own_copies[emu::cta()->cur]);
+    emu::cta()->own_copies[emu::cta()->cur].clear();
+    emu::pause(0);
+    for (auto &f : own) f();
+}
 inline void cp_async_arrive(uint64_t *bar)
 {
     auto &own = emu::cta()->own_copies[emu::cta()->cur];
