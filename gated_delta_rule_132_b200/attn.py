@@ -171,7 +171,8 @@ def _fwd(q, k, v, cu_seqlens, sizes, n, dt, scale, o, lse, workspace):
 
 def kda_attn_bwd(q, k, v, o, lse, dO, cu_seqlens=None, scale=None, workspace=None, stream=None):
     """Gradients of <dO, o> of :func:`kda_attn_fwd` (C: ``kda_attn_bwd``), from its inputs
-    and its two results. Returns a dict dq, dk, dv in q's dtype."""
+    and its two results. Returns a dict dq, dk, dv in q's dtype; tokens outside every
+    sequence are not written."""
     sizes, n, dt, scale = _prompt(q, k, v, cu_seqlens, scale)
     dev = q.device
     _check(o, "o", q.dtype, q.shape, dev)

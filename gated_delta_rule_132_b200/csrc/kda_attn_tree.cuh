@@ -66,8 +66,9 @@ __device__ __forceinline__ int end_of(const TreeProblem &p, int n)
 }
 
 // Keys per chunk of sequence n, and its length. Lengths are known on the device only, so
-// every warp adds them up: chunks are to give one CTA to every place and not more, and of
-// long calls up to f.rounds to a place, as long as they keep f.least_keys; no smaller than a
+// every warp adds them up (so a sequence's split, and with it its rounding, depends on the
+// others of its batch): chunks are to give one CTA to every place and not more, and of long
+// calls up to 1 / f.per_round to a place, as long as they keep f.least_keys; no smaller than a
 // tile and no larger than f.most_keys. In fp32, whose divisions are quick: most CTAs of a
 // short call find here that they have no chunk.
 __device__ __forceinline__ int chunk_of(const TreeParams &f, int n, int &end)

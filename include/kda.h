@@ -424,7 +424,9 @@ kda_status_t kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  * device in the same way. `scale` must be positive and finite. Sums, softmax
  * statistics and accumulators are fp32; with bf16 inputs the probabilities (and
  * in the backward the score gradients) are rounded to bf16 as operands of the
- * tensor-core products. Results do not depend on the order of execution.
+ * tensor-core products. Results do not depend on the order of execution: the same call gives
+ * the same bits. How sums are split (dK and dV over a group's heads, a tree's over its keys)
+ * goes by the sizes of the whole call, so a sequence may be rounded differently next to others.
  *
  * kda_attn_fwd: causal attention of every sequence,
  *     s_rc = scale <q_r, k_c> (c <= r),  lse_r = log sum_c e^(s_rc),
@@ -439,7 +441,8 @@ kda_status_t kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  *     grad_q_r = sum_c ds_rc k_c,  grad_k_c = sum_r ds_rc q_r,  grad_v_c = sum_r p_rc dO_r
  * (grad_k and grad_v summed over the group's query heads in fp32 before rounding). D comes
  * from the o that is given, rounded as it is; in bf16 p and ds are rounded to bf16 for the
- * products that sum them, which are in fp32.
+ * products that sum them, which are in fp32. Gradients of tokens outside every sequence are not
+ * written; what q, k, v, o, lse and dO hold there does not matter.
  *
  * Errors as for kda_chunk_fwd. kda_attn_status reads the status word of the last
  * kda_attn_fwd, kda_attn_bwd or kda_attn_tree on a workspace, as kda_chunk_fwd_status does.

@@ -4,6 +4,7 @@ import torch
 
 import attn_ref as R
 from test_gpu_attn import api, cu_of, inputs, spans_of
+from test_gpu_attn_tree import cache, random_parents
 
 pytestmark = pytest.mark.gpu
 
@@ -174,3 +175,50 @@ def test_copies_in_lists_of_all_lengths(C):
         w[dst[real].cuda()] = w[src[real].cuda()]
     attn.kda_cache_copy_pages(kp, vp, torch.stack([src, dst], 1).int().cuda().contiguous())
     assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+
+
+# Relative L2 error of a whole result. In bf16 each term of a sum has one rounded factor and the
+# sum is rounded once: relative errors of at most u = 2^-8, evenly spread over +-u of a value in
+# [1, 2) at worst, so u / sqrt(3) in the mean square, and independent of one another. Terms whose
+# signs are independent keep that share in their sum. Two such roundings: u sqrt(2 / 3) = 0.0032;
+# the bound leaves a quarter for chance and fp32. In fp32 a score's bound (2 d e sum |q k| scale,
+# some 2e-5 here) leads. A group of 16 keys left out of 1500 would show as 0.1.
+L2 = {torch.bfloat16: 0.004, torch.float32: 2e-5}
+
+
+def l2(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens,packed", [([1500], False), ([700, 13, 260, 1100], True)])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 128), (3, 1, 64), (2, 2, 32)])
+def test_whole_results(Hq, Hkv, d, lens, packed, dtype):
+    attn, spans = api(), spans_of(lens)
+    q, k, v, dO = inputs(44, sum(lens), Hq, Hkv, d, dtype)
+    cu = cu_of(lens) if packed else None
+    o, lse = attn.kda_attn_fwd(q, k, v, cu_seqlens=cu)
+    want = R.attn_fwd(q[0], k[0], v[0], spans, d ** -0.5)
+    assert l2(o[0], want[0]) <= L2[dtype]
+    g = attn.kda_attn_bwd(q, k, v, o, lse, dO, cu_seqlens=cu)
+    grads, _ = R.attn_bwd(q[0], k[0], v[0], o[0], lse[0], dO[0], spans, d ** -0.5)
+    for name, w in zip(("dq", "dk", "dv"), grads):
+        assert l2(g[name][0], w) <= L2[dtype], name
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n_draft", [1, 4, 8, 24, 50])
+def test_whole_tree_results_and_the_batch(n_draft, dtype):
+    """A whole call, and each of its sequences alone: the split of the keys goes by the batch, so
+    bits may differ, but all are within the bounds."""
+    q, kp, vp, table, ctx = cache(45, [3000, 33, 700, 1024], n_draft, 32, 8, 2, 128, dtype)
+    parents = random_parents(46, 4, n_draft)
+    o, lse = api().kda_attn_tree(q, kp, vp, table, ctx, parents=parents)
+    ro, rl, to, tl = R.attn_tree(q, kp, vp, table, ctx, parents, 128 ** -0.5)
+    assert l2(o, ro) <= L2[dtype]
+    for n in range(4):
+        part = slice(n, n + 1)
+        alone = api().kda_attn_tree(q[part], kp, vp, table[part], ctx[part], parents=parents[part])
+        R.close(alone[0], ro[part], to[part])
+        R.close(alone[1], rl[part], tl[part])
+        assert l2(alone[0], ro[part]) <= L2[dtype] * 1.5  # of one sequence, whose rows are few
