@@ -13,8 +13,8 @@
 // P = 2^(c s - c m) (c = scale log2 e, m the row's running reference) in registers,
 // writes P in bf16 over S, and O += P V reads it from there. Warps 0-3 own the rows of
 // query tile 0, warps 4-7 those of tile 1; warps 8 and 10 issue the MMAs of a tile each;
-// warp 9 loads, warp 11 clears values behind a sequence's end. A step goes in halves of 64 keys: the first half's P V and next S run
-// while the second half is in the softmax.
+// warp 9 loads, warp 11 clears values behind a sequence's end. A step goes in halves of 64
+// keys: the first half's P V and next S run while the second half is in the softmax.
 //
 // Bound: 32768 tokens, 32 query heads over 8 of 128 channels: 8.4 ms, 1.05 PFLOP/s, 0.64 of
 // the measured burst rate and, at the power limit where such a call runs, 0.76 of the
@@ -69,7 +69,7 @@ struct FwdShape {
     static constexpr uint32_t kTmemS = 0, kTmemO = 256;     // columns
 };
 
-enum : int { kErrQ = 101, kErrKv, kErrFree, kErrS, kErrP, kErrO, kErrDrain };
+enum : int { kErrQ = 101, kErrKv, kErrFree, kErrS, kErrP, kErrO, kErrDrain, kErrClean };
 
 template <int D>
 __device__ __noinline__ void recompute_row(const FwdParams &f, int row, int start, int h)
@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     go = __all_sync(0xffffffffu, tc::mbar_wait(kv_full + st, (g / S::kStages) & 1, abort, f.status,
                                                                kErrKv, f.spin));
                     if (!go) break;
-                    if (p == 1 && rows < kTileRows) clear_rows<D>(sm + S::kRing + (st * 2 + 1) * S::kTile, rows, (rows + 15) & ~15);
+                    if (p == 1 && rows < kTileRows)
+                        clear_rows<D>(sm + S::kRing + (st * 2 + 1) * S::kTile, rows, (rows + 15) & ~15);
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -224,8 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     const bool both = it > begin;  // and the first half's probabilities
                     const int st = g % S::kStages, use = g / S::kStages;
                     uint64_t *kv = kv_full + st;
-                    go = tc::wait_three(kv, use, both ? p_full + 2 * w : kv, both ? weights : use,
-                                        it == 1 ? clean + st : kv, use, abort, f.status, kErrKv, f.spin);
+                    go = tc::wait_both(kv, use, both ? p_full + 2 * w : kv, both ? weights : use, abort, f.status,
+                                       kErrKv, f.spin);
+                    // not before the stage is full: until then its last use may not be clean yet
+                    if (both && it == 1 && groups < kTileRows / 16) go = go && wait(clean + st, use, kErrClean);
 #pragma unroll
                     for (int h2 = 0; h2 < 2; ++h2) {
                         if (go && both) {  // O += P V of the same half of the step before

@@ -80,12 +80,13 @@ def test_moving_reference(host, heads):
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-@pytest.mark.parametrize("Hq,Hkv,d,lens", [(2, 1, 32, [30, 150]), (1, 1, 128, [300]), (1, 1, 64, [70])])
+@pytest.mark.parametrize("Hq,Hkv,d,lens", [(2, 1, 32, [30, 150]), (1, 1, 128, [300]), (1, 1, 64, [70]),
+                                           (16, 1, 32, [140]), (6, 3, 128, [140])])  # one such item after another
 def test_padding_takes_no_other_way(host, Hq, Hkv, d, lens, bad):
     """What lies behind the last sequence changes no bit: no row is computed again because of it."""
     spare = 60
     q, k, v = inputs(3, sum(lens) + spare, Hq, Hkv, d)
-    for seed in range(4):
+    for seed in range(8):
         want = run(host, (q, k, v), lens, True, 1, 10 * seed, spare)
         x = [t.clone() for t in (q, k, v)]
         for t in x:
