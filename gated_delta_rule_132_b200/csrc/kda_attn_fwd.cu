@@ -155,7 +155,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 
     if (warp >= 8) {
         tc::fewer_registers<kRegsOther>();
-        if (warp == 9 && lane == 0 && !f.starve) {
+        if (warp == 11) {
+            // The values that come with a sequence's end. It lets go of every stage too, so that
+            // it is never behind on one that is filled again.
+            int g = 0;
+            bool go = true;
+            for (int n = 0; go && t.get(f, n); ++n) {
+                const int rows = t.seq_end - t.seq_start - t.last * kTileRows;
+                for (int p = 0; p <= t.steps; ++p, ++g) {
+                    const int st = g % S::kStages;
+                    go = __all_sync(0xffffffffu, tc::mbar_wait(kv_full + st, (g / S::kStages) & 1, abort, f.status,
+                                                               kErrKv, f.spin));
+                    if (!go) break;
+                    if (p == 1 && rows < kTileRows)
+                        clear_rows<D>(sm + S::kRing + (st * 2 + 1) * S::kTile, rows, (rows + 15) & ~15);
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::mbar_arrive(clean + st);
+                        tc::mbar_arrive(kv_free + st);
+                    }
+                }
+            }
+        } else if (warp == 9 && lane == 0 && !f.starve) {
             int g = 0, n = 0;  // stages filled, items begun
             bool go = true;
             for (; go && t.get(f, n); ++n) {
@@ -180,29 +202,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             if (n) tc::mbar_drain(q_full, (n - 1) & 1, f.status, kErrDrain);
             for (int i = max(0, g - S::kStages); i < g; ++i)
                 tc::mbar_drain(kv_full + i % S::kStages, (i / S::kStages) & 1, f.status, kErrDrain);
-        }
-        // One warp looks after the values that come with a sequence's end. It lets go of every
-        // stage too, so that it is never behind on one that is filled again.
-        if (warp == 11) {
-            int g = 0;
-            bool go = true;
-            for (int n = 0; go && t.get(f, n); ++n) {
-                const int rows = t.seq_end - t.seq_start - t.last * kTileRows;
-                for (int p = 0; p <= t.steps; ++p, ++g) {
-                    const int st = g % S::kStages;
-                    go = __all_sync(0xffffffffu, tc::mbar_wait(kv_full + st, (g / S::kStages) & 1, abort, f.status,
-                                                               kErrKv, f.spin));
-                    if (!go) break;
-                    if (p == 1 && rows < kTileRows)
-                        clear_rows<D>(sm + S::kRing + (st * 2 + 1) * S::kTile, rows, (rows + 15) & ~15);
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tc::mbar_arrive(clean + st);
-                        tc::mbar_arrive(kv_free + st);
-                    }
-                }
-            }
         }
         // one warp issues for each query tile
         if (warp == 8 || warp == 10) {
@@ -239,8 +238,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                                                     it - 1 > begin || h2 > 0, lead);
                         }
                         if (!go || it < begin) continue;
-                        if (it < steps) tc::mma_rows_half<D>(s_acc + h2 * 64, q, k, h2, lead);
-                        tc::commit((it < steps ? s_full : o_full) + 2 * w + h2, lead);
+                        if (it < steps) {
+                            tc::mma_rows_half<D>(s_acc + h2 * 64, q, k, h2, lead);
+                            tc::commit(s_full + 2 * w + h2, lead);
+                        } else {
+                            tc::commit(o_full + 2 * w + h2, lead);
+                        }
                     }
                     weights += both;
                     if (!go) break;

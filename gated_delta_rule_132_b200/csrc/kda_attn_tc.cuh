@@ -55,6 +55,7 @@ __device__ __forceinline__ int nth_item(int n, int items)
 // (fence_proxy_async_smem) comes before the arrival that lets a product or a later copy have it.
 template <int D> __device__ __forceinline__ void clear_rows(uint8_t *tile, int first, int end)
 {
+#pragma unroll 1  // the callers are short of registers
     for (int u = first * 8 + (threadIdx.x & 31); u < end * 8; u += 32) {  // 16 bytes in each block
 #pragma unroll
         for (int b = 0; b < TileShape<D>::kBlocks; ++b)
