@@ -4,10 +4,10 @@
 // the diagonal down to the sequence's first tile: 128 tokens of two heads of one key/value
 // head where those come in pairs, else 256 tokens of one head, whose first tile sits out
 // a step and whose second is absent from every other sequence's end (24 packed prompts
-// of up to 700 tokens, 16 heads: 43 against 47 us). One persistent CTA per SM takes items
-// in order of falling work; its loads and products run on into the next item while the
-// rows of the last one are written. (With a CTA per item, beginning and end cost 8 us of
-// an SM, as much as five steps.)
+// of up to 700 tokens, 16 heads: 44 us, 47 without the pairs). One persistent CTA per SM
+// takes items in order of falling work; its loads and products run on into the next item
+// while the rows of the last one are written. (With a CTA per item, beginning and end cost
+// 8 us of an SM, as much as five steps.)
 //
 // Per tile pair S = Q K^T goes to TMEM, one thread per row turns it into
 // P = 2^(c s - c m) (c = scale log2 e, m the row's running reference) in registers,
@@ -16,8 +16,8 @@
 // warp 9 loads, warp 11 clears values behind a sequence's end. A step goes in halves of 64
 // keys: the first half's P V and next S run while the second half is in the softmax.
 //
-// Bound: 32768 tokens, 32 query heads over 8 of 128 channels: 8.4 ms, 1.05 PFLOP/s, 0.64 of
-// the measured burst rate and, at the power limit where such a call runs, 0.76 of the
+// Bound: 32768 tokens, 32 query heads over 8 of 128 channels: 8.5 ms, 1.03 PFLOP/s, 0.63 of
+// the measured burst rate and, at the power limit where such a call runs, 0.75 of the
 // sustained one. A step of both tiles takes about 3900 cycles: 64-wide products of S cost
 // as much as 128-wide ones (645 cycles a half, as all of Q is read either way), 3650 in
 // all, and the softmax issues for some 1000 cycles per 64 keys and warp, two warps to a

@@ -114,7 +114,9 @@ __device__ __forceinline__ void tma_load_4d(void *dst_smem, const void *tmap, in
 
 // A barrier's phase is told by its parity only: whoever waits on a barrier has to see every
 // phase of it, or be sure that it is at most one ahead. (With rings whose stages alternate
-// between two consumers, the number of stages is even for that.)
+// between two consumers, the number of stages is even for that; an arrival that nobody's next
+// step depends on has a barrier of its own.) Polled beside another barrier it has to be sure of
+// the phase before by itself, not only once the other one is through.
 //
 // Wait for two phases at once, by the whole warp: every other lane polls the other
 // barrier, since a poll costs some 150 cycles even of a phase that is complete.
